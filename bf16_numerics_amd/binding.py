@@ -39,9 +39,18 @@ EXPORTS = ("shard_range", "bfo_table_create", "bfo_table_create_layout", "bfo_ta
            "bfo_checkpoint_save", "bfo_checkpoint_done", "bfo_checkpoint_latest", "bfo_checkpoint_load",
            "bfo_stream_mix", "bfo_plan_runs", "bfo_step_scalars_fill", "adamw_sr_step_scheduled",
            "bfo_cursor_advance", "bfo_spread_layout", "bfo_norm_workspace_bytes", "grad_global_norm_noalloc", "master_to_bf16",
-           "bfo_checksum64", "adamw_sr_step_with_norm")
+           "bfo_checksum64", "adamw_sr_step_with_norm",
+           "layernorm_forward", "bfo_layernorm_workspace_bytes", "layernorm_backward",
+           "bfo_logits_workspace_bytes", "token_logprobs_forward", "token_logprobs_backward",
+           "distill_forward", "distill_backward")
 
 LR_CONSTANT, LR_LINEAR, LR_COSINE, LR_WSD = 0, 1, 2, 3
+
+BF16, F32 = 0, 1
+ACCUMULATE_DX, ACCUMULATE_PARAMS = 1, 2
+LAYERNORM_MAX_COLS = 16384
+TOP_MAX = 128
+VOCAB_MAX = 1 << 28
 
 
 class BfoTensor(ctypes.Structure):
@@ -95,7 +104,7 @@ def _lib():
         raise ImportError(f"{_LIB_PATH} is missing: build it first (python -m bf16_numerics_amd.build "
                           "or __graft_entry__.build())")
     lib = ctypes.CDLL(_LIB_PATH)
-    u64, u32, vp, i32 = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_int
+    u64, u32, vp, i32, f32 = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
     pu64 = ctypes.POINTER(ctypes.c_uint64)
     sig = {
         "shard_range": (i32, [u64, u32, u32, pu64, pu64]),
@@ -133,6 +142,14 @@ def _lib():
                                           vp, i32, vp]),
         "bfo_cursor_advance": (i32, [vp, vp]),
         "bfo_spread_layout": (i32, [pu64, u32, pu64, pu64]),
+        "layernorm_forward": (i32, [vp, u64, vp, vp, vp, u64, vp, vp, u64, u32, f32, i32, i32, vp]),
+        "bfo_layernorm_workspace_bytes": (i32, [u64, u32, pu64]),
+        "layernorm_backward": (i32, [vp, u64, vp, u64, vp, vp, vp, vp, u64, vp, vp, u64, u32, i32, i32, i32, vp, vp]),
+        "bfo_logits_workspace_bytes": (i32, [u64, u32, u32, pu64]),
+        "token_logprobs_forward": (i32, [vp, u64, u64, u32, i32, f32, vp, vp, vp, vp, u32, vp, vp, vp, vp]),
+        "token_logprobs_backward": (i32, [vp, u64, u64, u32, u32, i32, f32, vp, vp, vp, vp, vp, vp, u64, vp]),
+        "distill_forward": (i32, [vp, u64, u64, u32, i32, f32, vp, vp, u32, vp, vp, vp, vp, vp, vp]),
+        "distill_backward": (i32, [vp, u64, u64, u32, u32, i32, f32, vp, vp, u32, vp, vp, vp, vp, vp, u64, vp]),
         "bfo_status_string": (ctypes.c_char_p, [i32]),
         "bfo_last_hip_error": (i32, []),
     }
@@ -619,3 +636,229 @@ def checkpoint_load(directory, step, table, m, v, master=None, params=None):
         _check("bfo_checkpoint_load", _lib().bfo_checkpoint_load(os.fsencode(directory), step, table.handle, p, M,
                                                                mm, vv, ctypes.byref(seed), _stream(dev)))
     return seed.value
+
+
+# --------------------------------------------------------------------------
+# Operators of the training loop around the step (layer norm, token log
+# probabilities, distillation).  Matrices are 2-D tensors with unit column
+# stride (any row stride); the other arrays are contiguous.
+# --------------------------------------------------------------------------
+
+_DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _matrix(t, name, like=None):
+    """(device pointer, row stride, rows, columns) of a bf16 or fp32 matrix;
+    `like`: a matrix whose dtype, device and shape it must have."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPE_CODES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {t.dim()} dimensions")
+    rows, cols = t.shape
+    stride, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+        if t.shape != like.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    elif t.device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}, expected a GPU")
+    return t.data_ptr(), stride if rows > 1 else cols, rows, cols
+
+
+def _vector(t, dtype, count, name, dev):
+    """Device pointer of a contiguous tensor of `count` elements, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() != count:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {count}")
+    return t.data_ptr()
+
+
+def _param(t, cols, name, like, dev):
+    if t is None:
+        return None
+    if t.dtype not in _DTYPE_CODES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return _vector(t, like, cols, name, dev)
+
+
+def _workspace_ptr(workspace, need, dev, maker):
+    if workspace is None:
+        if need:
+            raise ValueError(f"workspace must be {maker}(...)")
+        return None
+    if workspace.device != dev or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must be {maker}(...) for these sizes")
+    return workspace.data_ptr()
+
+
+def _launch(name, dev, *args):
+    """Call entry point `name` with `dev` current, on dev's current stream."""
+    fn = getattr(_lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != OK:
+        raise BfoError(name, rc)
+
+
+def layernorm_workspace_bytes(rows, cols):
+    """Device bytes layernorm_backward needs as workspace."""
+    out = ctypes.c_uint64(0)
+    _check("bfo_layernorm_workspace_bytes", _lib().bfo_layernorm_workspace_bytes(rows, cols, ctypes.byref(out)))
+    return out.value
+
+
+def new_layernorm_workspace(rows, cols, device):
+    """A device buffer for layernorm_backward of rows x cols matrices (at least 16 bytes)."""
+    return torch.empty(max(16, layernorm_workspace_bytes(rows, cols)), dtype=torch.uint8, device=device)
+
+
+def layernorm_forward(x, weight, bias, out, mean=None, rstd=None, eps=1e-5):
+    """out = (x - mean) * rstd * weight + bias per row of x (bias may be None).
+    mean, rstd: float32 tensors of x's rows for the backward pass, or None."""
+    dev = x.device
+    xp, xs, rows, cols = _matrix(x, "x")
+    op, os_, _, _ = _matrix(out, "out", x)
+    w = _param(weight, cols, "weight", weight.dtype, dev)
+    b = _param(bias, cols, "bias", weight.dtype, dev)
+    _launch("layernorm_forward", dev, xp, xs, w, b, op, os_, _vector(mean, torch.float32, rows, "mean", dev),
+            _vector(rstd, torch.float32, rows, "rstd", dev), rows, cols, eps, _DTYPE_CODES[x.dtype],
+            _DTYPE_CODES[weight.dtype])
+
+
+def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, workspace=None, accumulate_dx=False,
+                       accumulate_params=False):
+    """Gradients of layernorm_forward into dx, dweight and dbias (None: not
+    wanted).  accumulate_*: add to what they hold.  workspace:
+    new_layernorm_workspace(rows, cols, device)."""
+    dev = x.device
+    xp, xs, rows, cols = _matrix(x, "x")
+    gp, gs, _, _ = _matrix(dout, "dout", x)
+    dp, ds, _, _ = _matrix(dx, "dx", x)
+    w = _param(weight, cols, "weight", weight.dtype, dev)
+    dw = _vector(dweight, weight.dtype, cols, "dweight", dev)
+    db = _vector(dbias, weight.dtype, cols, "dbias", dev)
+    ws = _workspace_ptr(workspace, layernorm_workspace_bytes(rows, cols), dev, "new_layernorm_workspace")
+    _launch("layernorm_backward", dev, gp, gs, xp, xs, w, _vector(mean, torch.float32, rows, "mean", dev),
+            _vector(rstd, torch.float32, rows, "rstd", dev), dp, ds, dw, db, rows, cols, _DTYPE_CODES[x.dtype],
+            _DTYPE_CODES[weight.dtype],
+            (ACCUMULATE_DX if accumulate_dx else 0) | (ACCUMULATE_PARAMS if accumulate_params else 0), ws)
+
+
+def logits_workspace_bytes(rows, vocab, top=0):
+    """Device bytes token_logprobs_forward (`top` alternatives) and distill_forward (top 0) need."""
+    out = ctypes.c_uint64(0)
+    _check("bfo_logits_workspace_bytes", _lib().bfo_logits_workspace_bytes(rows, vocab, top, ctypes.byref(out)))
+    return out.value
+
+
+def new_logits_workspace(rows, vocab, top, device):
+    """A device buffer of logits_workspace_bytes(rows, vocab, top) bytes (at least 16)."""
+    return torch.empty(max(16, logits_workspace_bytes(rows, vocab, top)), dtype=torch.uint8, device=device)
+
+
+def _vocab(vocab, cols):
+    if vocab is None:
+        return cols
+    if not 0 < vocab <= cols:
+        raise ValueError(f"vocab is {vocab}, the rows have {cols} columns")
+    return vocab
+
+
+def token_logprobs_forward(logits, targets=None, logprob=None, stats=None, entropy=None, top_index=None,
+                           top_logprob=None, vocab=None, scale=1.0, workspace=None):
+    """Log probabilities of `targets` (int32, negative: masked) under
+    softmax(scale * logits[:, :vocab]) into logprob, with stats (rows x 2: the
+    largest scaled score and the log of the sum of exponentials above it),
+    entropy, and the top_index.shape[1] best tokens.  Every output but the ones
+    wanted may be None."""
+    dev = logits.device
+    lp, ls, rows, cols = _matrix(logits, "logits")
+    v = _vocab(vocab, cols)
+    top = 0
+    if top_index is not None:
+        if top_index.dim() != 2 or top_index.shape[0] != rows:
+            raise ValueError("top_index must have a row of its own for each row of logits")
+        top = top_index.shape[1]
+    ws = _workspace_ptr(workspace, logits_workspace_bytes(rows, v, top), dev, "new_logits_workspace")
+    _launch("token_logprobs_forward", dev, lp, ls, rows, v, _DTYPE_CODES[logits.dtype], scale,
+            _vector(targets, torch.int32, rows, "targets", dev), _vector(logprob, torch.float32, rows, "logprob", dev),
+            _vector(stats, torch.float32, 2 * rows, "stats", dev),
+            _vector(entropy, torch.float32, rows, "entropy", dev), top,
+            _vector(top_index, torch.int32, rows * top, "top_index", dev),
+            _vector(top_logprob, torch.float32, rows * top, "top_logprob", dev), ws)
+
+
+def token_logprobs_backward(logits, targets, stats, dlogprob, dlogits, entropy=None, dentropy=None, vocab=None,
+                            scale=1.0):
+    """Gradient of sum(dlogprob * logprob + dentropy * entropy) into dlogits
+    (the logits' shape; may be the logits), from the forward pass's stats and
+    entropy; columns from vocab on get 0.  targets and dlogprob may both be None."""
+    dev = logits.device
+    lp, ls, rows, cols = _matrix(logits, "logits")
+    dp, ds, _, _ = _matrix(dlogits, "dlogits", logits)
+    _launch("token_logprobs_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols, _DTYPE_CODES[logits.dtype], scale,
+            _vector(targets, torch.int32, rows, "targets", dev),
+            _vector(stats, torch.float32, 2 * rows, "stats", dev),
+            _vector(entropy, torch.float32, rows, "entropy", dev),
+            _vector(dlogprob, torch.float32, rows, "dlogprob", dev),
+            _vector(dentropy, torch.float32, rows, "dentropy", dev), dp, ds)
+
+
+def _teacher(teacher_index, teacher_logits, rows, dev):
+    if teacher_index.dim() != 2 or teacher_index.shape[0] != rows:
+        raise ValueError("teacher_index must have a row of its own for each row of logits")
+    count = teacher_index.shape[1]
+    return (_vector(teacher_index, torch.int32, rows * count, "teacher_index", dev),
+            _vector(teacher_logits, torch.float32, rows * count, "teacher_logits", dev), count)
+
+
+def distill_forward(logits, teacher_index, teacher_logits, kl, stats=None, targets=None, logprob=None, vocab=None,
+                    scale=1.0, workspace=None):
+    """KL divergence of the teacher's softmax over its top logits (rows x count
+    int32 indexes, negative: no entry, and float32 logits) from the student's
+    softmax(scale * logits[:, :vocab]), per row into kl; targets and logprob
+    as in token_logprobs_forward."""
+    dev = logits.device
+    lp, ls, rows, cols = _matrix(logits, "logits")
+    v = _vocab(vocab, cols)
+    ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
+    ws = _workspace_ptr(workspace, logits_workspace_bytes(rows, v, 0), dev, "new_logits_workspace")
+    _launch("distill_forward", dev, lp, ls, rows, v, _DTYPE_CODES[logits.dtype], scale, ti, tl, count,
+            _vector(targets, torch.int32, rows, "targets", dev), _vector(kl, torch.float32, rows, "kl", dev),
+            _vector(logprob, torch.float32, rows, "logprob", dev),
+            _vector(stats, torch.float32, 2 * rows, "stats", dev), ws)
+
+
+def distill_backward(logits, teacher_index, teacher_logits, stats, dkl, dlogits, targets=None, dlogprob=None,
+                     vocab=None, scale=1.0):
+    """Gradient of sum(dkl * kl + dlogprob * logprob) into dlogits (the logits'
+    shape; may be the logits); columns from vocab on get 0."""
+    dev = logits.device
+    lp, ls, rows, cols = _matrix(logits, "logits")
+    dp, ds, _, _ = _matrix(dlogits, "dlogits", logits)
+    ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
+    _launch("distill_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols, _DTYPE_CODES[logits.dtype], scale, ti,
+            tl, count, _vector(targets, torch.int32, rows, "targets", dev),
+            _vector(stats, torch.float32, 2 * rows, "stats", dev),
+            _vector(dkl, torch.float32, rows, "dkl", dev),
+            _vector(dlogprob, torch.float32, rows, "dlogprob", dev), dp, ds)

@@ -7,41 +7,22 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <vector>
 
+#include "bfo_checks.hpp"
 #include "bfo_internal.hpp"
 
 namespace {
 
+using bfo::alignedTo;
+using bfo::anyOverlap;
+using bfo::span;
+
 thread_local int gLastHipError = 0;
 
 int hipFail(hipError_t e) { return bfo::recordHipFailure(e); }
-
-bool alignedTo(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// The byte range [lo, hi) an array argument covers; a null pointer covers
-// nothing.
-struct Span {
-    uintptr_t lo, hi;
-};
-
-Span span(const void *p, uint64_t bytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(p);
-    if (!p) return {0, 0};
-    return {x, bytes > UINTPTR_MAX - x ? UINTPTR_MAX : x + uintptr_t(bytes)};
-}
-
-// True when two of the arrays of one call share a byte: the kernels read and
-// write them as distinct (restrict) buffers.
-bool anyOverlap(std::initializer_list<Span> spans) {
-    for (const Span *a = spans.begin(); a != spans.end(); ++a)
-        for (const Span *b = a + 1; b != spans.end(); ++b)
-            if (a->lo < a->hi && b->lo < b->hi && a->lo < b->hi && b->lo < a->hi) return true;
-    return false;
-}
 
 }  // namespace
 

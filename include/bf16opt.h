@@ -489,6 +489,137 @@ uint64_t bfo_checksum64(const void *data, uint64_t bytes);
 #define BFO_REGION_BYTES (1ull << 34)
 int bfo_spread_layout(const uint64_t *bytes, uint32_t count, uint64_t *offsets, uint64_t *total);
 
+/* ---------------------------------------------------------------------------
+ * Operators of the training loop around the step: where the grads come from.
+ *
+ * Layer norm, the log probabilities of given tokens and distillation from a
+ * teacher's top logits, each with its gradient.  They take no table: every
+ * array is a plain device array on the current device.  Conventions beside
+ * those at the top of this file:
+ *   - Matrices are row-major with unit column stride; a `stride` is the
+ *     distance between rows in elements, at least the row's width (rows of a
+ *     wider buffer, or columns of one, are fine).  Rows and matrices may start
+ *     anywhere their type allows (2 bytes for bf16, 4 for fp32).
+ *   - dtype / param_dtype: BFO_BF16 (bf16 patterns) or BFO_F32; anything else
+ *     BFO_EINVAL.  All arithmetic is binary32; an output in bf16 is rounded
+ *     once, to nearest even.
+ *   - rows may be 0 (the matrices may then be NULL).
+ *   - Results are the same bits from call to call: sums run in an order that
+ *     depends on the sizes only, and there are no atomics in them.
+ *   - Outputs may not overlap an input or one another, except where a call
+ *     says so (BFO_EINVAL).  Only the rows' own elements are written.
+ *   - Workspaces are device memory, 16-byte aligned, of the size the matching
+ *     *_workspace_bytes gives, owned by the caller and used by this call only;
+ *     calls with separate workspaces may run at the same time, and graphs that
+ *     may run at the same time need a workspace each.  Calls allocate nothing
+ *     and can be recorded into a HIP graph.
+ *   - Errors: BFO_EINVAL, BFO_EMISALIGNED, BFO_ERANGE (a size or stride above
+ *     its limit), BFO_EHIP.
+ * ------------------------------------------------------------------------- */
+enum { BFO_BF16 = 0, BFO_F32 = 1 };
+
+/* Layer norm over the columns of x (rows x cols).  Per row:
+ *   mean = sum(x) / cols;  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps)
+ *   out = (x - mean) * rstd * weight + bias
+ * weight and bias hold cols values of param_dtype; bias may be NULL (0).
+ * out has x's type.  mean and rstd (rows floats each, for the backward pass)
+ * may be NULL.  1 <= cols <= BFO_LAYERNORM_MAX_COLS (0 -> BFO_EINVAL, above ->
+ * BFO_ERANGE); eps >= 0 and finite.  A row with an infinity or NaN gives NaN. */
+#define BFO_LAYERNORM_MAX_COLS 16384u
+int layernorm_forward(const void *x, uint64_t x_stride, const void *weight, const void *bias, void *out,
+                      uint64_t out_stride, float *mean, float *rstd, uint64_t rows, uint32_t cols, float eps,
+                      int dtype, int param_dtype, void *stream);
+
+/* *bytes = the workspace layernorm_backward needs.  Host only. */
+int bfo_layernorm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t *bytes);
+
+/* Gradients of layernorm_forward, from its mean and rstd.  With
+ * xhat = (x - mean) * rstd and h = weight * dout, per row:
+ *   dx = rstd * (h - sum(h) / cols - xhat * sum(h * xhat) / cols)
+ * and over the rows dweight = sum(dout * xhat), dbias = sum(dout).
+ * dout and dx have x's type, dweight and dbias param_dtype (so they can be the
+ * layer's places in the flat grads buffer); dbias may be NULL.
+ * accumulate: 0, or BFO_ACCUMULATE_DX (dx += , the residual stream's gradient)
+ * and/or BFO_ACCUMULATE_PARAMS (dweight, dbias += , micro-batches); the sum is
+ * formed in binary32 and rounded once.  rows == 0 writes (or adds) zeros to
+ * dweight and dbias. */
+enum { BFO_ACCUMULATE_DX = 1, BFO_ACCUMULATE_PARAMS = 2 };
+int layernorm_backward(const void *dout, uint64_t dout_stride, const void *x, uint64_t x_stride,
+                       const void *weight, const float *mean, const float *rstd, void *dx, uint64_t dx_stride,
+                       void *dweight, void *dbias, uint64_t rows, uint32_t cols, int dtype, int param_dtype,
+                       int accumulate, void *workspace, void *stream);
+
+/* *bytes = the workspace token_logprobs_forward (top tokens asked for) and
+ * distill_forward (top 0) need; may be 0, and workspace then NULL.  Host only. */
+int bfo_logits_workspace_bytes(uint64_t rows, uint32_t vocab, uint32_t top, uint64_t *bytes);
+
+/* Log probabilities of given tokens.  Row r of logits holds vocab scores (a
+ * wider row's further columns are not read); with z = scale * logits (scale:
+ * 1 / temperature, finite and > 0), M = max(z), S = sum(exp(z - M)):
+ *   stats[r] = {M, log(S)}  (2 floats; log-sum-exp = M + log(S))
+ *   logprob[r] = z[targets[r]] - M - log(S)
+ *   entropy[r] = log(S) - sum(exp(z - M) * (z - M)) / S
+ *   top_index[r][k], top_logprob[r][k], k < top: the `top` largest logits,
+ *     largest first, equal ones by the lower index, and their log probabilities.
+ * targets, logprob (both or neither), stats and entropy may be NULL;
+ * top <= BFO_TOP_MAX and <= vocab; top == 0 takes neither top array.
+ * A negative target masks its row: logprob 0.  A target >= vocab is no token:
+ * logprob NaN.  Scores of -inf have probability 0; a row of nothing else has
+ * stats {-inf, 0}, entropy 0 and log probabilities -inf.  A row with a NaN or
+ * +inf has NaN stats, entropy and log probabilities (top_index then orders NaN
+ * first).  1 <= vocab <= BFO_VOCAB_MAX. */
+#define BFO_TOP_MAX 128u
+#define BFO_VOCAB_MAX (1u << 28)
+int token_logprobs_forward(const void *logits, uint64_t stride, uint64_t rows, uint32_t vocab, int dtype,
+                           float scale, const int32_t *targets, float *logprob, float *stats, float *entropy,
+                           uint32_t top, int32_t *top_index, float *top_logprob, void *workspace, void *stream);
+
+/* Gradient of sum(dlogprob * logprob + dentropy * entropy) with respect to the
+ * logits, from the forward pass's stats and entropy.  With p = exp(z - M - log S):
+ *   dlogits[j] = scale * (dlogprob * ([j == target] - p[j])
+ *                         - dentropy * p[j] * (log p[j] + entropy))   j < vocab
+ *   dlogits[j] = 0                                                    vocab <= j < width
+ * (cross entropy: dlogprob = -1 / tokens.)  dlogits: rows of width >= vocab
+ * columns, of the logits' type; it may be the logits themselves (same pointer
+ * and stride).  targets and dlogprob, entropy and dentropy: both or neither of
+ * a pair, at least one pair.  Rows whose factors are all 0 (masked targets
+ * count as 0) and rows of -inf only get exact zeros, whatever they hold; a
+ * target >= vocab gives a row of NaN. */
+int token_logprobs_backward(const void *logits, uint64_t stride, uint64_t rows, uint32_t vocab, uint32_t width,
+                            int dtype, float scale, const int32_t *targets, const float *stats,
+                            const float *entropy, const float *dlogprob, const float *dentropy, void *dlogits,
+                            uint64_t dlogits_stride, void *stream);
+
+/* Distillation loss against a teacher's top logits.  Row r names `count`
+ * teacher tokens (teacher_index, teacher_logits: rows x count, contiguous; a
+ * negative index is no entry).  With q = softmax(scale * teacher_logits) over
+ * the row's entries and p the student's probabilities over the whole
+ * vocabulary, as in token_logprobs_forward:
+ *   kl[r] = sum_k q[k] * (log q[k] - log p[teacher_index[k]])
+ * (0 for a row without entries, or with entries of -inf only; an entry of
+ * probability 0 adds nothing).  Any
+ * per-row constant in the teacher's logits drops out, so top_logprob of the
+ * teacher's token_logprobs_forward serves too.  A token named twice counts with
+ * both probabilities.  An index >= vocab, or a NaN or +inf among the entries,
+ * gives NaN.  stats, targets and logprob as in token_logprobs_forward (all may
+ * be NULL), so that a loss on the true tokens takes no second pass.
+ * 1 <= count <= BFO_TOP_MAX. */
+int distill_forward(const void *logits, uint64_t stride, uint64_t rows, uint32_t vocab, int dtype, float scale,
+                    const int32_t *teacher_index, const float *teacher_logits, uint32_t count,
+                    const int32_t *targets, float *kl, float *logprob, float *stats, void *workspace,
+                    void *stream);
+
+/* Gradient of sum(dkl * kl + dlogprob * logprob) with respect to the student's
+ * logits (the teacher gets none):
+ *   dlogits[j] = scale * (dkl * (p[j] - q[j]) + dlogprob * ([j == target] - p[j]))
+ * with q[j] the sum over the entries naming j, and dkl counted as 0 in a row
+ * without entries.  targets and dlogprob: both or neither.  dlogits, width,
+ * zero and NaN rows as in token_logprobs_backward. */
+int distill_backward(const void *logits, uint64_t stride, uint64_t rows, uint32_t vocab, uint32_t width,
+                     int dtype, float scale, const int32_t *teacher_index, const float *teacher_logits,
+                     uint32_t count, const int32_t *targets, const float *stats, const float *dkl,
+                     const float *dlogprob, void *dlogits, uint64_t dlogits_stride, void *stream);
+
 /* Static string naming a status code. */
 const char *bfo_status_string(int status);
 

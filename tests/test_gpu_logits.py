@@ -1,0 +1,525 @@
+"""Token log probabilities and distillation on the GPU against their
+definitions in 64 bits.
+
+Tolerances count roundings of half a step u = 2^-24 of binary32.  A row's sum
+of exponentials is a chain of at most n = V / 64 + 64 additions and
+rescalings (each of at most 4 u), the exponential of a distance d costs
+(4 |d| + 4) u relative; with E the mean under p,
+  log sum:   rel = (n + 4 E|d| + 8) u  absolute
+  log prob:  rel + (3 |d| + 4) u
+  entropy:   rel + E(|d| (4 |d| + n + 8)) u + E|d| rel + (2 + H) 2 u.
+Gradients are compared with the formula on the very stats they are given: a
+probability is off by (6 |log p| + |z| + 12) u relative.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U = 2.0 ** -24
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def bfo():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    from bf16_numerics_amd import binding
+    torch.cuda.set_device(0)
+    return binding
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def scores(rows, vocab, dt, seed, pad=0, spread=2.0):
+    """Scores with a raised token per row; padding columns hold NaN, never to be read."""
+    g = gen(seed)
+    z = torch.full((rows, vocab + pad), NAN, device=DEV)
+    z[:, :vocab] = spread * torch.empty(rows, vocab, device=DEV).normal_(generator=g)
+    t = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    z[torch.arange(rows, device=DEV), t] += 8 * torch.rand(rows, generator=g, device=DEV)
+    t[torch.rand(rows, generator=g, device=DEV) < 0.2] = -1
+    return z.to(TYPES[dt]), t.to(torch.int32)
+
+
+def single(scale):
+    """The scale as the entry points take it: a binary32 value."""
+    return float(torch.tensor(scale, dtype=torch.float32))
+
+
+def reference(logits, V, scale, targets):
+    scale = single(scale)
+    z = logits[:, :V].double() * scale
+    m = z.max(1, keepdim=True).values
+    d = z - m
+    logs = torch.logsumexp(d, 1, keepdim=True)
+    logp = d - logs
+    p = logp.exp()
+    pd = torch.where(p > 0, p * d.abs(), 0.0).sum(1)
+    pdd = torch.where(p > 0, p * d * d, 0.0).sum(1)
+    ent = -torch.where(p > 0, p * logp, 0.0).sum(1)
+    n = V / 64 + 64
+    rel = (n + 4 * pd + 8) * U
+    t = targets.long()
+    at = logp.gather(1, t.clamp(min=0, max=V - 1)[:, None])[:, 0]
+    dt = d.gather(1, t.clamp(min=0, max=V - 1)[:, None])[:, 0].abs()
+    live = t >= 0
+    return {"m": m[:, 0], "logs": logs[:, 0], "rel": rel, "ent": ent, "logp": logp, "d": d,
+            "ent_tol": rel + (4 * pdd + (n + 8) * pd) * U + pd * rel + (2 + ent) * 2 * U,
+            "at": torch.where(live, at, 0.0), "at_tol": torch.where(live, rel + (3 * dt + 4) * U, 0.0)}
+
+
+def near(got, ref, tol, what):
+    got = got.double()
+    bad = ~((got - ref).abs() <= tol)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off; worst by {float((got - ref).abs().max())}"
+
+
+def top_reference(logits, V, K):
+    # equal scores by the lower index: stable, largest first; -0 and 0 are equal
+    return torch.sort(logits[:, :V].double() + 0.0, dim=1, descending=True, stable=True).indices[:, :K]
+
+
+def run_forward(bfo, logits, targets, V, scale=1.0, top=0):
+    R = logits.shape[0]
+    f = lambda *s: torch.full(s, NAN, device=DEV)  # noqa: E731
+    out = {"logprob": f(R), "stats": f(R, 2), "entropy": f(R)}
+    if top:
+        out["top_index"] = torch.full((R, top), -7, dtype=torch.int32, device=DEV)
+        out["top_logprob"] = f(R, top)
+    ws = torch.full_like(bfo.new_logits_workspace(R, V, top, DEV), 255)
+    bfo.token_logprobs_forward(logits, targets, out["logprob"], out["stats"], entropy=out["entropy"],
+                               top_index=out.get("top_index"), top_logprob=out.get("top_logprob"), vocab=V,
+                               scale=scale, workspace=ws)
+    return out
+
+
+def check_forward(out, logits, targets, V, scale, top):
+    ref = reference(logits, V, scale, targets)
+    near(out["stats"][:, 0], ref["m"], U * ref["m"].abs(), "max")
+    near(out["stats"][:, 1], ref["logs"], ref["rel"], "log sum")
+    near(out["logprob"], ref["at"], ref["at_tol"], "logprob")
+    near(out["entropy"], ref["ent"], ref["ent_tol"], "entropy")
+    if top:
+        index = top_reference(logits, V, top)
+        assert torch.equal(out["top_index"].long(), index)
+        near(out["top_logprob"], ref["logp"].gather(1, index),
+             ref["rel"][:, None] + (3 * ref["d"].gather(1, index).abs() + 4) * U, "top logprob")
+
+
+SIZES = [(1, 1), (3, 2), (5, 7), (9, 64), (2, 127), (4, 128), (33, 513), (7, 1000), (3, 4095), (3, 4096), (2, 4097),
+         (17, 8193), (5, 32000), (3, 50257), (2, 65537), (1, 131072), (1, 200003)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_forward_sizes(bfo, dt):
+    for k, (rows, V) in enumerate(SIZES):
+        for top in sorted({0, 1, min(V, 5), min(V, 20), min(V, 128)}):
+            scale = (1.0, 0.5, 1.7)[(k + top) % 3]
+            print(dt, rows, V, top, scale, flush=True)
+            logits, targets = scores(rows, V, dt, 300 + k, pad=(0, 5, 64)[k % 3])
+            check_forward(run_forward(bfo, logits, targets, V, scale, top), logits, targets, V, scale, top)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_forward_many_rows(bfo, dt):
+    logits, targets = scores(3001, 1031, dt, 17, pad=3)
+    check_forward(run_forward(bfo, logits, targets, 1031, 1.0, 20), logits, targets, 1031, 1.0, 20)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [300, 5000, 40001, 140000])
+def test_top_of_rows_that_do_not_thin_out(bfo, dt, V):
+    """Equal scores, few distinct scores, sorted rows, all the best in one
+    lane's columns, scores at the type's lowest value."""
+    t = TYPES[dt]
+    E = 16 // t.itemsize
+    rows = [torch.zeros(V), torch.full((V,), -3.0), torch.arange(V) % 3 * 1.0, torch.arange(V) * 0.25,
+            -torch.arange(V) * 0.25, torch.where(torch.arange(V) // E % 512 == 5, 4.0, 0.0),
+            torch.where(torch.arange(V) // E % 512 == 5, torch.arange(V) % 97 * 0.5, -1.0),
+            torch.full((V,), float(torch.finfo(t).min)), torch.full((V,), -INF), torch.full((V,), -INF),
+            torch.where(torch.arange(V) % 2 == 0, -0.0, 0.0)]
+    rows[9][V // 2] = 1.0
+    logits = torch.stack(rows).to(t).to(DEV)
+    targets = torch.full((len(rows),), V // 2, dtype=torch.int32, device=DEV)
+    for top in (1, 20, 128):
+        out = run_forward(bfo, logits, targets, V, 1.0, top)
+        index = top_reference(logits, V, top)
+        assert torch.equal(out["top_index"].long(), index)
+        keep = [i for i in range(len(rows)) if i != 8]
+        sub = {k: v[keep] for k, v in out.items()}
+        ref = reference(logits[keep], V, 1.0, targets[keep])
+        near(sub["stats"][:, 1], ref["logs"], ref["rel"], "log sum")
+        got, want = sub["top_logprob"].double(), ref["logp"].gather(1, index[keep])
+        tol = ref["rel"][:, None] + (3 * ref["d"].gather(1, index[keep]).abs() + 4) * U
+        assert (((got - want).abs() <= tol) | (got == want)).all()
+        # a row of -inf only
+        assert out["stats"][8].tolist() == [-INF, 0.0] and out["entropy"][8] == 0
+        assert out["logprob"][8] == -INF and (out["top_logprob"][8] == -INF).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_masked_scores_nan_inf_and_odd_targets(bfo, dt):
+    V, t = 5003, TYPES[dt]
+    logits, _ = scores(8, V, dt, 5)
+    logits = logits.clone()
+    logits[0, ::2] = -INF                                   # half the vocabulary masked out
+    logits[1, 1:] = float(torch.finfo(t).min)               # all but one at the lowest value
+    logits[2, 77] = NAN
+    logits[3, 78] = INF
+    logits[4, :] = -INF
+    targets = torch.tensor([3, 0, 5, 78, 9, -1, V, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    out = run_forward(bfo, logits, targets, V, 1.0, 10)
+    keep = [0, 1, 5]
+    check_forward({k: v[keep] for k, v in out.items()}, logits[keep], targets[keep], V, 1.0, 10)
+    for r in (2, 3):
+        for k in ("stats", "logprob", "entropy", "top_logprob"):
+            assert out[k][r].isnan().all(), (r, k)
+    assert out["top_index"][2, 0] == 77 and out["top_index"][3, 0] == 78
+    assert out["logprob"][5] == 0 and out["logprob"][6].isnan() and out["logprob"][7].isnan()
+    assert not out["stats"][6:].isnan().any()
+    # gradients: the empty row and rows without factors are 0, bad rows NaN, masked scores 0
+    R = 8
+    g = torch.full((R,), -0.25, device=DEV)
+    h = torch.full((R,), 0.125, device=DEV)
+    h[5] = 0
+    d = torch.full_like(logits, NAN)
+    bfo.token_logprobs_backward(logits, targets, out["stats"], g, d, entropy=out["entropy"], dentropy=h)
+    assert (d[0, ::2] == 0).all() and not d[0].isnan().any()
+    assert not d[1].isnan().any()
+    assert d[2].isnan().all() and d[3].isnan().all() and d[6].isnan().all() and d[7].isnan().all()
+    assert (d[4] == 0).all() and (d[5] == 0).all()
+    # a masked row's scores do not matter, whatever they hold
+    h.zero_()
+    targets.fill_(-1)
+    bfo.token_logprobs_backward(logits, targets, out["stats"], g, d, entropy=out["entropy"], dentropy=h)
+    assert (d == 0).all()
+
+
+def test_forward_outputs_are_optional(bfo):
+    logits, targets = scores(6, 3001, "bf16", 8)
+    full = run_forward(bfo, logits, targets, 3001, 1.0, 7)
+    lp = torch.empty(6, device=DEV)
+    bfo.token_logprobs_forward(logits, targets, lp)
+    assert torch.equal(lp, full["logprob"])
+    st = torch.empty(6, 2, device=DEV)
+    bfo.token_logprobs_forward(logits, stats=st)
+    assert torch.equal(st, full["stats"])
+    ti, tl = torch.empty(6, 7, dtype=torch.int32, device=DEV), torch.empty(6, 7, device=DEV)
+    bfo.token_logprobs_forward(logits, top_index=ti, top_logprob=tl,
+                               workspace=bfo.new_logits_workspace(6, 3001, 7, DEV))
+    assert torch.equal(ti, full["top_index"]) and torch.equal(tl, full["top_logprob"])
+    e = logits[:0]
+    bfo.token_logprobs_forward(e, targets[:0], lp[:0], st[:0])
+    bfo.token_logprobs_backward(e, targets[:0], st[:0], lp[:0], e.clone())
+
+
+# -------------------------------------------------------------------------
+# Gradients
+# -------------------------------------------------------------------------
+
+def gradient_reference(logits, V, scale, stats, base, slope, ent, sparse):
+    """scale * (p * (base + slope * (log p + ent)) + sparse) and its tolerance,
+    from the given stats."""
+    scale = single(scale)
+    z = logits[:, :V].double() * scale
+    s = stats.double()
+    logp = z - s[:, :1] - s[:, 1:]
+    p = logp.exp()
+    lp = torch.where(p > 0, logp, 0.0)
+    z = torch.where(p > 0, z, 0.0)
+    b, k, h = base.double()[:, None], slope.double()[:, None], ent.double()[:, None]
+    dense = p * (b + k * (lp + h))
+    ref = scale * (dense + sparse)
+    size = p * (b.abs() + k.abs() * (lp.abs() + h.abs()))
+    tol = scale * (size * (6 * lp.abs() + z.abs() + 16) * U + 4 * U * (size + sparse.abs())) + 2 * U * ref.abs()
+    return ref, tol
+
+
+def check_gradient(d, V, ref, tol, what=""):
+    half = torch.finfo(d.dtype).eps / 2 if d.dtype != torch.float32 else 0.0
+    near(d[:, :V], ref, tol + half * (ref.abs() + tol) + 1e-37, what)
+    assert (d[:, V:] == 0).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("with_entropy,with_targets", [(True, True), (False, True), (True, False)])
+def test_logprob_gradient(bfo, dt, with_entropy, with_targets):
+    for k, (rows, V) in enumerate(SIZES + [(1500, 257)]):
+        pad = (0, 7, 64)[k % 3]
+        scale = (1.0, 0.5, 1.7)[k % 3]
+        print(dt, rows, V, pad, flush=True)
+        logits, targets = scores(rows, V, dt, 400 + k, pad=pad)
+        out = run_forward(bfo, logits, targets, V, scale)
+        g = gen(k)
+        dlp = torch.empty(rows, device=DEV).normal_(generator=g)
+        den = torch.empty(rows, device=DEV).normal_(generator=g) if with_entropy else torch.zeros(rows, device=DEV)
+        d = torch.full_like(logits, NAN)
+        bfo.token_logprobs_backward(logits, targets if with_targets else None, out["stats"],
+                                    dlp if with_targets else None, d, entropy=out["entropy"] if with_entropy else None,
+                                    dentropy=den if with_entropy else None, vocab=V, scale=scale)
+        hard = torch.where(targets >= 0, dlp, 0.0) if with_targets else torch.zeros(rows, device=DEV)
+        sparse = torch.zeros(rows, V, dtype=torch.float64, device=DEV)
+        sparse.scatter_(1, targets.clamp(min=0).long()[:, None], hard.double()[:, None])
+        check_gradient(d, V, *gradient_reference(logits, V, scale, out["stats"], -hard, -den, out["entropy"], sparse))
+
+
+def test_logprob_gradient_in_place_and_strided(bfo):
+    logits, targets = scores(65, 5001, "bf16", 3, pad=39)
+    out = run_forward(bfo, logits, targets, 5001)
+    g = torch.full((65,), -1 / 65, device=DEV)
+    apart = torch.empty_like(logits)
+    bfo.token_logprobs_backward(logits, targets, out["stats"], g, apart, vocab=5001)
+    place = logits.clone()
+    bfo.token_logprobs_backward(place, targets, out["stats"], g, place, vocab=5001)
+    assert torch.equal(apart, place)
+    wide = torch.full((65, 5040 + 33), 5.0, dtype=torch.bfloat16, device=DEV)
+    bfo.token_logprobs_backward(logits, targets, out["stats"], g, wide[:, 33:], vocab=5001)
+    assert torch.equal(wide[:, 33:], apart) and (wide[:, :33] == 5).all()
+
+
+def teacher(rows, V, K, seed):
+    """K distinct tokens a row, some rows with fewer, some with none."""
+    g = gen(seed)
+    index = torch.stack([torch.randperm(V, generator=g, device=DEV)[:K] for _ in range(rows)])
+    value = 3 * torch.empty(rows, K, device=DEV).normal_(generator=g)
+    keep = torch.randint(0, 2 * K + 1, (rows, 1), generator=g, device=DEV)
+    index = torch.where(torch.arange(K, device=DEV)[None] < keep, index, -1)
+    return index.to(torch.int32), value
+
+
+def teacher_reference(index, value, scale):
+    scale = single(scale)
+    v = torch.where(index >= 0, value.double() * scale, -INF)
+    live = (v > -INF).any(1, keepdim=True)
+    v = torch.where(live, v, 0.0)
+    logq = torch.log_softmax(v, 1)
+    q = torch.where(live & (index >= 0), logq.exp(), 0.0)
+    spread = torch.where(q > 0, v.max(1, keepdim=True).values - v, 0.0)
+    return q, logq, live[:, 0], spread
+
+
+def distill_reference(logits, V, scale, index, value, targets):
+    ref = reference(logits, V, scale, targets)
+    q, logq, live, spread = teacher_reference(index, value, scale)
+    logp = ref["logp"].gather(1, index.clamp(min=0).long())
+    dist = ref["d"].gather(1, index.clamp(min=0).long()).abs()
+    terms = torch.where(q > 0, q * (logq - logp), 0.0)
+    # log q: up to (4 spread + 80) u; log p as above; q itself (4 spread + 80) u relative; 10 additions
+    tol = torch.where(q > 0, q * ((4 * spread + 80) * U * (1 + (logq - logp).abs()) + ref["rel"][:, None]
+                                  + (3 * dist + 6) * U) + 10 * U * terms.abs(), 0.0)
+    return ref, q, live, spread, terms.sum(1), tol.sum(1)
+
+
+def run_distill(bfo, logits, index, value, V, scale, targets=None):
+    R = logits.shape[0]
+    f = lambda *s: torch.full(s, NAN, device=DEV)  # noqa: E731
+    kl, stats, lp = f(R), f(R, 2), f(R) if targets is not None else None
+    bfo.distill_forward(logits, index, value, kl, stats, targets=targets, logprob=lp, vocab=V, scale=scale,
+                        workspace=torch.full_like(bfo.new_logits_workspace(R, V, 0, DEV), 255))
+    return kl, stats, lp
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("hard", [False, True])
+def test_distill_forward_and_gradient(bfo, dt, hard):
+    for k, (rows, V) in enumerate(SIZES + [(700, 513)]):
+        for K in sorted({1, min(V, 20), min(V, 65), min(V, 128)}):
+            scale = (1.0, 0.5, 1.7)[(k + K) % 3]
+            print(dt, hard, rows, V, K, flush=True)
+            logits, targets = scores(rows, V, dt, 500 + k, pad=(0, 7, 64)[k % 3])
+            index, value = teacher(rows, V, K, 600 + k)
+            kl, stats, lp = run_distill(bfo, logits, index, value, V, scale, targets if hard else None)
+            ref, q, live, spread, want, tol = distill_reference(logits, V, scale, index, value, targets)
+            near(kl, want, tol, "kl")
+            near(stats[:, 1], ref["logs"], ref["rel"], "log sum")
+            if hard:
+                near(lp, ref["at"], ref["at_tol"], "logprob")
+            g = gen(k + K)
+            dkl = torch.empty(rows, device=DEV).normal_(generator=g)
+            dlp = torch.empty(rows, device=DEV).normal_(generator=g)
+            d = torch.full_like(logits, NAN)
+            bfo.distill_backward(logits, index, value, stats, dkl, d, targets=targets if hard else None,
+                                 dlogprob=dlp if hard else None, vocab=V, scale=scale)
+            h = torch.where(targets >= 0, dlp, 0.0) if hard else torch.zeros(rows, device=DEV)
+            sparse = torch.zeros(rows, V, dtype=torch.float64, device=DEV)
+            extra = torch.zeros_like(sparse)
+            at = index.clamp(min=0).long()
+            sparse.scatter_add_(1, at, -dkl.double()[:, None] * q)
+            extra.scatter_add_(1, at, dkl.double().abs()[:, None] * q * (4 * spread + 80) * U)
+            sparse.scatter_add_(1, targets.clamp(min=0).long()[:, None], h.double()[:, None])
+            base = torch.where(live, dkl, 0.0) - h
+            zero = torch.zeros(rows, device=DEV)
+            r, t = gradient_reference(logits, V, scale, stats, base, zero, zero, sparse)
+            # base is one rounded difference of terms that may cancel
+            p = (logits[:, :V].double() * single(scale) - stats.double().sum(1, keepdim=True)).exp()
+            t = t + scale * (extra + p * (dkl.abs() + h.abs()).double()[:, None] * 2 * U)
+            check_gradient(d, V, r, t, "dlogits")
+
+
+def test_distill_odd_entries(bfo):
+    """A token named several times, entries of -inf, rows without entries,
+    a student that gives a teacher's token nothing, bad indexes and NaN."""
+    V = 3001
+    logits, targets = scores(9, V, "f32", 12)
+    logits = logits.clone()
+    index, value = teacher(9, V, 16, 13)
+    index[:] = torch.arange(16, device=DEV, dtype=torch.int32) * 100 + 7
+    index[0] = 55                                            # one token, sixteen times
+    index[1, ::2] = 1234
+    value[2, 3:] = -INF
+    index[3] = -1
+    value[4] = -INF
+    logits[5, 107] = -INF                                    # named by the teacher
+    index[6, 4] = V
+    value[7, 2] = NAN
+    index[8, 9], value[8, 9] = -1, NAN                       # no entry: its value is not looked at
+    kl, stats, _ = run_distill(bfo, logits, index, value, V, 1.0)
+    keep = [0, 1, 2, 8]
+    _, q, _, _, want, tol = distill_reference(logits[keep], V, 1.0, index[keep], value[keep], targets[keep])
+    near(kl[keep], want, tol, "kl")
+    assert kl[3] == 0 and kl[4] == 0 and kl[5] == INF and kl[6].isnan() and kl[7].isnan()
+    d = torch.full_like(logits, NAN)
+    dkl = torch.full((9,), 0.5, device=DEV)
+    bfo.distill_backward(logits, index, value, stats, dkl, d)
+    assert (d[3] == 0).all() and (d[4] == 0).all() and d[6].isnan().all() and d[7].isnan().all()
+    assert not d[5].isnan().any()
+    p = (logits.double() - stats.double().sum(1, keepdim=True)).exp()
+    q5 = torch.softmax(value[5].double(), 0)
+    assert abs(float(d[5, 107]) + 0.5 * float(q5[1])) <= 100 * U
+    for i, r in enumerate(keep):
+        sparse = torch.zeros(V, dtype=torch.float64, device=DEV)
+        sparse.index_add_(0, index[r].clamp(min=0).long(), q[i])
+        near(d[r], 0.5 * (p[r] - sparse), 0.5 * (p[r] + sparse) * 400 * U + 1e-37, "dlogits")
+    # the same bits every time, also where equal indexes add
+    again = torch.full_like(logits, NAN)
+    for _ in range(5):
+        bfo.distill_backward(logits, index, value, stats, dkl, again)
+        assert torch.equal(torch.nan_to_num(d, 9.0), torch.nan_to_num(again, 9.0))
+
+
+def test_teacher_side_feeds_the_student_side(bfo):
+    """A teacher's top log probabilities serve as its logits."""
+    V, K = 4001, 20
+    z, t = scores(50, V, "bf16", 21)
+    out = run_forward(bfo, z, t, V, 1.0, K)
+    student, _ = scores(50, V, "bf16", 22)
+    raw = torch.gather(z.float(), 1, out["top_index"].long())
+    a, _, _ = run_distill(bfo, student, out["top_index"], out["top_logprob"], V, 1.0)
+    b, _, _ = run_distill(bfo, student, out["top_index"], raw, V, 1.0)
+    _, _, _, _, want, tol = distill_reference(student, V, 1.0, out["top_index"], raw, t)
+    near(a, want, tol + 50 * U * (1 + want.abs()), "kl from log probabilities")
+    near(b, want, tol, "kl from scores")
+    # the student being the teacher: only the mass outside the top remains, -log of the mass inside
+    same, _, _ = run_distill(bfo, z, out["top_index"], raw, V, 1.0)
+    inside = torch.softmax(z.double(), 1).gather(1, out["top_index"].long()).sum(1)
+    near(same, -inside.log(), 200 * U * (1 + out["entropy"].double()), "kl to itself")
+
+
+def test_gradients_against_differences(bfo):
+    """Directional derivatives of the losses by central differences of their
+    definitions in 64 bits."""
+    V, R, K, scale = 211, 6, 9, single(0.7)
+    logits, targets = scores(R, V, "f32", 31)
+    index, value = teacher(R, V, K, 32)
+    g = gen(33)
+    a, b, c = (torch.empty(R, device=DEV).normal_(generator=g) for _ in range(3))
+    out = run_forward(bfo, logits, targets, V, scale)
+    d1, d2 = torch.empty_like(logits), torch.empty_like(logits)
+    bfo.token_logprobs_backward(logits, targets, out["stats"], a, d1, entropy=out["entropy"], dentropy=b, scale=scale)
+    bfo.distill_backward(logits, index, value, out["stats"], c, d2, targets=targets, dlogprob=a, scale=scale)
+    q, logq, _, _ = teacher_reference(index, value, scale)
+
+    def losses(z):
+        logp = torch.log_softmax(z * scale, 1)
+        at = torch.where(targets >= 0, logp.gather(1, targets.clamp(min=0).long()[:, None])[:, 0], 0.0)
+        ent = -(logp.exp() * logp).sum(1)
+        kl = torch.where(q > 0, q * (logq - logp.gather(1, index.clamp(min=0).long())), 0.0).sum(1)
+        return (a * at + b * ent).sum(), (a * at + c * kl).sum()
+
+    z = logits.double()
+    # what a gradient's terms are made of before they cancel: its rounding is tens of u of these
+    logp = torch.log_softmax(z * scale, 1)
+    p, ent = logp.exp(), out["entropy"].double()[:, None]
+    size = [p * (a.abs()[:, None] + b.abs()[:, None] * (logp.abs() + ent)), p * (a.abs() + c.abs())[:, None]]
+    for s in size:
+        s.scatter_add_(1, targets.clamp(min=0).long()[:, None], a.double().abs()[:, None])
+    size[1].scatter_add_(1, index.clamp(min=0).long(), c.double().abs()[:, None] * q)
+    for trial in range(3):
+        v = torch.empty(R, V, dtype=torch.float64, device=DEV).normal_(generator=g)
+        h = 1e-5
+        up, down = losses(z + h * v), losses(z - h * v)
+        for d, x, y, s in ((d1, up[0], down[0], size[0]), (d2, up[1], down[1], size[1])):
+            slope = float((x - y) / (2 * h))
+            terms = float((scale * s * v.abs()).sum())
+            # h^2 times third derivatives, and the loss's rounding over h, stay below 1e-9
+            assert abs(float((d.double() * v).sum()) - slope) <= 200 * U * terms + 1e-9
+
+
+def test_rows_past_32_bit_offsets(bfo):
+    """The last rows of a matrix whose element offsets pass 2^32."""
+    V, stride = 50257, 50304
+    R = (1 << 32) // stride + 40
+    buf = torch.zeros(R * stride, dtype=torch.bfloat16, device=DEV)
+    logits = buf.view(R, stride)
+    few, t = scores(40, V, "bf16", 77)
+    logits[-40:, :V] = few
+    targets = torch.full((R,), -1, dtype=torch.int32, device=DEV)
+    targets[-40:] = t
+    out = run_forward(bfo, logits, targets, V, 1.0, 3)
+    check_forward({k: v[-40:] for k, v in out.items()}, few, t, V, 1.0, 3)
+    g = torch.ones(R, device=DEV)
+    bfo.token_logprobs_backward(logits, targets, out["stats"], g, logits, vocab=V)
+    apart = torch.empty_like(few)
+    bfo.token_logprobs_backward(few, t, out["stats"][-40:].contiguous(), g[-40:].contiguous(), apart)
+    assert torch.equal(logits[-40:, :V], apart) and (logits[:-40] == 0).all() and (logits[-40:, V:] == 0).all()
+    del buf, logits
+    torch.cuda.empty_cache()
+
+
+def test_same_bits_beside_other_rows_and_on_streams(bfo):
+    V = 9001
+    logits, targets = scores(600, V, "bf16", 51)
+    whole = run_forward(bfo, logits, targets, V, 1.0, 20)
+    for r in (0, 299, 599):
+        one = run_forward(bfo, logits[r:r + 1], targets[r:r + 1], V, 1.0, 20)
+        check_forward(one, logits[r:r + 1], targets[r:r + 1], V, 1.0, 20)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(run_forward(bfo, logits, targets, V, 1.0, 20))
+        torch.cuda.synchronize()
+        for o in outs:
+            for k in whole:
+                assert torch.equal(o[k], whole[k]), k
+
+
+def test_binding_refusals(bfo):
+    logits, targets = scores(4, 100, "bf16", 1)
+    f = torch.empty(4, device=DEV)
+    with pytest.raises(ValueError, match="vocab is 101"):
+        bfo.token_logprobs_forward(logits, targets, f, vocab=101)
+    with pytest.raises(TypeError, match="targets must be torch.int32"):
+        bfo.token_logprobs_forward(logits, targets.long(), f)
+    with pytest.raises(ValueError, match="stats has"):
+        bfo.token_logprobs_forward(logits, targets, f, stats=f)
+    with pytest.raises(bfo.BfoError):
+        bfo.token_logprobs_forward(logits, targets, None)
+    with pytest.raises(bfo.BfoError):
+        bfo.token_logprobs_forward(logits, targets, f, scale=0.0)
+    with pytest.raises(ValueError, match="row of its own"):
+        bfo.token_logprobs_forward(logits, top_index=torch.empty(3, 2, dtype=torch.int32, device=DEV),
+                                   top_logprob=torch.empty(4, 2, device=DEV))
+    with pytest.raises(ValueError, match="shape"):
+        bfo.token_logprobs_backward(logits, targets, torch.empty(4, 2, device=DEV), f, logits[:, :99])
+    index = torch.zeros(4, 0, dtype=torch.int32, device=DEV)
+    with pytest.raises(bfo.BfoError):
+        bfo.distill_forward(logits, index, torch.empty(4, 0, device=DEV), f)
+    assert math.isfinite(bfo.logits_workspace_bytes(1, 1 << 28, 128))
