@@ -647,9 +647,8 @@ def checkpoint_load(directory, step, table, m, v, master=None, params=None):
 _DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _matrix(t, name, like=None):
-    """(device pointer, row stride, rows, columns) of a bf16 or fp32 matrix;
-    `like`: a matrix whose dtype, device and shape it must have."""
+def _matrix(t, name):
+    """(device pointer, row stride, rows, columns) of a bf16 or fp32 matrix on a GPU."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _DTYPE_CODES:
@@ -660,16 +659,26 @@ def _matrix(t, name, like=None):
     stride, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    if like is not None:
-        if t.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-        if t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-        if t.shape != like.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
-    elif t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, expected a GPU")
     return t.data_ptr(), stride if rows > 1 else cols, rows, cols
+
+
+def _matrix_like(t, name, like):
+    """(device pointer, row stride) of a matrix of like's dtype, device and shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    stride, step = t.stride()
+    rows, cols = t.shape
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), stride if rows > 1 else cols
 
 
 def _vector(t, dtype, count, name, dev):
@@ -689,12 +698,10 @@ def _vector(t, dtype, count, name, dev):
     return t.data_ptr()
 
 
-def _param(t, cols, name, like, dev):
-    if t is None:
-        return None
-    if t.dtype not in _DTYPE_CODES:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    return _vector(t, like, cols, name, dev)
+def _param_type(weight):
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in _DTYPE_CODES:
+        raise TypeError("weight must be a torch.bfloat16 or torch.float32 tensor")
+    return weight.dtype
 
 
 def _workspace_ptr(workspace, need, dev, maker):
@@ -708,14 +715,21 @@ def _workspace_ptr(workspace, need, dev, maker):
     return workspace.data_ptr()
 
 
+# The current stream's handle without building a Stream object around it
+# (0.1 against 1.9 us; small calls are bound by what the host does).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(name, dev, *args):
     """Call entry point `name` with `dev` current, on dev's current stream."""
-    fn = getattr(_lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    fn = getattr(_L, name)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _current_raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, _current_raw_stream(index))
     if rc != OK:
         raise BfoError(name, rc)
 
@@ -737,12 +751,11 @@ def layernorm_forward(x, weight, bias, out, mean=None, rstd=None, eps=1e-5):
     mean, rstd: float32 tensors of x's rows for the backward pass, or None."""
     dev = x.device
     xp, xs, rows, cols = _matrix(x, "x")
-    op, os_, _, _ = _matrix(out, "out", x)
-    w = _param(weight, cols, "weight", weight.dtype, dev)
-    b = _param(bias, cols, "bias", weight.dtype, dev)
-    _launch("layernorm_forward", dev, xp, xs, w, b, op, os_, _vector(mean, torch.float32, rows, "mean", dev),
-            _vector(rstd, torch.float32, rows, "rstd", dev), rows, cols, eps, _DTYPE_CODES[x.dtype],
-            _DTYPE_CODES[weight.dtype])
+    op, os_ = _matrix_like(out, "out", x)
+    pt = _param_type(weight)
+    _launch("layernorm_forward", dev, xp, xs, _vector(weight, pt, cols, "weight", dev),
+            _vector(bias, pt, cols, "bias", dev), op, os_, _vector(mean, torch.float32, rows, "mean", dev),
+            _vector(rstd, torch.float32, rows, "rstd", dev), rows, cols, eps, _DTYPE_CODES[x.dtype], _DTYPE_CODES[pt])
 
 
 def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, workspace=None, accumulate_dx=False,
@@ -752,15 +765,16 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, wor
     new_layernorm_workspace(rows, cols, device)."""
     dev = x.device
     xp, xs, rows, cols = _matrix(x, "x")
-    gp, gs, _, _ = _matrix(dout, "dout", x)
-    dp, ds, _, _ = _matrix(dx, "dx", x)
-    w = _param(weight, cols, "weight", weight.dtype, dev)
-    dw = _vector(dweight, weight.dtype, cols, "dweight", dev)
-    db = _vector(dbias, weight.dtype, cols, "dbias", dev)
+    gp, gs = _matrix_like(dout, "dout", x)
+    dp, ds = _matrix_like(dx, "dx", x)
+    pt = _param_type(weight)
+    w = _vector(weight, pt, cols, "weight", dev)
+    dw = _vector(dweight, pt, cols, "dweight", dev)
+    db = _vector(dbias, pt, cols, "dbias", dev)
     ws = _workspace_ptr(workspace, layernorm_workspace_bytes(rows, cols), dev, "new_layernorm_workspace")
     _launch("layernorm_backward", dev, gp, gs, xp, xs, w, _vector(mean, torch.float32, rows, "mean", dev),
             _vector(rstd, torch.float32, rows, "rstd", dev), dp, ds, dw, db, rows, cols, _DTYPE_CODES[x.dtype],
-            _DTYPE_CODES[weight.dtype],
+            _DTYPE_CODES[pt],
             (ACCUMULATE_DX if accumulate_dx else 0) | (ACCUMULATE_PARAMS if accumulate_params else 0), ws)
 
 
@@ -815,7 +829,7 @@ def token_logprobs_backward(logits, targets, stats, dlogprob, dlogits, entropy=N
     entropy; columns from vocab on get 0.  targets and dlogprob may both be None."""
     dev = logits.device
     lp, ls, rows, cols = _matrix(logits, "logits")
-    dp, ds, _, _ = _matrix(dlogits, "dlogits", logits)
+    dp, ds = _matrix_like(dlogits, "dlogits", logits)
     _launch("token_logprobs_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols, _DTYPE_CODES[logits.dtype], scale,
             _vector(targets, torch.int32, rows, "targets", dev),
             _vector(stats, torch.float32, 2 * rows, "stats", dev),
@@ -855,7 +869,7 @@ def distill_backward(logits, teacher_index, teacher_logits, stats, dkl, dlogits,
     shape; may be the logits); columns from vocab on get 0."""
     dev = logits.device
     lp, ls, rows, cols = _matrix(logits, "logits")
-    dp, ds, _, _ = _matrix(dlogits, "dlogits", logits)
+    dp, ds = _matrix_like(dlogits, "dlogits", logits)
     ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
     _launch("distill_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols, _DTYPE_CODES[logits.dtype], scale, ti,
             tl, count, _vector(targets, torch.int32, rows, "targets", dev),

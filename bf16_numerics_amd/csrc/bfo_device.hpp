@@ -70,6 +70,23 @@ struct Chunk {
             }
         }
     }
+    // Columns [c, c + N) of a row of `cols`, -inf outside it (c may be negative).
+    __device__ __forceinline__ void loadScores(const T *row, int c, int cols) {
+        constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : 0xFF80u;
+        if (c >= 0 && c + N <= cols) {
+            load(row + c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? kNone : kNone | kNone << 16;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (uint32_t(c + i) < uint32_t(cols)) {
+                    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(row[c + i]);
+                    else w[i >> 1] ^= (uint32_t(row[c + i]) ^ kNone) << (16 * (i & 1));
+                }
+            }
+        }
+    }
     // Columns [c, c + N) of a row of `cols`, 0 beyond it.
     template <bool kNontemporal = false>
     __device__ __forceinline__ void loadRow(const T *row, uint32_t c, uint32_t cols) {
@@ -79,10 +96,11 @@ struct Chunk {
     }
 };
 
-// Stores N values at columns [c, c + N) of a row of `cols`, rounded to T.
-template <bool kNontemporal = false, typename T, int N>
-__device__ __forceinline__ void storeRow(T *row, uint32_t c, uint32_t cols, const float (&v)[N]) {
-    if (c + N <= cols) {
+// Stores N values at columns [c, c + N) of a row of `cols`, rounded to T; what
+// lies outside the row is left alone (c may be negative).
+template <typename T, int N>
+__device__ __forceinline__ void storeRow(T *row, int c, int cols, const float (&v)[N]) {
+    if (c >= 0 && c + N <= cols) {
         uint32_t w[N * sizeof(T) / 4];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -90,26 +108,51 @@ __device__ __forceinline__ void storeRow(T *row, uint32_t c, uint32_t cols, cons
             else if (i % 2 == 0) w[i / 2] = packBf16(v[i], v[i + 1]);
         }
 #pragma unroll
-        for (int i = 0; i < int(N * sizeof(T) / 4); i += 4) {
-            const Words4 q = {w[i], w[i + 1], w[i + 2], w[i + 3]};
-            Words4 *p = reinterpret_cast<Words4 *>(row + c) + i / 4;
-            if constexpr (kNontemporal) __builtin_nontemporal_store(q, p);
-            else *p = q;
-        }
+        for (int i = 0; i < int(N * sizeof(T) / 4); i += 4)
+            *(reinterpret_cast<Words4 *>(row + c) + i / 4) = Words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (c + uint32_t(i) < cols) storeOne(row + c + i, v[i]);
+            if (uint32_t(c + i) < uint32_t(cols)) storeOne(row + c + i, v[i]);
     }
 }
 
-// Sum over aligned groups of kLanes lanes, the same bits in every lane of a
-// group.
+// Reductions over 16 lanes or the whole wavefront through DPP: rotations
+// within rows of 16 (every lane of a row ends with the same bits), then rows
+// added to their successors, so that lane 63 holds the total.  About a tenth
+// of the latency of exchanges through the LDS crossbar.
+template <int kCtrl, int kRowMask = 0xF>
+__device__ __forceinline__ float dpp(float old, float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(old), __float_as_uint(v), kCtrl, kRowMask, 0xF,
+                                                       false));
+}
+constexpr int kRowRotate = 0x120, kRowBroadcast15 = 0x142, kRowBroadcast31 = 0x143;
+__device__ __forceinline__ float lastLane(float v) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
 template <int kLanes>
 __device__ __forceinline__ float laneSum(float v) {
-#pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+    static_assert(kLanes == 16 || kLanes == 64, "one DPP row or the wavefront");
+    v += dpp<kRowRotate + 8>(0.0f, v);
+    v += dpp<kRowRotate + 4>(0.0f, v);
+    v += dpp<kRowRotate + 2>(0.0f, v);
+    v += dpp<kRowRotate + 1>(0.0f, v);
+    if constexpr (kLanes == 64) {
+        v += dpp<kRowBroadcast15, 0xA>(0.0f, v);
+        v += dpp<kRowBroadcast31, 0xC>(0.0f, v);
+        v = lastLane(v);
+    }
     return v;
+}
+// The wavefront's largest number (a NaN is passed over).
+__device__ __forceinline__ float waveMax(float v) {
+    v = fmaxf(v, dpp<kRowRotate + 8>(v, v));
+    v = fmaxf(v, dpp<kRowRotate + 4>(v, v));
+    v = fmaxf(v, dpp<kRowRotate + 2>(v, v));
+    v = fmaxf(v, dpp<kRowRotate + 1>(v, v));
+    v = fmaxf(v, dpp<kRowBroadcast15, 0xA>(v, v));
+    v = fmaxf(v, dpp<kRowBroadcast31, 0xC>(v, v));
+    return lastLane(v);
 }
 
 // 2^x and the larger of numbers (a NaN is passed over), one instruction each.

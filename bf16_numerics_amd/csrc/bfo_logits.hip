@@ -6,6 +6,8 @@
 // maximum, sum of exponentials and sum of their products with the score
 // (for the entropy) per lane, joined at the end.  Backward: one pass that
 // forms every probability again from the row's maximum and log sum.
+#include <type_traits>
+
 #include "bfo_device.hpp"
 #include "bfo_ops.hpp"
 
@@ -29,18 +31,11 @@ __device__ __forceinline__ Stat raised(const Stat &a, float m, float k) {
     const float d = a.m - m, r = exp2Fast(d * k);
     return {m, a.s * r, r == 0.0f ? 0.0f : r * fmaf(a.s, d, a.t)};
 }
-__device__ __forceinline__ Stat joined(const Stat &a, const Stat &b, float k) {
-    const float m = fmaxf(a.m, b.m);
-    const Stat x = raised(a, m, k), y = raised(b, m, k);
-    return {m, x.s + y.s, x.t + y.t};
-}
-__device__ __forceinline__ Stat waveJoined(Stat a, float k) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const Stat b = {__shfl_xor(a.m, d, 64), __shfl_xor(a.s, d, 64), __shfl_xor(a.t, d, 64)};
-        a = joined(a, b, k);
-    }
-    return a;
+// The wavefront's statistics, in every lane.
+__device__ __forceinline__ Stat waveJoined(const Stat &a, float k) {
+    const float m = waveMax(a.m);
+    const Stat b = raised(a, m, k);
+    return {m, laneSum<64>(b.s), laneSum<64>(b.t)};
 }
 
 // ---------------------------------------------------------------------------
@@ -56,17 +51,36 @@ __device__ __forceinline__ float ofKey(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-constexpr int kBlock = 512;             // lanes per row
-constexpr int kWaves = kBlock / 64;
-constexpr int kGroups = kBlock / 2;     // groups of lanes whose maxima bound the top
+// A row's workgroup: kBlock lanes take the row in steps of kUnroll 16-byte
+// chunks each, whose loads are in flight together.
+constexpr int kUnroll = 4;
+template <typename T>
+constexpr uint32_t chunkElems() {
+    return 16 / sizeof(T);
+}
+
+// Chunks are cut on 128-byte lines of memory, not from the row's first column:
+// the columns of a row's first line that come before the row.
+template <typename T>
+__device__ __forceinline__ int leadOf(const T *row) {
+    return int((reinterpret_cast<uintptr_t>(row) & 127u) / sizeof(T));
+}
+template <typename T>
+constexpr uint32_t kMaxLead = 128 / sizeof(T) - 1;
+
+constexpr int kGroups = 256;            // groups of lanes whose maxima bound the top
+constexpr int kSlots = 16;              // stretches of steps whose maxima are kept per lane
 constexpr uint32_t kCandidates = 1024;  // scores the top is picked from
 
+template <int kBlock>
 struct TopShared {
     alignas(16) uint32_t groupKey[kGroups];
+    uint16_t slotKey[kSlots * kBlock];  // upper halves of the keys of the maxima
+    uint16_t pairs[kCandidates];        // the slots that may hold a candidate
     uint64_t candidate[kCandidates];
     uint32_t histogram[256];
-    uint32_t threshold, count, need, digit;
-    uint32_t waveCount[kWaves];
+    uint32_t threshold, pairCount, count, need, digit;
+    uint32_t waveCount[kBlock / 64];
 };
 
 // The largest 16-bit prefix that at least `top` of the kGroups keys reach:
@@ -87,8 +101,8 @@ __device__ __forceinline__ uint32_t prefixReached(const uint32_t *keys, uint32_t
 // The row's exact top, whatever it holds: the top-th key by four rounds of
 // 256 bins, then the keys above it and the first equal ones in index order.
 // For rows that the bound does not thin out (many equal scores, NaN).
-template <typename T>
-__device__ void exactTop(const T *row, uint32_t V, uint32_t top, TopShared &sh) {
+template <typename T, int kBlock>
+__device__ __noinline__ void exactTop(const T *row, uint32_t V, uint32_t top, TopShared<kBlock> &sh) {
     uint32_t prefix = 0, need = top;
     for (int shift = 24; shift >= 0; shift -= 8) {
         for (uint32_t i = threadIdx.x; i < 256; i += kBlock) sh.histogram[i] = 0;
@@ -120,7 +134,7 @@ __device__ void exactTop(const T *row, uint32_t V, uint32_t top, TopShared &sh) 
         if ((threadIdx.x & 63) == 0) sh.waveCount[threadIdx.x >> 6] = uint32_t(__popcll(same));
         __syncthreads();
         uint32_t before = equal, all = equal;
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < kBlock / 64; ++w) {
             if (w < int(threadIdx.x >> 6)) before += sh.waveCount[w];
             all += sh.waveCount[w];
         }
@@ -132,30 +146,89 @@ __device__ void exactTop(const T *row, uint32_t V, uint32_t top, TopShared &sh) 
     }
 }
 
-// One pass over the row: E scores of a 16-byte chunk per lane and step.
-template <typename T, bool kEntropy>
-__device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k) {
-    constexpr int E = 16 / int(sizeof(T));
+// One pass over the row.  The maximum is raised once a step.  With kTop, the
+// keys of each stretch's maxima stay in slotKey: `perSlot` steps a stretch.
+template <typename T, int kBlock, bool kEntropy, bool kTop>
+__device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint32_t perSlot, uint16_t *slotKey) {
+    constexpr uint32_t E = chunkElems<T>();
     Stat a = {kLowest, 0.0f, 0.0f};
-    for (uint32_t c = threadIdx.x * E; c < V; c += kBlock * E) {
-        Chunk<T, E> v;
-        float x[E];
-        v.loadRow(row, c, V);
+    uint32_t step = 0;
+    float slotMax = -INFINITY;
+    for (int c = int(threadIdx.x * E) - leadOf(row); c < int(V); c += kBlock * E * kUnroll) {
+        Chunk<T, E> v[kUnroll];
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = c + uint32_t(e) < V ? v[e] : -INFINITY;
-        float m = a.m;
+        for (int u = 0; u < kUnroll; ++u) v[u].loadScores(row, c + int(kBlock * E * u), int(V));
+        float m = max3(kLowest, v[0][0], v[0][1]);
 #pragma unroll
-        for (int e = 0; e < E; e += 2) m = max3(m, x[e], x[e + 1]);
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int e = 0; e < int(E); e += 2) m = max3(m, v[u][e], v[u][e + 1]);
+        if constexpr (kTop) {
+            slotMax = fmaxf(slotMax, m);
+            if (++step % perSlot == 0) {
+                slotKey[(step / perSlot - 1) * kBlock + threadIdx.x] = uint16_t(keyOf(slotMax) >> 16);
+                slotMax = -INFINITY;
+            }
+        }
+        m = fmaxf(m, a.m);
         a = raised(a, m, k);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float d = x[e] - m, p = exp2Fast(d * k);
-            a.s += p;
-            if constexpr (kEntropy) a.t = fmaf(p, fmaxf(d, kLowest), a.t);
-        }
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int e = 0; e < int(E); ++e) {
+                const float d = v[u][e] - m, p = exp2Fast(d * k);
+                a.s += p;
+                // p is 0 where d is -inf: their product has to be 0 too
+                if constexpr (kEntropy) a.t = fmaf(p, fmaxf(d, kLowest), a.t);
+            }
+    }
+    if constexpr (kTop) {
+        // The stretch that was under way; the later ones hold no scores.
+        uint32_t slot = step / perSlot;
+        if (step % perSlot) slotKey[slot++ * kBlock + threadIdx.x] = uint16_t(keyOf(slotMax) >> 16);
+        for (; slot < uint32_t(kSlots); ++slot) slotKey[slot * kBlock + threadIdx.x] = 0;
     }
     return a;
 }
+
+// The candidates of the row's top: every score whose key reaches the bound.
+// False if there are too many.
+template <typename T, int kBlock>
+__device__ __forceinline__ bool gatherCandidates(const T *row, uint32_t V, uint32_t perSlot, uint32_t slots,
+                                                 TopShared<kBlock> &sh) {
+    constexpr uint32_t E = chunkElems<T>();
+    const uint32_t thr = sh.threshold;
+    for (uint32_t slot = 0; slot < slots; ++slot) {
+        const uint32_t at = slot * kBlock + threadIdx.x;
+        if (uint32_t(sh.slotKey[at]) << 16 >= thr && sh.slotKey[at]) {
+            const uint32_t n = atomicAdd(&sh.pairCount, 1u);
+            if (n < kCandidates) sh.pairs[n] = uint16_t(at);
+        }
+    }
+    __syncthreads();
+    const uint32_t pairs = sh.pairCount;
+    if (pairs > kCandidates) return false;
+    const uint32_t perPair = perSlot * kUnroll;  // chunks of a stretch
+    for (uint32_t i = threadIdx.x; i < pairs * perPair; i += kBlock) {
+        const uint32_t at = sh.pairs[i / perPair], chunk = (at / kBlock) * perPair + i % perPair;
+        const int c = int((chunk * kBlock + at % kBlock) * E) - leadOf(row);
+        if (c >= int(V)) continue;
+        Chunk<T, E> v;
+        v.loadScores(row, c, int(V));
+#pragma unroll
+        for (int e = 0; e < int(E); ++e) {
+            const uint32_t key = keyOf(v[e]);
+            if (key >= thr && uint32_t(c + e) < V) {
+                const uint32_t n = atomicAdd(&sh.count, 1u);
+                if (n < kCandidates) sh.candidate[n] = (uint64_t(key) << 32) | (0xFFFFFFFFu - uint32_t(c + e));
+            }
+        }
+    }
+    __syncthreads();
+    return sh.count <= kCandidates;
+}
+
+struct Empty {};
 
 struct RowResult {
     float m, s, t, logs, scaled;  // scaled: scale * m
@@ -193,10 +266,7 @@ struct Teacher {
     }
     __device__ __forceinline__ void softmax(float scale) {
         any = __ballot(id[0] >= 0 || id[1] >= 0) != 0;
-        float m = fmaxf(x[0], x[1]);
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-        m = fmaxf(m, kLowest);
+        const float m = fmaxf(waveMax(fmaxf(x[0], x[1])), kLowest);
         float e[2], s = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -216,34 +286,61 @@ struct Teacher {
     }
 };
 
-template <typename T, bool kEntropy, bool kTeacher>
-__global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a) {
+template <typename T, int kBlock, bool kEntropy, bool kTop, bool kTeacher>
+__global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, uint32_t perSlot) {
+    constexpr int kWaves = kBlock / 64;
+    constexpr uint32_t E = chunkElems<T>();
     __shared__ Stat stats[kWaves];
-    __shared__ TopShared sh;
+    __shared__ std::conditional_t<kTop, TopShared<kBlock>, Empty> sh;
     const uint32_t V = a.vocab;
     const float k = a.scale * kLog2e;
     for (uint64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const T *row = static_cast<const T *>(a.logits.p) + r * a.logits.stride;
-        const Stat mine = laneStat<T, kEntropy>(row, V, k);
+        // What the end of the row needs is asked for first.
+        const int target = a.targets ? a.targets[r] : -1;
+        const float targetScore = target >= 0 && uint32_t(target) < V ? toFloat(row[target]) : 0.0f;
+        Teacher te;
+        float teacherScore[2] = {0.0f, 0.0f};
+        if constexpr (kTeacher) {
+            if (threadIdx.x < 64) {
+                te.load(a.teacherIndex + r * a.count, a.teacherLogits + r * a.count, a.count);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (te.id[i] >= 0 && uint32_t(te.id[i]) < V) teacherScore[i] = toFloat(row[te.id[i]]);
+            }
+        }
+        uint16_t *slotKey = nullptr;
+        if constexpr (kTop) slotKey = sh.slotKey;
+        const Stat mine = laneStat<T, kBlock, kEntropy, kTop>(row, V, k, perSlot, slotKey);
         const Stat wave = waveJoined(mine, k);
         if ((threadIdx.x & 63) == 0) stats[threadIdx.x >> 6] = wave;
-        if (a.top) {
+        if constexpr (kTop) {
             // Lanes without scores hold key 0; one whose maximum may be -inf holds that key.
-            uint32_t key = threadIdx.x * (16 / sizeof(T)) < V ? keyOf(mine.m > kLowest ? mine.m : -INFINITY) : 0u;
-            key = max(key, uint32_t(__shfl_xor(int(key), 1, 64)));
-            if (threadIdx.x % 2 == 0) sh.groupKey[threadIdx.x / 2] = key;
+            const int c = int(threadIdx.x * E) - leadOf(row);  // its first chunk, whole or not, or its second
+            const bool some = (c < int(V) && c + int(E) > 0) || c + int(kBlock * E) < int(V);
+            uint32_t key = some ? keyOf(mine.m > kLowest ? mine.m : -INFINITY) : 0u;
+#pragma unroll
+            for (int d = 1; d < kBlock / kGroups; d *= 2) key = max(key, uint32_t(__shfl_xor(int(key), d, 64)));
+            if (threadIdx.x % (kBlock / kGroups) == 0) sh.groupKey[threadIdx.x / (kBlock / kGroups)] = key;
         }
         __syncthreads();
         Stat all = stats[0];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) all = joined(all, stats[w], k);
+        for (int w = 1; w < kWaves; ++w) all.m = fmaxf(all.m, stats[w].m);
+        all.s = all.t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const Stat b = raised(stats[w], all.m, k);
+            all.s += b.s;
+            all.t += b.t;
+        }
         const RowResult res = rowResult(all, a.scale);
         if (threadIdx.x == 0) {
             if (a.stats) a.stats[2 * r] = res.scaled, a.stats[2 * r + 1] = res.logs;
-            if (a.logprob) {
-                const int t = a.targets[r];
-                a.logprob[r] = t < 0 ? 0.0f : uint32_t(t) >= V ? NAN : logProb(res, toFloat(row[t]), a.scale);
-            }
+            if (a.logprob)
+                a.logprob[r] = target < 0            ? 0.0f
+                               : uint32_t(target) >= V ? NAN
+                                                       : logProb(res, targetScore, a.scale);
             if constexpr (kEntropy) {
                 if (a.entropy)
                     a.entropy[r] = res.empty ? 0.0f : res.finite ? res.logs - a.scale * res.t / res.s : NAN;
@@ -251,46 +348,27 @@ __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a) {
         }
         if constexpr (kTeacher) {
             if (threadIdx.x < 64) {
-                Teacher te;
-                te.load(a.teacherIndex + r * a.count, a.teacherLogits + r * a.count, a.count);
                 te.softmax(a.scale);
                 float kl = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (te.id[i] < 0) continue;
                     if (uint32_t(te.id[i]) >= V) kl = NAN;
-                    else if (te.q[i] != 0.0f)
-                        kl += te.q[i] * (te.logq[i] - logProb(res, toFloat(row[te.id[i]]), a.scale));
+                    else if (te.q[i] != 0.0f) kl += te.q[i] * (te.logq[i] - logProb(res, teacherScore[i], a.scale));
                 }
                 kl = laneSum<64>(kl);
                 if (threadIdx.x == 0) a.kl[r] = kl;
             }
         }
-        if (a.top) {
+        if constexpr (kTop) {
             if (threadIdx.x < 64) {
                 const uint32_t thr = prefixReached(sh.groupKey, a.top);
-                if (threadIdx.x == 0) sh.threshold = thr, sh.count = 0;
+                if (threadIdx.x == 0) sh.threshold = thr, sh.count = sh.pairCount = 0;
             }
             __syncthreads();
-            const uint32_t thr = sh.threshold;
-            const bool bounded = res.finite && !res.empty;
-            if (bounded && keyOf(mine.m) >= thr) {
-                constexpr int E = 16 / int(sizeof(T));
-                for (uint32_t c = threadIdx.x * E; c < V; c += kBlock * E) {
-                    Chunk<T, E> v;
-                    v.loadRow(row, c, V);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const uint32_t key = keyOf(v[e]);
-                        if (key >= thr && c + uint32_t(e) < V) {
-                            const uint32_t at = atomicAdd(&sh.count, 1u);
-                            if (at < kCandidates) sh.candidate[at] = (uint64_t(key) << 32) | (0xFFFFFFFFu - (c + e));
-                        }
-                    }
-                }
-            }
-            __syncthreads();
-            if (!bounded || sh.count > kCandidates) {
+            const uint32_t steps = (V + leadOf(row) + kBlock * E * kUnroll - 1) / (kBlock * E * kUnroll);
+            const bool bounded = res.finite && !res.empty;  // the same in every lane
+            if (!bounded || !gatherCandidates(row, V, perSlot, (steps + perSlot - 1) / perSlot, sh)) {
                 __syncthreads();
                 exactTop(row, V, a.top, sh);
             }
@@ -314,10 +392,10 @@ __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a) {
 // Backward: a workgroup owns a segment of a row's columns.
 // ---------------------------------------------------------------------------
 constexpr int kBackBlock = 256;
-constexpr int kBackChunks = 4;
+constexpr int kBackChunks = 4;  // 16-byte chunks per lane
 template <typename T>
 constexpr uint32_t backSegment() {
-    return kBackBlock * kBackChunks * (16 / sizeof(T));
+    return kBackBlock * kBackChunks * chunkElems<T>();
 }
 
 // Teacher entries inside the segment, chained per 16-byte chunk: head[chunk]
@@ -335,24 +413,24 @@ static_assert(BFO_TOP_MAX <= 128, "a lane of one wavefront holds two entries");
 
 // One wavefront: writes the chains of the entries with columns in [c0, c1),
 // each with its part of the gradient, and the part of the row's `base`.
-__device__ __forceinline__ void buildChains(Chains &ch, const Teacher &te, float dkl, uint32_t vocab, uint32_t c0,
-                                            uint32_t c1, uint32_t perChunk) {
+__device__ __forceinline__ void buildChains(Chains &ch, const Teacher &te, float dkl, uint32_t vocab, int c0, int c1,
+                                            uint32_t perChunk) {
     const uint32_t lane = threadIdx.x & 63;
     const uint64_t below = (1ull << lane) - 1;
     const bool bad = __ballot((te.id[0] >= 0 && uint32_t(te.id[0]) >= vocab) ||
                               (te.id[1] >= 0 && uint32_t(te.id[1]) >= vocab)) != 0;
-    const bool in0 = te.id[0] >= 0 && uint32_t(te.id[0]) >= c0 && uint32_t(te.id[0]) < c1;
-    const bool in1 = te.id[1] >= 0 && uint32_t(te.id[1]) >= c0 && uint32_t(te.id[1]) < c1;
+    const bool in0 = te.id[0] >= 0 && te.id[0] >= c0 && te.id[0] < c1;
+    const bool in1 = te.id[1] >= 0 && te.id[1] >= c0 && te.id[1] < c1;
     const uint64_t m0 = __ballot(in0), m1 = __ballot(in1);
     const uint32_t n0 = uint32_t(__popcll(m0)), n = n0 + uint32_t(__popcll(m1));
     if (in0) {
         const uint32_t at = uint32_t(__popcll(m0 & below));
-        ch.column[at] = uint32_t(te.id[0]) - c0;
+        ch.column[at] = uint32_t(te.id[0] - c0);
         ch.value[at] = -dkl * te.q[0];
     }
     if (in1) {
         const uint32_t at = n0 + uint32_t(__popcll(m1 & below));
-        ch.column[at] = uint32_t(te.id[1]) - c0;
+        ch.column[at] = uint32_t(te.id[1] - c0);
         ch.value[at] = -dkl * te.q[1];
     }
     if (lane == 0) ch.base = bad || te.nan ? NAN : te.any ? dkl : 0.0f;
@@ -373,16 +451,18 @@ __device__ __forceinline__ void buildChains(Chains &ch, const Teacher &te, float
     }
 }
 
-// Segments run along x, rows along y.
+// Segments run along x, rows along y.  Segments are cut on 128-byte lines of
+// the output, which is written in whole lines but for the row's ends.
 template <typename T, bool kEntropy, bool kTeacher>
 __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackward a, uint32_t segment) {
-    constexpr int E = 16 / int(sizeof(T));
-    __shared__ Chains ch;
-    const uint32_t V = a.vocab, c0 = blockIdx.x * segment;
-    const uint32_t end = min(c0 + segment, a.width);  // the segment's columns: [c0, end)
+    constexpr int E = int(chunkElems<T>());
+    __shared__ std::conditional_t<kTeacher, Chains, Empty> ch;
+    const int V = int(a.vocab);
     for (uint64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
         const T *row = static_cast<const T *>(a.logits.p) + r * a.logits.stride;
         T *out = static_cast<T *>(a.dlogits.p) + r * a.dlogits.stride;
+        // the segment's columns: [c0, end), those from 0 on
+        const int c0 = int(blockIdx.x * segment) - leadOf(out), end = min(c0 + int(segment), int(a.width));
         const float m = a.stats[2 * r], logs = a.stats[2 * r + 1];
         // dlogits = scale * (p * (base + slope * log p) + what its tokens get)
         int target = -1;
@@ -391,7 +471,7 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
             target = a.targets[r];
             if (target >= 0) {
                 hard = a.dlogprob[r];
-                base = uint32_t(target) >= V ? NAN : -hard;
+                base = target >= V ? NAN : -hard;
             }
         }
         if constexpr (kEntropy) {
@@ -401,13 +481,11 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
         }
         if constexpr (kTeacher) dkl = a.dkl[r];
         bool live = m != -INFINITY && !(hard == 0.0f && base == 0.0f && slope == 0.0f && dkl == 0.0f);
+        const int first = c0 + int(threadIdx.x) * E;
         Chunk<T, E> v[kBackChunks];
         if (live) {
 #pragma unroll
-            for (int k = 0; k < kBackChunks; ++k) {
-                const uint32_t c = (threadIdx.x + kBackBlock * k) * E;
-                if (c < segment) v[k].loadRow(row, c0 + c, V);
-            }
+            for (int k = 0; k < kBackChunks; ++k) v[k].loadScores(row, first + kBackBlock * E * k, min(V, end));
         }
         if constexpr (kTeacher) {
             if (live) {
@@ -418,7 +496,7 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
                     te.softmax(a.scale);
                 }
                 __syncthreads();
-                if (threadIdx.x < 64) buildChains(ch, te, dkl, V, c0, end, E);
+                if (threadIdx.x < 64) buildChains(ch, te, dkl, uint32_t(V), c0, end, E);
                 __syncthreads();
                 base += ch.base;
                 live = !(hard == 0.0f && base == 0.0f && ch.base == 0.0f);
@@ -426,33 +504,39 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
         }
 #pragma unroll
         for (int k = 0; k < kBackChunks; ++k) {
-            const uint32_t at = (threadIdx.x + kBackBlock * k) * E, c = c0 + at;
-            if (at >= segment || c >= end) continue;
+            const int c = first + kBackBlock * E * k;
             float y[E];
             if (live) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
+                    // columns outside the vocabulary hold -inf, so p = 0 there
                     const float lp = fmaf(v[k][e], a.scale, -m) - logs;
                     const float p = exp2Fast(lp * kLog2e);
                     // p is 0 well above -1e4, where the product has to be 0 too
                     y[e] = p * (kEntropy ? fmaf(slope, fmaxf(lp, -1e4f), base) : base);
                 }
                 if constexpr (kTeacher) {
-                    uint32_t h = ch.head[threadIdx.x + kBackBlock * k];
-                    while (h != Chains::kNone) {
-                        const uint32_t col = ch.column[h] - at;
-                        const float val = ch.value[h];
+                    if (c < end) {
+                        uint32_t h = ch.head[(c - c0) / E];
+                        while (h != Chains::kNone) {
+                            const int col = int(ch.column[h]) + c0 - c;
+                            const float val = ch.value[h];
 #pragma unroll
-                        for (int e = 0; e < E; ++e) y[e] += col == uint32_t(e) ? val : 0.0f;
-                        h = ch.next[h];
+                            for (int e = 0; e < E; ++e) y[e] += col == e ? val : 0.0f;
+                            h = ch.next[h];
+                        }
                     }
                 }
-                if (target >= 0 && uint32_t(target) - c < uint32_t(E)) {
+                if (target >= c && target < c + E) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) y[e] += uint32_t(target) - c == uint32_t(e) ? hard : 0.0f;
+                    for (int e = 0; e < E; ++e) y[e] += target - c == e ? hard : 0.0f;
                 }
 #pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = c + uint32_t(e) < V ? y[e] * a.scale : 0.0f;
+                for (int e = 0; e < E; ++e) y[e] *= a.scale;
+                if (c + E > V) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[e] = c + e < V ? y[e] : 0.0f;
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] = 0.0f;
@@ -463,22 +547,37 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
     }
 }
 
-template <typename T>
-hipError_t forward(const LogitsForward &a, hipStream_t stream) {
+template <typename T, int kBlock>
+hipError_t forwardOf(const LogitsForward &a, hipStream_t stream) {
     const dim3 grid(uint32_t(a.rows < kMaxGrid ? a.rows : kMaxGrid)), block(kBlock);
-    if (a.count) hipLaunchKernelGGL((logitsForwardKernel<T, false, true>), grid, block, 0, stream, a);
-    else if (a.entropy) hipLaunchKernelGGL((logitsForwardKernel<T, true, false>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((logitsForwardKernel<T, false, false>), grid, block, 0, stream, a);
+    constexpr uint32_t step = kBlock * chunkElems<T>() * kUnroll;
+    const uint32_t perSlot = ((a.vocab + kMaxLead<T> + step - 1) / step + kSlots - 1) / kSlots;
+    if (a.count) hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, false, false, true>), grid, block, 0, stream, a, perSlot);
+    else if (a.entropy && a.top) hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, true, true, false>), grid, block, 0, stream, a, perSlot);
+    else if (a.entropy) hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, true, false, false>), grid, block, 0, stream, a, perSlot);
+    else if (a.top) hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, false, true, false>), grid, block, 0, stream, a, perSlot);
+    else hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, false, false, false>), grid, block, 0, stream, a, perSlot);
     return hipGetLastError();
 }
 
 template <typename T>
+hipError_t forward(const LogitsForward &a, hipStream_t stream) {
+    // Where every CU has a few rows, small workgroups let the ends of some rows
+    // hide behind the passes of others: 8192 x 50257 bf16 with 20 alternatives
+    // 166 us against 185 with 512 lanes and 405 with 1024 (whose registers leave
+    // one row a CU).  With few rows a row's own pass counts: 64 x 131072 17.4 us
+    // with 512 lanes against 23.4; 512 x 32000 14.5 against 13.8.
+    return a.rows > 512 ? forwardOf<T, 256>(a, stream) : forwardOf<T, 512>(a, stream);
+}
+
+template <typename T>
 hipError_t backward(const LogitsBackward &a, hipStream_t stream) {
-    constexpr uint32_t most = backSegment<T>(), line = 128 / sizeof(T);
-    // Even segments, each starting on a 128-byte line of the row.
-    const uint32_t segments = (a.width + most - 1) / most;
-    const uint32_t segment = ((a.width + segments - 1) / segments + line - 1) / line * line;
-    const dim3 grid((a.width + segment - 1) / segment, uint32_t(a.rows < 65535 ? a.rows : 65535)), block(kBackBlock);
+    constexpr uint32_t line = 128 / sizeof(T);
+    const uint32_t columns = a.width + kMaxLead<T>;
+    // Even segments of whole lines.
+    const uint32_t segments = (columns + backSegment<T>() - 1) / backSegment<T>();
+    const uint32_t segment = ((columns + segments - 1) / segments + line - 1) / line * line;
+    const dim3 grid((columns + segment - 1) / segment, uint32_t(a.rows < 65535 ? a.rows : 65535)), block(kBackBlock);
     if (a.count) hipLaunchKernelGGL((logitsBackwardKernel<T, false, true>), grid, block, 0, stream, a, segment);
     else if (a.dentropy) hipLaunchKernelGGL((logitsBackwardKernel<T, true, false>), grid, block, 0, stream, a, segment);
     else hipLaunchKernelGGL((logitsBackwardKernel<T, false, false>), grid, block, 0, stream, a, segment);
