@@ -40,6 +40,12 @@ struct Chunk {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         else return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
     }
+    // Makes the compiler forget what it knows of the values, so that they stay
+    // packed from one use to the next.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
+    }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0u;
@@ -59,48 +65,41 @@ struct Chunk {
             }
         }
     }
-    // The first n < N values; the others 0.
-    __device__ __forceinline__ void loadPart(const T *p, int n) {
+    // Columns [c, c + N) of those from `base` on, of which [0, cols) are there;
+    // 0 for the others, and for all if not `live`.  The zeros come first, so that
+    // no load waits for another one's lanes.  Here and below a `base` that is the
+    // same in all lanes keeps the addresses at one scalar and one lane offset.
+    __device__ __forceinline__ void loadRow(const T *base, int c, int cols, bool live = true) {
         zero();
+        if (live && c + N <= cols) load(base + c);
+        else if (live && c < cols) loadPart(base, c, 0, cols);
+    }
+    // The same with [lo, hi) there and -inf elsewhere.
+    __device__ __forceinline__ void loadScores(const T *base, int c, int lo, int hi) {
+        constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : 0xFF80u;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? kNone : kNone | kNone << 16;
+        if (c >= lo && c + N <= hi) load(base + c);
+        else if (c + N > lo && c < hi) loadPart(base, c, lo, hi);
+    }
+    // Value by value, those of [lo, hi) only.
+    __device__ __forceinline__ void loadPart(const T *base, int c, int lo, int hi) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if (i < n) {
-                if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(p[i]);
-                else w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+            if (c + i >= lo && c + i < hi) {
+                if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(base[c + i]);
+                else if (i & 1) w[i >> 1] = (w[i >> 1] & 0x0000FFFFu) | uint32_t(base[c + i]) << 16;
+                else w[i >> 1] = (w[i >> 1] & 0xFFFF0000u) | base[c + i];
             }
         }
-    }
-    // Columns [c, c + N) of a row of `cols`, -inf outside it (c may be negative).
-    __device__ __forceinline__ void loadScores(const T *row, int c, int cols) {
-        constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : 0xFF80u;
-        if (c >= 0 && c + N <= cols) {
-            load(row + c);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? kNone : kNone | kNone << 16;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (uint32_t(c + i) < uint32_t(cols)) {
-                    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(row[c + i]);
-                    else w[i >> 1] ^= (uint32_t(row[c + i]) ^ kNone) << (16 * (i & 1));
-                }
-            }
-        }
-    }
-    // Columns [c, c + N) of a row of `cols`, 0 beyond it.
-    template <bool kNontemporal = false>
-    __device__ __forceinline__ void loadRow(const T *row, uint32_t c, uint32_t cols) {
-        if (c + N <= cols) load<kNontemporal>(row + c);
-        else if (c < cols) loadPart(row + c, int(cols - c));
-        else zero();
     }
 };
 
-// Stores N values at columns [c, c + N) of a row of `cols`, rounded to T; what
-// lies outside the row is left alone (c may be negative).
+// Stores N values, rounded to T, at those of the columns [c, c + N) from
+// `base` on that lie in [lo, hi).
 template <typename T, int N>
-__device__ __forceinline__ void storeRow(T *row, int c, int cols, const float (&v)[N]) {
-    if (c >= 0 && c + N <= cols) {
+__device__ __forceinline__ void storeRow(T *base, int c, int lo, int hi, const float (&v)[N]) {
+    if (c >= lo && c + N <= hi) {
         uint32_t w[N * sizeof(T) / 4];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -109,11 +108,11 @@ __device__ __forceinline__ void storeRow(T *row, int c, int cols, const float (&
         }
 #pragma unroll
         for (int i = 0; i < int(N * sizeof(T) / 4); i += 4)
-            *(reinterpret_cast<Words4 *>(row + c) + i / 4) = Words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
-    } else {
+            *(reinterpret_cast<Words4 *>(base + c) + i / 4) = Words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+    } else if (c + N > lo && c < hi) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (uint32_t(c + i) < uint32_t(cols)) storeOne(row + c + i, v[i]);
+            if (c + i >= lo && c + i < hi) storeOne(base + c + i, v[i]);
     }
 }
 

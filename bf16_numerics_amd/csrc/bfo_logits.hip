@@ -154,10 +154,15 @@ __device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint
     Stat a = {kLowest, 0.0f, 0.0f};
     uint32_t step = 0;
     float slotMax = -INFINITY;
-    for (int c = int(threadIdx.x * E) - leadOf(row); c < int(V); c += kBlock * E * kUnroll) {
+    const int lead = leadOf(row), end = int(V) + lead, c = int(threadIdx.x * E);  // columns from the row's line on
+    const T *line = row - lead;
+    for (int c0 = 0; c0 + c < end; c0 += kBlock * E * kUnroll) {
         Chunk<T, E> v[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) v[u].loadScores(row, c + int(kBlock * E * u), int(V));
+        for (int u = 0; u < kUnroll; ++u) {
+            const int at = c0 + int(kBlock * E) * u;
+            v[u].loadScores(line + at, c, lead - at, end - at);
+        }
         float m = max3(kLowest, v[0][0], v[0][1]);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
@@ -214,7 +219,7 @@ __device__ __forceinline__ bool gatherCandidates(const T *row, uint32_t V, uint3
         const int c = int((chunk * kBlock + at % kBlock) * E) - leadOf(row);
         if (c >= int(V)) continue;
         Chunk<T, E> v;
-        v.loadScores(row, c, int(V));
+        v.loadScores(row, c, 0, int(V));
 #pragma unroll
         for (int e = 0; e < int(E); ++e) {
             const uint32_t key = keyOf(v[e]);
@@ -461,7 +466,7 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
     for (uint64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
         const T *row = static_cast<const T *>(a.logits.p) + r * a.logits.stride;
         T *out = static_cast<T *>(a.dlogits.p) + r * a.dlogits.stride;
-        // the segment's columns: [c0, end), those from 0 on
+        // the segment's columns are those of [c0, end) that are not negative
         const int c0 = int(blockIdx.x * segment) - leadOf(out), end = min(c0 + int(segment), int(a.width));
         const float m = a.stats[2 * r], logs = a.stats[2 * r + 1];
         // dlogits = scale * (p * (base + slope * log p) + what its tokens get)
@@ -481,11 +486,14 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
         }
         if constexpr (kTeacher) dkl = a.dkl[r];
         bool live = m != -INFINITY && !(hard == 0.0f && base == 0.0f && slope == 0.0f && dkl == 0.0f);
-        const int first = c0 + int(threadIdx.x) * E;
+        const int lane = int(threadIdx.x) * E;
         Chunk<T, E> v[kBackChunks];
         if (live) {
 #pragma unroll
-            for (int k = 0; k < kBackChunks; ++k) v[k].loadScores(row, first + kBackBlock * E * k, min(V, end));
+            for (int k = 0; k < kBackChunks; ++k) {
+                const int at = c0 + kBackBlock * E * k;
+                v[k].loadScores(row + at, lane, -at, min(V, end) - at);
+            }
         }
         if constexpr (kTeacher) {
             if (live) {
@@ -504,7 +512,7 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
         }
 #pragma unroll
         for (int k = 0; k < kBackChunks; ++k) {
-            const int c = first + kBackBlock * E * k;
+            const int at = c0 + kBackBlock * E * k, c = at + lane;
             float y[E];
             if (live) {
 #pragma unroll
@@ -541,7 +549,7 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] = 0.0f;
             }
-            storeRow(out, c, end, y);
+            storeRow(out + at, lane, -at, end - at, y);
         }
         if constexpr (kTeacher) __syncthreads();
     }
