@@ -75,11 +75,12 @@ struct Chunk {
         else if (live && c < cols) loadPart(base, c, 0, cols);
     }
     // The same with [lo, hi) there and -inf elsewhere.
+    template <bool kNontemporal = false>
     __device__ __forceinline__ void loadScores(const T *base, int c, int lo, int hi) {
         constexpr uint32_t kNone = sizeof(T) == 4 ? 0xFF800000u : 0xFF80u;
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? kNone : kNone | kNone << 16;
-        if (c >= lo && c + N <= hi) load(base + c);
+        if (c >= lo && c + N <= hi) load<kNontemporal>(base + c);
         else if (c + N > lo && c < hi) loadPart(base, c, lo, hi);
     }
     // Value by value, those of [lo, hi) only.
@@ -152,6 +153,19 @@ __device__ __forceinline__ float waveMax(float v) {
     v = fmaxf(v, dpp<kRowBroadcast15, 0xA>(v, v));
     v = fmaxf(v, dpp<kRowBroadcast31, 0xC>(v, v));
     return lastLane(v);
+}
+
+// The wavefront's smallest or largest value.
+template <bool kMax>
+__device__ __forceinline__ uint32_t waveExtreme(uint32_t v) {
+    auto with = [&](uint32_t o) { v = kMax ? max(v, o) : min(v, o); };
+    with(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 8, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 4, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 2, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 1, 0xF, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(v, v, kRowBroadcast15, 0xA, 0xF, false));
+    with(__builtin_amdgcn_update_dpp(v, v, kRowBroadcast31, 0xC, 0xF, false));
+    return __builtin_amdgcn_readlane(v, 63);
 }
 
 // 2^x and the larger of numbers (a NaN is passed over), one instruction each.

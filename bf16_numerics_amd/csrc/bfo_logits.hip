@@ -68,34 +68,41 @@ __device__ __forceinline__ int leadOf(const T *row) {
 template <typename T>
 constexpr uint32_t kMaxLead = 128 / sizeof(T) - 1;
 
-constexpr int kGroups = 256;            // groups of lanes whose maxima bound the top
-constexpr int kSlots = 16;              // stretches of steps whose maxima are kept per lane
-constexpr uint32_t kCandidates = 1024;  // scores the top is picked from
+constexpr uint32_t kNoScores = 0xFFFF;  // upper half of a NaN, which reaches no bound
+constexpr int kGroups = 256;           // groups of lanes whose maxima bound the top
+constexpr int kSlots = 28;             // stretches of a lane's chunks whose maxima are kept
+constexpr uint32_t kCandidates = 512;  // scores the top is picked from
 
 template <int kBlock>
 struct TopShared {
     alignas(16) uint32_t groupKey[kGroups];
-    uint16_t slotKey[kSlots * kBlock];  // upper halves of the keys of the maxima
+    alignas(16) uint64_t candidate[kCandidates];
+    uint16_t slotMax[kSlots * kBlock];  // upper halves of the maxima, kNoScores for none
     uint16_t pairs[kCandidates];        // the slots that may hold a candidate
-    uint64_t candidate[kCandidates];
     uint32_t histogram[256];
-    uint32_t threshold, pairCount, count, need, digit;
+    float bound;
+    uint32_t pairCount, count, need, digit;
     uint32_t waveCount[kBlock / 64];
 };
 
-// The largest 16-bit prefix that at least `top` of the kGroups keys reach:
-// a lower bound of the row's top-th key, since every group's key is that of a
-// score of its own.  One wavefront, four keys a lane.
-__device__ __forceinline__ uint32_t prefixReached(const uint32_t *keys, uint32_t top) {
+// A lower bound of the row's top-th score: every group's key is that of a score
+// of its own, so what `top` of the kGroups keys reach is reached by that many
+// scores.  The largest such 14-bit prefix, found below the keys' common one; one
+// wavefront, four keys a lane.
+__device__ __forceinline__ float boundOf(const uint32_t *keys, uint32_t top) {
+    constexpr int kLowBit = 18;
     const uint4 v = reinterpret_cast<const uint4 *>(keys)[threadIdx.x & 63];
-    uint32_t thr = 0;
-    for (int bit = 31; bit >= 16; --bit) {
-        const uint32_t c = thr | (1u << bit);
+    const uint32_t most = waveExtreme<true>(max(max(v.x, v.y), max(v.z, v.w)));
+    const uint32_t least = waveExtreme<false>(min(min(v.x, v.y), min(v.z, v.w)));
+    const int high = max(31 - __clz(int(most ^ least)), kLowBit - 1);  // the highest bit that differs
+    uint32_t bound = most & ~((2u << high) - 1u);
+    for (int bit = high; bit >= kLowBit; --bit) {
+        const uint32_t c = bound | (1u << bit);
         const int n = __popcll(__ballot(v.x >= c)) + __popcll(__ballot(v.y >= c)) + __popcll(__ballot(v.z >= c)) +
                       __popcll(__ballot(v.w >= c));
-        if (n >= int(top)) thr = c;
+        if (n >= int(top)) bound = c;
     }
-    return thr;
+    return bound <= keyOf(-INFINITY) ? -INFINITY : ofKey(bound);
 }
 
 // The row's exact top, whatever it holds: the top-th key by four rounds of
@@ -146,14 +153,21 @@ __device__ __noinline__ void exactTop(const T *row, uint32_t V, uint32_t top, To
     }
 }
 
-// One pass over the row.  The maximum is raised once a step.  With kTop, the
-// keys of each stretch's maxima stay in slotKey: `perSlot` steps a stretch.
-template <typename T, int kBlock, bool kEntropy, bool kTop>
-__device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint32_t perSlot, uint16_t *slotKey) {
+// One pass over the row.  The maximum is raised once a step.  With kTop, the maxima of stretches of
+// `perSlot` chunks of the lane stay in slotMax.
+template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop>
+__device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint32_t perSlot, uint16_t *slotMax) {
     constexpr uint32_t E = chunkElems<T>();
     Stat a = {kLowest, 0.0f, 0.0f};
-    uint32_t step = 0;
-    float slotMax = -INFINITY;
+    uint32_t slot = 0, held = 0;
+    float stretch = -INFINITY;
+    auto endStretch = [&] {
+        // + 0 makes -0 the 0 it is equal to
+        slotMax[slot * kBlock + threadIdx.x] = uint16_t(__float_as_uint(stretch + 0.0f) >> 16);
+        ++slot;
+        held = 0;
+        stretch = -INFINITY;
+    };
     const int lead = leadOf(row), end = int(V) + lead, c = int(threadIdx.x * E);  // columns from the row's line on
     const T *line = row - lead;
     for (int c0 = 0; c0 + c < end; c0 += kBlock * E * kUnroll) {
@@ -161,21 +175,22 @@ __device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int at = c0 + int(kBlock * E) * u;
-            v[u].loadScores(line + at, c, lead - at, end - at);
+            v[u].template loadScores<kNontemporal>(line + at, c, lead - at, end - at);
         }
-        float m = max3(kLowest, v[0][0], v[0][1]);
+        float m = a.m;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int u = 0; u < kUnroll; ++u) {
+            float top = kTop ? fmaxf(v[u][0], v[u][1]) : m;
 #pragma unroll
-            for (int e = 0; e < int(E); e += 2) m = max3(m, v[u][e], v[u][e + 1]);
-        if constexpr (kTop) {
-            slotMax = fmaxf(slotMax, m);
-            if (++step % perSlot == 0) {
-                slotKey[(step / perSlot - 1) * kBlock + threadIdx.x] = uint16_t(keyOf(slotMax) >> 16);
-                slotMax = -INFINITY;
+            for (int e = kTop ? 2 : 0; e < int(E); e += 2) top = max3(top, v[u][e], v[u][e + 1]);
+            if constexpr (kTop) {
+                stretch = fmaxf(stretch, top);
+                if (++held == perSlot) endStretch();
+                m = fmaxf(m, top);
+            } else {
+                m = top;
             }
         }
-        m = fmaxf(m, a.m);
         a = raised(a, m, k);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
@@ -188,45 +203,63 @@ __device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint
             }
     }
     if constexpr (kTop) {
-        // The stretch that was under way; the later ones hold no scores.
-        uint32_t slot = step / perSlot;
-        if (step % perSlot) slotKey[slot++ * kBlock + threadIdx.x] = uint16_t(keyOf(slotMax) >> 16);
-        for (; slot < uint32_t(kSlots); ++slot) slotKey[slot * kBlock + threadIdx.x] = 0;
+        if (held) endStretch();
+        for (; slot < uint32_t(kSlots); ++slot) slotMax[slot * kBlock + threadIdx.x] = uint16_t(kNoScores);
     }
     return a;
 }
 
-// The candidates of the row's top: every score whose key reaches the bound.
-// False if there are too many.
+// A number of its own below the counter's new value for each active lane, with
+// one atomic a wavefront.
+__device__ __forceinline__ uint32_t claimOne(uint32_t *counter) {
+    const uint64_t active = __ballot(1);
+    const uint32_t before = uint32_t(__popcll(active & ((1ull << (threadIdx.x & 63)) - 1)));
+    uint32_t first = 0;
+    if (before == 0) first = atomicAdd(counter, uint32_t(__popcll(active)));
+    return uint32_t(__builtin_amdgcn_readfirstlane(int(first))) + before;
+}
+
+// The candidates of the row's top: every score that reaches the bound.  False
+// if there are too many.
 template <typename T, int kBlock>
-__device__ __forceinline__ bool gatherCandidates(const T *row, uint32_t V, uint32_t perSlot, uint32_t slots,
+__device__ __forceinline__ bool gatherCandidates(const T *row, uint32_t V, uint32_t perSlot,
                                                  TopShared<kBlock> &sh) {
     constexpr uint32_t E = chunkElems<T>();
-    const uint32_t thr = sh.threshold;
-    for (uint32_t slot = 0; slot < slots; ++slot) {
-        const uint32_t at = slot * kBlock + threadIdx.x;
-        if (uint32_t(sh.slotKey[at]) << 16 >= thr && sh.slotKey[at]) {
-            const uint32_t n = atomicAdd(&sh.pairCount, 1u);
-            if (n < kCandidates) sh.pairs[n] = uint16_t(at);
+    const float bound = sh.bound;
+    uint32_t hits = 0;
+#pragma unroll
+    for (int slot = 0; slot < kSlots; ++slot) {
+        // the maximum cut to its upper half, towards 0: what the bound needs cut the same way or lower; NaN for none
+        const float m = __uint_as_float(uint32_t(sh.slotMax[slot * kBlock + threadIdx.x]) << 16);
+        hits |= (m >= bound ? 1u : 0u) << slot;
+    }
+    while (__ballot(hits != 0)) {
+        if (hits) {
+            const uint32_t n = claimOne(&sh.pairCount);
+            if (n < kCandidates) sh.pairs[n] = uint16_t((__ffs(int(hits)) - 1) * kBlock + threadIdx.x);
+            hits &= hits - 1;
         }
     }
     __syncthreads();
     const uint32_t pairs = sh.pairCount;
     if (pairs > kCandidates) return false;
-    const uint32_t perPair = perSlot * kUnroll;  // chunks of a stretch
-    for (uint32_t i = threadIdx.x; i < pairs * perPair; i += kBlock) {
-        const uint32_t at = sh.pairs[i / perPair], chunk = (at / kBlock) * perPair + i % perPair;
+    for (uint32_t i = threadIdx.x; i < pairs * perSlot; i += kBlock) {
+        const uint32_t at = sh.pairs[i / perSlot], chunk = (at / kBlock) * perSlot + i % perSlot;
         const int c = int((chunk * kBlock + at % kBlock) * E) - leadOf(row);
         if (c >= int(V)) continue;
         Chunk<T, E> v;
         v.loadScores(row, c, 0, int(V));
+        uint32_t reached = 0;
 #pragma unroll
-        for (int e = 0; e < int(E); ++e) {
-            const uint32_t key = keyOf(v[e]);
-            if (key >= thr && uint32_t(c + e) < V) {
-                const uint32_t n = atomicAdd(&sh.count, 1u);
-                if (n < kCandidates) sh.candidate[n] = (uint64_t(key) << 32) | (0xFFFFFFFFu - uint32_t(c + e));
-            }
+        for (int e = 0; e < int(E); ++e) reached |= (v[e] >= bound && uint32_t(c + e) < V ? 1u : 0u) << e;
+        while (reached) {
+            const int at = __ffs(int(reached)) - 1;
+            reached &= reached - 1;
+            float x = v[0];
+#pragma unroll
+            for (int e = 1; e < int(E); ++e) x = at == e ? v[e] : x;
+            const uint32_t n = claimOne(&sh.count);
+            if (n < kCandidates) sh.candidate[n] = (uint64_t(keyOf(x)) << 32) | (0xFFFFFFFFu - uint32_t(c + at));
         }
     }
     __syncthreads();
@@ -252,6 +285,29 @@ __device__ __forceinline__ RowResult rowResult(const Stat &a, float scale) {
 __device__ __forceinline__ float logProb(const RowResult &r, float x, float scale) {
     if (r.empty) return -INFINITY;
     return r.finite ? (x - r.m) * scale - r.logs : NAN;
+}
+
+// Writes the top: keys are unique, so a candidate's place is the number of
+// those above it.
+template <int kBlock>
+__device__ __forceinline__ void placeCandidates(const LogitsForward &a, uint64_t r, const RowResult &res,
+                                                TopShared<kBlock> &sh) {
+    const uint32_t n = sh.count;
+    for (uint32_t i = threadIdx.x; i < n; i += kBlock) {
+        const uint64_t key = sh.candidate[i];
+        const ulonglong2 *pairs = reinterpret_cast<const ulonglong2 *>(sh.candidate);
+        uint32_t place = n & 1u ? sh.candidate[n - 1] > key : 0;
+#pragma unroll 4
+        for (uint32_t j = 0; j < n / 2; ++j) {
+            const ulonglong2 other = pairs[j];
+            place += other.x > key;
+            place += other.y > key;
+        }
+        if (place < a.top) {
+            a.topIndex[r * a.top + place] = int32_t(0xFFFFFFFFu - uint32_t(key));
+            a.topLogprob[r * a.top + place] = logProb(res, ofKey(uint32_t(key >> 32)), a.scale);
+        }
+    }
 }
 
 // The teacher's probabilities of the two entries a lane holds (entries lane
@@ -291,7 +347,7 @@ struct Teacher {
     }
 };
 
-template <typename T, int kBlock, bool kEntropy, bool kTop, bool kTeacher>
+template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop, bool kTeacher>
 __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, uint32_t perSlot) {
     constexpr int kWaves = kBlock / 64;
     constexpr uint32_t E = chunkElems<T>();
@@ -314,9 +370,9 @@ __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, u
                     if (te.id[i] >= 0 && uint32_t(te.id[i]) < V) teacherScore[i] = toFloat(row[te.id[i]]);
             }
         }
-        uint16_t *slotKey = nullptr;
-        if constexpr (kTop) slotKey = sh.slotKey;
-        const Stat mine = laneStat<T, kBlock, kEntropy, kTop>(row, V, k, perSlot, slotKey);
+        uint16_t *slotMax = nullptr;
+        if constexpr (kTop) slotMax = sh.slotMax;
+        const Stat mine = laneStat<T, kBlock, kNontemporal, kEntropy, kTop>(row, V, k, perSlot, slotMax);
         const Stat wave = waveJoined(mine, k);
         if ((threadIdx.x & 63) == 0) stats[threadIdx.x >> 6] = wave;
         if constexpr (kTop) {
@@ -339,17 +395,17 @@ __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, u
             all.s += b.s;
             all.t += b.t;
         }
+        // The last wavefront writes the row's results while the first one looks for
+        // the bound of its top.
         const RowResult res = rowResult(all, a.scale);
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == kBlock - 64) {
             if (a.stats) a.stats[2 * r] = res.scaled, a.stats[2 * r + 1] = res.logs;
             if (a.logprob)
                 a.logprob[r] = target < 0            ? 0.0f
                                : uint32_t(target) >= V ? NAN
                                                        : logProb(res, targetScore, a.scale);
-            if constexpr (kEntropy) {
-                if (a.entropy)
-                    a.entropy[r] = res.empty ? 0.0f : res.finite ? res.logs - a.scale * res.t / res.s : NAN;
-            }
+            if constexpr (kEntropy)
+                a.entropy[r] = res.empty ? 0.0f : res.finite ? res.logs - a.scale * res.t / res.s : NAN;
         }
         if constexpr (kTeacher) {
             if (threadIdx.x < 64) {
@@ -367,27 +423,16 @@ __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, u
         }
         if constexpr (kTop) {
             if (threadIdx.x < 64) {
-                const uint32_t thr = prefixReached(sh.groupKey, a.top);
-                if (threadIdx.x == 0) sh.threshold = thr, sh.count = sh.pairCount = 0;
+                const float bound = boundOf(sh.groupKey, a.top);
+                if (threadIdx.x == 0) sh.bound = bound, sh.count = sh.pairCount = 0;
             }
             __syncthreads();
-            const uint32_t steps = (V + leadOf(row) + kBlock * E * kUnroll - 1) / (kBlock * E * kUnroll);
             const bool bounded = res.finite && !res.empty;  // the same in every lane
-            if (!bounded || !gatherCandidates(row, V, perSlot, (steps + perSlot - 1) / perSlot, sh)) {
+            if (!bounded || !gatherCandidates(row, V, perSlot, sh)) {
                 __syncthreads();
                 exactTop(row, V, a.top, sh);
             }
-            // Keys are unique, so a candidate's place is the number above it.
-            const uint32_t n = sh.count;
-            for (uint32_t i = threadIdx.x; i < n; i += kBlock) {
-                const uint64_t key = sh.candidate[i];
-                uint32_t place = 0;
-                for (uint32_t j = 0; j < n; ++j) place += sh.candidate[j] > key;
-                if (place < a.top) {
-                    a.topIndex[r * a.top + place] = int32_t(0xFFFFFFFFu - uint32_t(key));
-                    a.topLogprob[r * a.top + place] = logProb(res, ofKey(uint32_t(key >> 32)), a.scale);
-                }
-            }
+            placeCandidates<kBlock>(a, r, res, sh);
         }
         __syncthreads();
     }
@@ -555,27 +600,39 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
     }
 }
 
-template <typename T, int kBlock>
-hipError_t forwardOf(const LogitsForward &a, hipStream_t stream) {
-    const dim3 grid(uint32_t(a.rows < kMaxGrid ? a.rows : kMaxGrid)), block(kBlock);
+template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop, bool kTeacher>
+void forwardOf(const LogitsForward &a, hipStream_t stream) {
+    // A lane's chunks, in whole steps, in at most kSlots stretches.
     constexpr uint32_t step = kBlock * chunkElems<T>() * kUnroll;
-    const uint32_t perSlot = ((a.vocab + kMaxLead<T> + step - 1) / step + kSlots - 1) / kSlots;
-    if (a.count) hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, false, false, true>), grid, block, 0, stream, a, perSlot);
-    else if (a.entropy && a.top) hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, true, true, false>), grid, block, 0, stream, a, perSlot);
-    else if (a.entropy) hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, true, false, false>), grid, block, 0, stream, a, perSlot);
-    else if (a.top) hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, false, true, false>), grid, block, 0, stream, a, perSlot);
-    else hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, false, false, false>), grid, block, 0, stream, a, perSlot);
+    const uint32_t perSlot = ((a.vocab + kMaxLead<T> + step - 1) / step * kUnroll + kSlots - 1) / kSlots;
+    const dim3 grid(uint32_t(a.rows < kMaxGrid ? a.rows : kMaxGrid));
+    hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, kNontemporal, kEntropy, kTop, kTeacher>), grid, dim3(kBlock), 0,
+                       stream, a, perSlot);
+}
+
+template <typename T, int kBlock, bool kNontemporal>
+hipError_t forwardKind(const LogitsForward &a, hipStream_t stream) {
+    if (a.count) forwardOf<T, kBlock, kNontemporal, false, false, true>(a, stream);
+    else if (a.entropy && a.top) forwardOf<T, kBlock, kNontemporal, true, true, false>(a, stream);
+    else if (a.entropy) forwardOf<T, kBlock, kNontemporal, true, false, false>(a, stream);
+    else if (a.top) forwardOf<T, kBlock, kNontemporal, false, true, false>(a, stream);
+    else forwardOf<T, kBlock, kNontemporal, false, false, false>(a, stream);
     return hipGetLastError();
 }
 
+// Where every CU has a few rows, small workgroups let the ends of some rows hide
+// behind the passes of others: 8192 x 50257 bf16 with 20 alternatives 166 us
+// with 256 lanes, 185 with 512, 405 with 1024 (whose registers leave one row a
+// CU).  With few rows a row's own pass counts: 64 x 131072 23 us with 256 lanes,
+// 17 with 512; 512 x 32000 14 with both.  Scores of over 64 MB are loaded
+// nontemporally: 8192 x 50257 bf16 147 -> 136 us, fp32 4096 x 50257 139 -> 123,
+// 2048 x 32000 bf16 25 -> 23; below that it gave nothing, and up to 4% away where
+// the caches still held them.
 template <typename T>
 hipError_t forward(const LogitsForward &a, hipStream_t stream) {
-    // Where every CU has a few rows, small workgroups let the ends of some rows
-    // hide behind the passes of others: 8192 x 50257 bf16 with 20 alternatives
-    // 166 us against 185 with 512 lanes and 405 with 1024 (whose registers leave
-    // one row a CU).  With few rows a row's own pass counts: 64 x 131072 17.4 us
-    // with 512 lanes against 23.4; 512 x 32000 14.5 against 13.8.
-    return a.rows > 512 ? forwardOf<T, 256>(a, stream) : forwardOf<T, 512>(a, stream);
+    if (a.rows <= 512) return forwardKind<T, 512, false>(a, stream);
+    if (a.rows * a.vocab * sizeof(T) <= (uint64_t(64) << 20)) return forwardKind<T, 256, false>(a, stream);
+    return forwardKind<T, 256, true>(a, stream);
 }
 
 template <typename T>
