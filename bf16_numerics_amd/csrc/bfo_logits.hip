@@ -287,11 +287,16 @@ __device__ __forceinline__ float logProb(const RowResult &r, float x, float scal
     return r.finite ? (x - r.m) * scale - r.logs : NAN;
 }
 
-// Writes the top: keys are unique, so a candidate's place is the number of
-// those above it.
-template <int kBlock>
-__device__ __forceinline__ void placeCandidates(const LogitsForward &a, uint64_t r, const RowResult &res,
-                                                TopShared<kBlock> &sh) {
+__device__ __forceinline__ void writeTop(const LogitsForward &a, uint64_t r, const RowResult &res, uint64_t key,
+                                         uint32_t place) {
+    a.topIndex[r * a.top + place] = int32_t(0xFFFFFFFFu - uint32_t(key));
+    a.topLogprob[r * a.top + place] = logProb(res, ofKey(uint32_t(key >> 32)), a.scale);
+}
+
+// Calls put(key, place) for the top: keys are unique, so a candidate's place
+// is the number of those above it.
+template <int kBlock, typename F>
+__device__ __forceinline__ void placeCandidates(const TopShared<kBlock> &sh, uint32_t top, F put) {
     const uint32_t n = sh.count;
     for (uint32_t i = threadIdx.x; i < n; i += kBlock) {
         const uint64_t key = sh.candidate[i];
@@ -303,12 +308,23 @@ __device__ __forceinline__ void placeCandidates(const LogitsForward &a, uint64_t
             place += other.x > key;
             place += other.y > key;
         }
-        if (place < a.top) {
-            a.topIndex[r * a.top + place] = int32_t(0xFFFFFFFFu - uint32_t(key));
-            a.topLogprob[r * a.top + place] = logProb(res, ofKey(uint32_t(key >> 32)), a.scale);
-        }
+        if (place < top) put(key, place);
     }
 }
+
+// The segments of each row where few rows are split: statistics ({m, s, t, 0})
+// and the keys of the segments' tops in the workspace.
+struct Segments {
+    uint32_t count, length;
+
+    __device__ __forceinline__ float4 *stats(const LogitsForward &a) const {
+        return static_cast<float4 *>(a.workspace);
+    }
+    __device__ __forceinline__ uint64_t *keys(const LogitsForward &a) const {
+        return reinterpret_cast<uint64_t *>(stats(a) + a.rows * count);
+    }
+};
+constexpr uint32_t kMaxSegments = 8;
 
 // The teacher's probabilities of the two entries a lane holds (entries lane
 // and lane + 64), over the wavefront; -1 marks no entry.
@@ -347,29 +363,76 @@ struct Teacher {
     }
 };
 
-template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop, bool kTeacher>
-__global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, uint32_t perSlot) {
+// What the end of a row needs besides its statistics, asked for at its start.
+template <typename T, bool kTeacher>
+struct RowEnd {
+    int target;
+    float targetScore;
+    Teacher teacher;
+    float teacherScore[2];
+
+    __device__ __forceinline__ void load(const LogitsForward &a, uint64_t r, const T *row) {
+        const uint32_t V = a.vocab;
+        target = a.targets ? a.targets[r] : -1;
+        targetScore = target >= 0 && uint32_t(target) < V ? toFloat(row[target]) : 0.0f;
+        if constexpr (kTeacher) {
+            if (threadIdx.x < 64) {
+                teacher.load(a.teacherIndex + r * a.count, a.teacherLogits + r * a.count, a.count);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool token = teacher.id[i] >= 0 && uint32_t(teacher.id[i]) < V;
+                    teacherScore[i] = token ? toFloat(row[teacher.id[i]]) : 0.0f;
+                }
+            }
+        }
+    }
+    // Thread `writer` writes the row's results, the first wavefront those
+    // against the teacher.
+    __device__ __forceinline__ void write(const LogitsForward &a, uint64_t r, const RowResult &res, bool entropy,
+                                          uint32_t writer) {
+        const uint32_t V = a.vocab;
+        if (threadIdx.x == writer) {
+            if (a.stats) a.stats[2 * r] = res.scaled, a.stats[2 * r + 1] = res.logs;
+            if (a.logprob)
+                a.logprob[r] = target < 0            ? 0.0f
+                               : uint32_t(target) >= V ? NAN
+                                                       : logProb(res, targetScore, a.scale);
+            if (entropy) a.entropy[r] = res.empty ? 0.0f : res.finite ? res.logs - a.scale * res.t / res.s : NAN;
+        }
+        if constexpr (kTeacher) {
+            if (threadIdx.x < 64) {
+                teacher.softmax(a.scale);
+                float kl = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (teacher.id[i] < 0) continue;
+                    if (uint32_t(teacher.id[i]) >= V) kl = NAN;
+                    else if (teacher.q[i] != 0.0f)
+                        kl += teacher.q[i] * (teacher.logq[i] - logProb(res, teacherScore[i], a.scale));
+                }
+                kl = laneSum<64>(kl);
+                if (threadIdx.x == 0) a.kl[r] = kl;
+            }
+        }
+    }
+};
+
+// One workgroup per row, or (kSplit) per segment of a row: then the results are
+// the segment's statistics and the keys of its top, in the workspace, for
+// logitsJoinKernel.
+template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop, bool kTeacher, bool kSplit>
+__global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, uint32_t perSlot, Segments seg) {
     constexpr int kWaves = kBlock / 64;
     constexpr uint32_t E = chunkElems<T>();
     __shared__ Stat stats[kWaves];
     __shared__ std::conditional_t<kTop, TopShared<kBlock>, Empty> sh;
-    const uint32_t V = a.vocab;
+    const uint32_t first = kSplit ? blockIdx.y * seg.length : 0;  // the segment's columns: V from `first` on
+    const uint32_t V = kSplit ? min(seg.length, a.vocab - first) : a.vocab;
     const float k = a.scale * kLog2e;
     for (uint64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const T *row = static_cast<const T *>(a.logits.p) + r * a.logits.stride;
-        // What the end of the row needs is asked for first.
-        const int target = a.targets ? a.targets[r] : -1;
-        const float targetScore = target >= 0 && uint32_t(target) < V ? toFloat(row[target]) : 0.0f;
-        Teacher te;
-        float teacherScore[2] = {0.0f, 0.0f};
-        if constexpr (kTeacher) {
-            if (threadIdx.x < 64) {
-                te.load(a.teacherIndex + r * a.count, a.teacherLogits + r * a.count, a.count);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (te.id[i] >= 0 && uint32_t(te.id[i]) < V) teacherScore[i] = toFloat(row[te.id[i]]);
-            }
-        }
+        const T *row = static_cast<const T *>(a.logits.p) + r * a.logits.stride + first;
+        RowEnd<T, kTeacher> end;
+        if constexpr (!kSplit) end.load(a, r, row);
         uint16_t *slotMax = nullptr;
         if constexpr (kTop) slotMax = sh.slotMax;
         const Stat mine = laneStat<T, kBlock, kNontemporal, kEntropy, kTop>(row, V, k, perSlot, slotMax);
@@ -398,28 +461,10 @@ __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, u
         // The last wavefront writes the row's results while the first one looks for
         // the bound of its top.
         const RowResult res = rowResult(all, a.scale);
-        if (threadIdx.x == kBlock - 64) {
-            if (a.stats) a.stats[2 * r] = res.scaled, a.stats[2 * r + 1] = res.logs;
-            if (a.logprob)
-                a.logprob[r] = target < 0            ? 0.0f
-                               : uint32_t(target) >= V ? NAN
-                                                       : logProb(res, targetScore, a.scale);
-            if constexpr (kEntropy)
-                a.entropy[r] = res.empty ? 0.0f : res.finite ? res.logs - a.scale * res.t / res.s : NAN;
-        }
-        if constexpr (kTeacher) {
-            if (threadIdx.x < 64) {
-                te.softmax(a.scale);
-                float kl = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (te.id[i] < 0) continue;
-                    if (uint32_t(te.id[i]) >= V) kl = NAN;
-                    else if (te.q[i] != 0.0f) kl += te.q[i] * (te.logq[i] - logProb(res, teacherScore[i], a.scale));
-                }
-                kl = laneSum<64>(kl);
-                if (threadIdx.x == 0) a.kl[r] = kl;
-            }
+        if constexpr (kSplit) {
+            if (threadIdx.x == kBlock - 64) seg.stats(a)[r * seg.count + blockIdx.y] = {all.m, all.s, all.t, 0.0f};
+        } else {
+            end.write(a, r, res, kEntropy, kBlock - 64);
         }
         if constexpr (kTop) {
             if (threadIdx.x < 64) {
@@ -432,9 +477,47 @@ __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, u
                 __syncthreads();
                 exactTop(row, V, a.top, sh);
             }
-            placeCandidates<kBlock>(a, r, res, sh);
+            placeCandidates<kBlock>(sh, a.top, [&](uint64_t key, uint32_t place) {
+                if constexpr (kSplit) seg.keys(a)[(r * seg.count + blockIdx.y) * a.top + place] = key - first;
+                else writeTop(a, r, res, key, place);
+            });
         }
         __syncthreads();
+    }
+}
+
+// The segments of a row joined: their statistics, and the best of their tops,
+// where a key's place is its own in its segment's plus, by bisection, the
+// number of larger ones in the others'.
+constexpr int kJoinBlock = 256;
+template <typename T, bool kTeacher>
+__global__ __launch_bounds__(kJoinBlock) void logitsJoinKernel(LogitsForward a, Segments seg) {
+    __shared__ uint64_t keys[kMaxSegments * BFO_TOP_MAX];
+    const uint64_t r = blockIdx.x;
+    const float k = a.scale * kLog2e;
+    RowEnd<T, kTeacher> end;
+    end.load(a, r, static_cast<const T *>(a.logits.p) + r * a.logits.stride);
+    const uint32_t count = seg.count * a.top;
+    for (uint32_t i = threadIdx.x; i < count; i += kJoinBlock) keys[i] = seg.keys(a)[r * count + i];
+    const uint32_t lane = threadIdx.x & 63;
+    const float4 part = lane < seg.count ? seg.stats(a)[r * seg.count + lane] : float4{kLowest, 0.0f, 0.0f, 0.0f};
+    const RowResult res = rowResult(waveJoined({part.x, part.y, part.z}, k), a.scale);
+    end.write(a, r, res, a.entropy != nullptr, kJoinBlock - 64);
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < count; i += kJoinBlock) {
+        const uint64_t key = keys[i];
+        const uint32_t own = i / a.top;
+        uint32_t place = i % a.top;
+        for (uint32_t s = 0; s < seg.count; ++s) {
+            uint32_t low = 0, high = s == own ? 0 : a.top;
+            while (low < high) {
+                const uint32_t mid = (low + high) / 2;
+                if (keys[s * a.top + mid] > key) low = mid + 1;
+                else high = mid;
+            }
+            place += low;
+        }
+        if (place < a.top) writeTop(a, r, res, key, place);
     }
 }
 
@@ -600,23 +683,44 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
     }
 }
 
-template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop, bool kTeacher>
-void forwardOf(const LogitsForward &a, hipStream_t stream) {
-    // A lane's chunks, in whole steps, in at most kSlots stretches.
-    constexpr uint32_t step = kBlock * chunkElems<T>() * kUnroll;
-    const uint32_t perSlot = ((a.vocab + kMaxLead<T> + step - 1) / step * kUnroll + kSlots - 1) / kSlots;
-    const dim3 grid(uint32_t(a.rows < kMaxGrid ? a.rows : kMaxGrid));
-    hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, kNontemporal, kEntropy, kTop, kTeacher>), grid, dim3(kBlock), 0,
-                       stream, a, perSlot);
+// Few rows of many scores are split, to at most one workgroup a CU and at least
+// 16,384 scores a segment; one workgroup reads its row at little more than 20
+// GB/s.  One row of 262,144 bf16 scores 16.4 -> 5.5 us, with entropy and 20
+// alternatives 24.6 -> 12.6; 64 rows of 131,072 16.7 -> 13.6.  At 50,257 scores
+// the second launch costs what the split gains (9.3 -> 10.3), and above 8
+// segments joining their tops costs more again (20 us with 16).  A last segment
+// still holds more than BFO_TOP_MAX scores.
+Segments segmentsOf(uint64_t rows, uint32_t vocab) {
+    uint32_t n = vocab < 65536 || rows > 128 ? 1 : vocab / 16384;
+    if (n > kMaxSegments) n = kMaxSegments;
+    if (n * rows > 256) n = uint32_t(256 / rows);
+    if (n < 2) return {1, vocab};
+    const uint32_t length = ((vocab + n - 1) / n + 63) / 64 * 64;
+    return {(vocab + length - 1) / length, length};
 }
 
-template <typename T, int kBlock, bool kNontemporal>
-hipError_t forwardKind(const LogitsForward &a, hipStream_t stream) {
-    if (a.count) forwardOf<T, kBlock, kNontemporal, false, false, true>(a, stream);
-    else if (a.entropy && a.top) forwardOf<T, kBlock, kNontemporal, true, true, false>(a, stream);
-    else if (a.entropy) forwardOf<T, kBlock, kNontemporal, true, false, false>(a, stream);
-    else if (a.top) forwardOf<T, kBlock, kNontemporal, false, true, false>(a, stream);
-    else forwardOf<T, kBlock, kNontemporal, false, false, false>(a, stream);
+template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop, bool kTeacher, bool kSplit>
+void forwardOf(const LogitsForward &a, Segments seg, hipStream_t stream) {
+    // A lane's chunks, in whole steps, in at most kSlots stretches.
+    constexpr uint32_t step = kBlock * chunkElems<T>() * kUnroll;
+    const uint32_t perSlot = ((seg.length + kMaxLead<T> + step - 1) / step * kUnroll + kSlots - 1) / kSlots;
+    const dim3 grid(uint32_t(a.rows < kMaxGrid ? a.rows : kMaxGrid), seg.count);
+    hipLaunchKernelGGL((logitsForwardKernel<T, kBlock, kNontemporal, kEntropy, kTop, kTeacher, kSplit>), grid,
+                       dim3(kBlock), 0, stream, a, perSlot, seg);
+}
+
+template <typename T, int kBlock, bool kNontemporal, bool kSplit>
+hipError_t forwardKind(const LogitsForward &a, Segments seg, hipStream_t stream) {
+    if (a.count && !kSplit) forwardOf<T, kBlock, kNontemporal, false, false, !kSplit, kSplit>(a, seg, stream);
+    else if (a.entropy && a.top) forwardOf<T, kBlock, kNontemporal, true, true, false, kSplit>(a, seg, stream);
+    else if (a.entropy) forwardOf<T, kBlock, kNontemporal, true, false, false, kSplit>(a, seg, stream);
+    else if (a.top) forwardOf<T, kBlock, kNontemporal, false, true, false, kSplit>(a, seg, stream);
+    else forwardOf<T, kBlock, kNontemporal, false, false, false, kSplit>(a, seg, stream);
+    if constexpr (kSplit) {
+        const dim3 grid(uint32_t(a.rows)), block(kJoinBlock);
+        if (a.count) hipLaunchKernelGGL((logitsJoinKernel<T, true>), grid, block, 0, stream, a, seg);
+        else hipLaunchKernelGGL((logitsJoinKernel<T, false>), grid, block, 0, stream, a, seg);
+    }
     return hipGetLastError();
 }
 
@@ -630,9 +734,11 @@ hipError_t forwardKind(const LogitsForward &a, hipStream_t stream) {
 // the caches still held them.
 template <typename T>
 hipError_t forward(const LogitsForward &a, hipStream_t stream) {
-    if (a.rows <= 512) return forwardKind<T, 512, false>(a, stream);
-    if (a.rows * a.vocab * sizeof(T) <= (uint64_t(64) << 20)) return forwardKind<T, 256, false>(a, stream);
-    return forwardKind<T, 256, true>(a, stream);
+    const Segments seg = segmentsOf(a.rows, a.vocab);
+    if (seg.count > 1) return forwardKind<T, 512, false, true>(a, seg, stream);
+    if (a.rows <= 512) return forwardKind<T, 512, false, false>(a, seg, stream);
+    if (a.rows * a.vocab * sizeof(T) <= (uint64_t(64) << 20)) return forwardKind<T, 256, false, false>(a, seg, stream);
+    return forwardKind<T, 256, true, false>(a, seg, stream);
 }
 
 template <typename T>
@@ -651,7 +757,10 @@ hipError_t backward(const LogitsBackward &a, hipStream_t stream) {
 
 }  // namespace
 
-uint64_t logitsWorkspaceBytes(uint64_t, uint32_t, uint32_t) { return 0; }
+uint64_t logitsWorkspaceBytes(uint64_t rows, uint32_t vocab, uint32_t top) {
+    const Segments seg = segmentsOf(rows, vocab);
+    return seg.count > 1 ? rows * seg.count * (sizeof(float4) + top * sizeof(uint64_t)) : 0;
+}
 
 hipError_t launchLogitsForward(const LogitsForward &a, int dtype, hipStream_t stream) {
     if (!a.rows) return hipSuccess;

@@ -84,6 +84,12 @@ def top_reference(logits, V, K):
     return torch.sort(logits[:, :V].double() + 0.0, dim=1, descending=True, stable=True).indices[:, :K]
 
 
+def top_reference_nan_first(logits, V, K):
+    z = logits[:, :V].double() + 0.0
+    z[z == INF] = 1e300
+    return torch.sort(torch.where(z.isnan(), INF, z), dim=1, descending=True, stable=True).indices[:, :K]
+
+
 def run_forward(bfo, logits, targets, V, scale=1.0, top=0):
     R = logits.shape[0]
     f = lambda *s: torch.full(s, NAN, device=DEV)  # noqa: E731
@@ -198,6 +204,45 @@ def test_masked_scores_nan_inf_and_odd_targets(bfo, dt):
     targets.fill_(-1)
     bfo.token_logprobs_backward(logits, targets, out["stats"], g, d, entropy=out["entropy"], dentropy=h)
     assert (d == 0).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_few_rows_of_a_long_vocabulary(bfo, dt):
+    """Rows that are split over workgroups: NaN, +inf and -inf in one stretch of
+    the vocabulary only, equal scores across the stretches, targets and teacher
+    tokens anywhere, odd starts; the same bits every time."""
+    V, pad = 131071, 1
+    logits, targets = scores(7, V, dt, 91, pad=pad)
+    logits = logits.clone()
+    logits[1, 100_000:] = -INF
+    logits[2, ::16384] = 40.0                                # ties in every stretch
+    logits[3, 5] = NAN
+    logits[4, V - 1] = INF
+    logits[5, :V] = -INF
+    logits[6, :] = 0.0
+    targets = torch.tensor([V - 1, 3, 16384, 5, 6, 7, -1], dtype=torch.int32, device=DEV)
+    assert bfo.logits_workspace_bytes(7, V, 128) > 0
+    for top in (1, 20, 128):
+        out = run_forward(bfo, logits, targets, V, 1.0, top)
+        assert torch.equal(out["top_index"].long(), top_reference_nan_first(logits, V, top))
+        keep = [0, 2, 6]
+        check_forward({k: v[keep] for k, v in out.items()}, logits[keep], targets[keep], V, 1.0, top)
+        check_forward({k: v[1:2] for k, v in out.items()}, logits[1:2], targets[1:2], V, 1.0, top)
+        for r in (3, 4):
+            assert all(out[k][r].isnan().all() for k in ("stats", "logprob", "entropy", "top_logprob"))
+        assert out["stats"][5].tolist() == [-INF, 0.0] and out["entropy"][5] == 0 and out["logprob"][5] == -INF
+        again = run_forward(bfo, logits, targets, V, 1.0, top)
+        for k in out:
+            assert torch.equal(torch.nan_to_num(out[k], 9.0), torch.nan_to_num(again[k], 9.0)), k
+    with pytest.raises(ValueError, match="new_logits_workspace"):
+        bfo.token_logprobs_forward(logits, stats=torch.empty(7, 2, device=DEV), vocab=V)
+    index, value = teacher(7, V, 128, 92)
+    index[0, :3] = torch.tensor([0, V - 1, 16384], dtype=torch.int32)
+    kl, _, lp = run_distill(bfo, logits, index, value, V, 1.0, targets)
+    keep = [0, 2, 6]
+    ref, _, _, _, want, tol = distill_reference(logits[keep], V, 1.0, index[keep], value[keep], targets[keep])
+    near(kl[keep], want, tol, "kl")
+    near(lp[keep], ref["at"], ref["at_tol"], "logprob")
 
 
 def test_forward_outputs_are_optional(bfo):

@@ -125,6 +125,15 @@ def test_token_logprobs_forward_refusals(bfo):
     assert lib.bfo_logits_workspace_bytes(4, 1000, 129, ctypes.byref(out)) == bfo.ERANGE
     assert lib.bfo_logits_workspace_bytes(4, (1 << 28) + 1, 0, ctypes.byref(out)) == bfo.ERANGE
     assert lib.bfo_logits_workspace_bytes(0, 100, 5, ctypes.byref(out)) == bfo.OK and out.value == 0
+    # few rows of many scores need a workspace: none, or one on the outputs, is refused
+    assert lib.bfo_logits_workspace_bytes(1, 131072, 128, ctypes.byref(out)) == bfo.OK and out.value > 0
+    assert f(rows=1, V=131072, s=131072, ws=None) == bfo.EINVAL
+    assert f(rows=1, V=131072, s=131072, ws=ptr(3)) == bfo.EINVAL
+    assert kd(bfo, rows=1, V=131072, s=131072, ws=None) == bfo.EINVAL
+    for rows in range(0, 300):
+        for vocab in (1, 65535, 65536, 65537, 131071, 1 << 20, 1 << 28):
+            assert lib.bfo_logits_workspace_bytes(rows, vocab, min(vocab, 128), ctypes.byref(out)) == bfo.OK
+            assert out.value <= 256 * (16 + 8 * 128)
 
 
 def lp_backward(bfo, **kw):
