@@ -6,6 +6,7 @@ kernels.  Importing this module fails loudly when the library has not been
 built -- there is no fallback path.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -664,18 +665,17 @@ def _matrix(t, name):
     return t.data_ptr(), stride if rows > 1 else cols, rows, cols
 
 
-def _matrix_like(t, name, like):
-    """(device pointer, row stride) of a matrix of like's dtype, device and shape."""
+def _matrix_like(t, name, dtype, dev, rows, cols):
+    """(device pointer, row stride) of a rows x cols matrix of that dtype and device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if t.shape != like.shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
     stride, step = t.stride()
-    rows, cols = t.shape
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     return t.data_ptr(), stride if rows > 1 else cols
@@ -734,6 +734,7 @@ def _launch(name, dev, *args):
         raise BfoError(name, rc)
 
 
+@functools.lru_cache(maxsize=4096)
 def layernorm_workspace_bytes(rows, cols):
     """Device bytes layernorm_backward needs as workspace."""
     out = ctypes.c_uint64(0)
@@ -751,7 +752,7 @@ def layernorm_forward(x, weight, bias, out, mean=None, rstd=None, eps=1e-5):
     mean, rstd: float32 tensors of x's rows for the backward pass, or None."""
     dev = x.device
     xp, xs, rows, cols = _matrix(x, "x")
-    op, os_ = _matrix_like(out, "out", x)
+    op, os_ = _matrix_like(out, "out", x.dtype, dev, rows, cols)
     pt = _param_type(weight)
     _launch("layernorm_forward", dev, xp, xs, _vector(weight, pt, cols, "weight", dev),
             _vector(bias, pt, cols, "bias", dev), op, os_, _vector(mean, torch.float32, rows, "mean", dev),
@@ -765,8 +766,8 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, wor
     new_layernorm_workspace(rows, cols, device)."""
     dev = x.device
     xp, xs, rows, cols = _matrix(x, "x")
-    gp, gs = _matrix_like(dout, "dout", x)
-    dp, ds = _matrix_like(dx, "dx", x)
+    gp, gs = _matrix_like(dout, "dout", x.dtype, dev, rows, cols)
+    dp, ds = _matrix_like(dx, "dx", x.dtype, dev, rows, cols)
     pt = _param_type(weight)
     w = _vector(weight, pt, cols, "weight", dev)
     dw = _vector(dweight, pt, cols, "dweight", dev)
@@ -778,6 +779,7 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, wor
             (ACCUMULATE_DX if accumulate_dx else 0) | (ACCUMULATE_PARAMS if accumulate_params else 0), ws)
 
 
+@functools.lru_cache(maxsize=4096)
 def logits_workspace_bytes(rows, vocab, top=0):
     """Device bytes token_logprobs_forward (`top` alternatives) and distill_forward (top 0) need."""
     out = ctypes.c_uint64(0)
@@ -829,7 +831,7 @@ def token_logprobs_backward(logits, targets, stats, dlogprob, dlogits, entropy=N
     entropy; columns from vocab on get 0.  targets and dlogprob may both be None."""
     dev = logits.device
     lp, ls, rows, cols = _matrix(logits, "logits")
-    dp, ds = _matrix_like(dlogits, "dlogits", logits)
+    dp, ds = _matrix_like(dlogits, "dlogits", logits.dtype, dev, rows, cols)
     _launch("token_logprobs_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols, _DTYPE_CODES[logits.dtype], scale,
             _vector(targets, torch.int32, rows, "targets", dev),
             _vector(stats, torch.float32, 2 * rows, "stats", dev),
@@ -869,7 +871,7 @@ def distill_backward(logits, teacher_index, teacher_logits, stats, dkl, dlogits,
     shape; may be the logits); columns from vocab on get 0."""
     dev = logits.device
     lp, ls, rows, cols = _matrix(logits, "logits")
-    dp, ds = _matrix_like(dlogits, "dlogits", logits)
+    dp, ds = _matrix_like(dlogits, "dlogits", logits.dtype, dev, rows, cols)
     ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
     _launch("distill_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols, _DTYPE_CODES[logits.dtype], scale, ti,
             tl, count, _vector(targets, torch.int32, rows, "targets", dev),

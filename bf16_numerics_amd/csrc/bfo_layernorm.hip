@@ -114,29 +114,23 @@ __global__ __launch_bounds__(kBlock) void lnForwardKernel(LayerNormForward a) {
     }
 }
 
-// Stage 1: dx of the workgroup's rows, and its sums of dout * xhat and dout per
-// column, which stay in registers over the rows, are added over the row groups
-// through LDS and end as one row of the partials.
-template <typename T, typename W, int kLanes, int kChunks, int kBlock>
-__global__ __launch_bounds__(kBlock) void lnBackwardKernel(LayerNormBackward a) {
+// dx of the rows first, first + step, ... of a workgroup's kBlock / kLanes row
+// groups; with kSums, each lane's sums of dout * xhat and dout per column.
+template <typename T, typename W, int kLanes, int kChunks, int kBlock, bool kSums, int kSlots>
+__device__ __forceinline__ void rowGradients(const LayerNormBackward &a, uint64_t first, uint64_t step,
+                                             float (&red)[2][kBlock / 64][2], float (&dw)[kSlots],
+                                             float (&db)[kSlots]) {
     constexpr int E = 16 / int(sizeof(T));
-    constexpr int kRows = kBlock / kLanes;
-    constexpr int kSlots = kChunks * E;
-    __shared__ float red[2][kBlock / 64][2];
-    __shared__ float sums[kRows > 1 ? 2 * kSlots * kLanes : 1];
     constexpr int kWidth = kLanes * E;  // columns from chunk to chunk
-    const int lane = int(threadIdx.x % kLanes), c = lane * E, C = int(a.cols);
+    const int c = int(threadIdx.x % kLanes) * E, C = int(a.cols);
     const uint32_t sub = rowGroup<kLanes>();
     const float inv = 1.0f / float(C);
     const bool addDx = (a.accumulate & BFO_ACCUMULATE_DX) != 0;
     Chunk<W, E> w[kChunks];
-    float dw[kSlots], db[kSlots];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) w[k].loadRow(static_cast<const W *>(a.weight) + kWidth * k, c, C - kWidth * k);
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) dw[i] = db[i] = 0.0f;
     int turn = 0;
-    for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < a.rows; base += uint64_t(gridDim.x) * kRows) {
+    for (uint64_t base = first; base < a.rows; base += step) {
         const uint64_t row = base + sub;
         const bool live = row < a.rows;
         const T *x = static_cast<const T *>(a.x.p) + row * a.x.stride;
@@ -148,10 +142,10 @@ __global__ __launch_bounds__(kBlock) void lnBackwardKernel(LayerNormBackward a) 
             xr[k].loadRow(x + kWidth * k, c, C - kWidth * k, live);
             gr[k].loadRow(g + kWidth * k, c, C - kWidth * k, live);
         }
-        float xhat[kSlots], h[kSlots], s[2] = {0.0f, 0.0f};
+        float xhat[kChunks * E], h[kChunks * E], s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
-            if constexpr (kSlots > 8) w[k].forget();  // two registers a value are too many
+            if constexpr (kChunks * E > 8) w[k].forget();  // two registers a value are too many
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int j = k * E + e;
@@ -159,8 +153,10 @@ __global__ __launch_bounds__(kBlock) void lnBackwardKernel(LayerNormBackward a) 
                 h[j] = gr[k][e] * w[k][e];
                 s[0] += h[j];
                 s[1] = fmaf(h[j], xhat[j], s[1]);
-                dw[j] = fmaf(gr[k][e], xhat[j], dw[j]);
-                db[j] += gr[k][e];
+                if constexpr (kSums) {
+                    dw[j] = fmaf(gr[k][e], xhat[j], dw[j]);
+                    db[j] += gr[k][e];
+                }
             }
         }
         rowSums<kLanes, kBlock>(s, red[turn]);
@@ -183,6 +179,31 @@ __global__ __launch_bounds__(kBlock) void lnBackwardKernel(LayerNormBackward a) 
             storeRow(dx + kWidth * k, c, 0, C - kWidth * k, y);
         }
     }
+}
+
+template <typename W>
+__device__ __forceinline__ void storeParam(W *out, float v, bool add) {
+    storeOne(out, add ? toFloat(*out) + v : v);
+}
+
+// Stage 1: dx of the workgroup's rows, and its sums per column, which stay in
+// registers over the rows, are added over the row groups through LDS and end
+// as one row of the partials.
+template <typename T, typename W, int kLanes, int kChunks, int kBlock>
+__global__ __launch_bounds__(kBlock) void lnBackwardKernel(LayerNormBackward a) {
+    constexpr int E = 16 / int(sizeof(T));
+    constexpr int kRows = kBlock / kLanes;
+    constexpr int kSlots = kChunks * E;
+    constexpr int kWidth = kLanes * E;
+    __shared__ float red[2][kBlock / 64][2];
+    __shared__ float sums[kRows > 1 ? 2 * kSlots * kLanes : 1];
+    const int lane = int(threadIdx.x % kLanes), c = lane * E, C = int(a.cols);
+    const uint32_t sub = rowGroup<kLanes>();
+    float dw[kSlots], db[kSlots];
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) dw[i] = db[i] = 0.0f;
+    rowGradients<T, W, kLanes, kChunks, kBlock, true>(a, uint64_t(blockIdx.x) * kRows, uint64_t(gridDim.x) * kRows, red,
+                                                      dw, db);
     float *part = a.partials + uint64_t(blockIdx.x) * 2 * C;
     if constexpr (kRows > 1) {
         // The groups add in turn: group 0 first, then 1, ...
@@ -210,6 +231,67 @@ __global__ __launch_bounds__(kBlock) void lnBackwardKernel(LayerNormBackward a) 
     }
 }
 
+// Few rows, in one launch and without partials: mean and rstd are given, so
+// dweight and dbias need nothing of dx.  The first workgroups sum 32 columns
+// each over all rows (8 lanes a row, kBlock / 8 rows at a time), the others
+// form dx; both read x and dout, which the caches hold.
+constexpr int kSlabCols = 32;
+template <typename T, typename W, int kLanes, int kChunks, int kBlock>
+__global__ __launch_bounds__(kBlock) void lnBackwardFewKernel(LayerNormBackward a, uint32_t slabs) {
+    constexpr int kRows = kBlock / kLanes;
+    constexpr int N = 4, kRowLanes = kSlabCols / N, kGroups = kBlock / kRowLanes, kAtOnce = 4;
+    constexpr int kParts = kBlock / (2 * kSlabCols);  // lanes that add one column's sums
+    __shared__ float red[2][kBlock / 64][2];
+    __shared__ float sums[kGroups][2 * kSlabCols + 1];
+    if (blockIdx.x >= slabs) {
+        float none[1];
+        rowGradients<T, W, kLanes, kChunks, kBlock, false>(a, uint64_t(blockIdx.x - slabs) * kRows,
+                                                           uint64_t(gridDim.x - slabs) * kRows, red, none, none);
+        return;
+    }
+    const int c0 = int(blockIdx.x) * kSlabCols, left = int(a.cols) - c0;
+    const int c = int(threadIdx.x % kRowLanes) * N;
+    const uint32_t group = threadIdx.x / kRowLanes;
+    float dw[N] = {}, db[N] = {};
+    for (uint64_t base = group; base < a.rows; base += kGroups * kAtOnce) {
+        Chunk<T, N> xr[kAtOnce], gr[kAtOnce];
+        float mean[kAtOnce], rstd[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const uint64_t row = base + kGroups * i;
+            const bool live = row < a.rows;
+            xr[i].loadRow(static_cast<const T *>(a.x.p) + row * a.x.stride + c0, c, left, live);
+            gr[i].loadRow(static_cast<const T *>(a.dout.p) + row * a.dout.stride + c0, c, left, live);
+            mean[i] = live ? a.mean[row] : 0.0f;
+            rstd[i] = live ? a.rstd[row] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                dw[e] = fmaf(gr[i][e], (xr[i][e] - mean[i]) * rstd[i], dw[e]);
+                db[e] += gr[i][e];
+            }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        sums[group][c + e] = dw[e];
+        sums[group][kSlabCols + c + e] = db[e];
+    }
+    __syncthreads();
+    const int column = int(threadIdx.x) / kParts, part = int(threadIdx.x) % kParts;
+    float t = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kGroups / kParts; ++g) t += sums[part * (kGroups / kParts) + g][column];
+#pragma unroll
+    for (int d = 1; d < kParts; d *= 2) t += __shfl_xor(t, d, 64);
+    const int at = column % kSlabCols;
+    if (part == 0 && at < left) {
+        W *out = static_cast<W *>(column < kSlabCols ? a.dweight : a.dbias);
+        if (out) storeParam(out + c0 + at, t, (a.accumulate & BFO_ACCUMULATE_PARAMS) != 0);
+    }
+}
+
 // Stage 2: 32 columns per workgroup; 32 groups of lanes add every 32nd partial
 // row each, then the groups' sums are added in order.
 constexpr int kParamCols = 32, kParamGroups = 32;
@@ -233,8 +315,7 @@ __global__ __launch_bounds__(kParamCols *kParamGroups) void lnParamKernel(const 
         float t = 0.0f;
 #pragma unroll
         for (int g = 0; g < kParamGroups; ++g) t += sums[g][lane];
-        if (add) t += toFloat(out[c]);
-        storeOne(out + c, t);
+        storeParam(out + c, t, add != 0);
     }
 }
 
@@ -267,6 +348,12 @@ struct BackwardShape {
     static constexpr int kRows = kBlock / kLanes;
 };
 
+// Up to here one launch for all gradients is faster than rows and partials: 512
+// rows of 1,600 bf16 5.2 us against 8.9, 256 rows of 4,096 3.6 against 11.1, one
+// row 2.7 against 5.0.  With 1,024 rows it is even (10.0), with 2,048 slower
+// (18.8 against 11.4): a column workgroup walks all rows by itself.
+constexpr uint64_t kFewRows = 512;
+
 template <typename F>
 auto byWidth(uint32_t cols, F f) {
     if (cols <= 128) return f(std::integral_constant<int, 0>{});
@@ -296,6 +383,7 @@ hipError_t byTypes(int dtype, int paramDtype, F f) {
 // CU has registers for one workgroup (4096 x 8192 bf16: 50 us against 55 with
 // 512, whose partials are twice as many).
 uint32_t lnBackwardBlocks(uint64_t rows, uint32_t cols) {
+    if (rows <= kFewRows) return 0;
     const int perBlock = byWidth(cols, [](auto width) {
         constexpr int kWidth = decltype(width)::value;
         static_assert(BackwardShape<kWidth, bf16_t>::kRows == BackwardShape<kWidth, float>::kRows,
@@ -322,6 +410,15 @@ hipError_t launchLayerNormForward(const LayerNormForward &a, hipStream_t stream)
 
 hipError_t launchLayerNormBackward(const LayerNormBackward &a, hipStream_t stream) {
     const uint32_t blocks = lnBackwardBlocks(a.rows, a.cols);
+    if (a.rows && a.rows <= kFewRows)
+        return byTypes(a.dtype, a.paramDtype, [&](auto t, auto w) {
+            byWidth(a.cols, [&](auto width) {
+                using S = BackwardShape<decltype(width)::value, decltype(t)>;
+                const uint32_t slabs = (a.cols + kSlabCols - 1) / kSlabCols;
+                hipLaunchKernelGGL((lnBackwardFewKernel<decltype(t), decltype(w), S::kLanes, S::kChunks, S::kBlock>),
+                                   dim3(slabs + gridFor(a.rows, S::kRows, 1024)), dim3(S::kBlock), 0, stream, a, slabs);
+            });
+        });
     return byTypes(a.dtype, a.paramDtype, [&](auto t, auto w) {
         using W = decltype(w);
         if (blocks)

@@ -170,7 +170,9 @@ int layernorm_backward(const void *dout, uint64_t dout_stride, const void *x, ui
     if (rc == BFO_OK) rc = matrix(x, x_stride, rows, cols, dtype, in);
     if (rc == BFO_OK) rc = matrix(dx, dx_stride, rows, cols, dtype, res);
     if (rc != BFO_OK) return rc;
-    if (rows && (!mean || !rstd || !workspace)) return BFO_EINVAL;
+    if (rows && (!mean || !rstd)) return BFO_EINVAL;
+    const uint64_t need = bfo::lnWorkspaceBytes(rows, cols);
+    if (need && !workspace) return BFO_EINVAL;
     if (!allAligned({weight, dweight, dbias}, sizeOf(param_dtype)) || !allAligned({mean, rstd}, 4) ||
         !alignedTo(workspace, 16))
         return BFO_EMISALIGNED;
@@ -180,7 +182,7 @@ int layernorm_backward(const void *dout, uint64_t dout_stride, const void *x, ui
                        reads(rstd, 4 * rows),
                        writes(dweight, pb),
                        writes(dbias, pb),
-                       writes(workspace, bfo::lnWorkspaceBytes(rows, cols))};
+                       writes(workspace, need)};
     if (conflict(use) || conflict(g, false, use) || conflict(in, false, use) || conflict(res, true, use) ||
         overlap(g, res) || overlap(in, res))
         return BFO_EINVAL;

@@ -22,8 +22,8 @@ struct Matrix {
 
 // Layer norm backward: stage 1 runs lnBackwardBlocks workgroups, each of which
 // sums its rows' terms of dweight and dbias into one row of 2 * cols floats of
-// the workspace; stage 2 adds those rows.  The partition depends on the sizes
-// only.
+// the workspace; stage 2 adds those rows.  Few rows (0 workgroups here) take
+// one launch without partials.  The partition depends on the sizes only.
 uint32_t lnBackwardBlocks(uint64_t rows, uint32_t cols);
 inline uint64_t lnWorkspaceBytes(uint64_t rows, uint32_t cols) {
     return uint64_t(lnBackwardBlocks(rows, cols)) * 2 * cols * sizeof(float);

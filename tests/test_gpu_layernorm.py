@@ -159,7 +159,8 @@ def backward_reference(x, d, w, mean, rstd):
 
 def param_depth(rows):
     """Additions in a chain of the parameter sums: rows per group of lanes (at least 512 groups once
-    there are that many rows), up to 16 groups of a workgroup, 16 partial rows per lane group, 32 groups."""
+    there are that many rows), up to 16 groups of a workgroup, 16 partial rows per lane group, 32 groups.
+    (Up to 512 rows: 16 rows per group of lanes, 8 groups, 4 exchanges -- fewer.)"""
     return rows // 512 + 1 + 16 + 16 + 32 + 4
 
 
@@ -194,7 +195,7 @@ def stats_of(x, eps=1e-5):
 
 @pytest.mark.parametrize("dt,pdt", COMBOS)
 def test_backward_sizes(bfo, dt, pdt):
-    for k, (rows, cols) in enumerate(SHAPES + [(2048, 64), (2049, 768), (5000, 33)]):
+    for k, (rows, cols) in enumerate(SHAPES + [(2048, 64), (2049, 768), (5000, 33), (512, 300), (513, 300), (511, 2049), (700, 9000)]):
         print(dt, pdt, rows, cols, flush=True)
         x, d, w, _ = inputs(rows, cols, TYPES[dt], TYPES[pdt], 200 + k, pad=k % 3)
         mean, rstd = stats_of(x)
@@ -311,8 +312,13 @@ def test_binding_refusals(bfo):
     with pytest.raises(ValueError, match="weight is on cpu"):
         bfo.layernorm_forward(x, w.cpu(), b.cpu(), out)
     mean, rstd = stats_of(x)
+    many, _, _, _ = inputs(3000, 64, torch.bfloat16, torch.bfloat16, 2)
+    s = stats_of(many)
     with pytest.raises(ValueError, match="new_layernorm_workspace"):
-        bfo.layernorm_backward(d, x, w, mean, rstd, out, w.clone(), b.clone())
+        bfo.layernorm_backward(many, many.clone(), w, *s, torch.empty_like(many), w.clone(), b.clone())
+    with pytest.raises(ValueError, match="new_layernorm_workspace"):
+        bfo.layernorm_backward(many, many.clone(), w, *s, torch.empty_like(many), w.clone(), b.clone(),
+                               workspace=bfo.new_layernorm_workspace(600, 64, DEV))
     with pytest.raises(bfo.BfoError):
         bfo.layernorm_backward(d, x, w, mean, rstd, d, w.clone(), b.clone(),
                                workspace=bfo.new_layernorm_workspace(8, 64, DEV))

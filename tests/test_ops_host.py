@@ -58,7 +58,7 @@ def test_layernorm_forward_refusals(bfo):
 
 def ln_backward(bfo, **kw):
     a = dict(g=ptr(0), gs=64, x=ptr(1), xs=64, w=ptr(2), mean=ptr(3), rstd=ptr(4), dx=ptr(5), ds=64, dw=ptr(6),
-             db=ptr(7), rows=4, cols=64, dt=0, pdt=0, acc=0, ws=ptr(8))
+             db=ptr(7), rows=3000, cols=64, dt=0, pdt=0, acc=0, ws=ptr(8))
     a.update(kw)
     return bfo.library().layernorm_backward(a["g"], a["gs"], a["x"], a["xs"], a["w"], a["mean"], a["rstd"], a["dx"],
                                             a["ds"], a["dw"], a["db"], a["rows"], a["cols"], a["dt"], a["pdt"],
@@ -85,9 +85,9 @@ def test_layernorm_backward_refusals(bfo):
     assert lib.bfo_layernorm_workspace_bytes(4, 0, ctypes.byref(out)) == bfo.EINVAL
     assert lib.bfo_layernorm_workspace_bytes(4, 16385, ctypes.byref(out)) == bfo.ERANGE
     assert lib.bfo_layernorm_workspace_bytes(0, 64, ctypes.byref(out)) == bfo.OK and out.value == 0
-    for rows in (1, 5, 1000, 1 << 20):
+    for rows in (1, 5, 512, 513, 1000, 1 << 20):
         assert lib.bfo_layernorm_workspace_bytes(rows, 16384, ctypes.byref(out)) == bfo.OK
-        assert 0 < out.value <= 8 * 16384 * min(rows, 4096)
+        assert out.value <= 8 * 16384 * min(rows, 4096) and (out.value > 0) == (rows > 512)
 
 
 def lp_forward(bfo, **kw):
