@@ -275,10 +275,12 @@ struct RowResult {
 __device__ __forceinline__ RowResult rowResult(const Stat &a, float scale) {
     RowResult r;
     r.m = a.m, r.s = a.s, r.t = a.t;
-    r.empty = a.s == 0.0f;
-    r.finite = a.s - a.s == 0.0f;
+    // Scores are infinities where their product with the scale is one.
+    const float scaled = a.m * scale;
+    r.empty = a.s == 0.0f || (a.s > 0.0f && scaled == -INFINITY);
+    r.finite = a.s - a.s == 0.0f && scaled < INFINITY;
     r.logs = r.empty ? 0.0f : r.finite ? logf(a.s) : NAN;
-    r.scaled = r.empty ? -INFINITY : r.finite ? a.m * scale : NAN;
+    r.scaled = r.empty ? -INFINITY : r.finite ? scaled : NAN;
     return r;
 }
 // log probability of score x.

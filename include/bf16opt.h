@@ -566,7 +566,8 @@ int bfo_logits_workspace_bytes(uint64_t rows, uint32_t vocab, uint32_t top, uint
  * top <= BFO_TOP_MAX and <= vocab; top == 0 takes neither top array.
  * A negative target masks its row: logprob 0.  A target >= vocab is no token:
  * logprob NaN.  Scores of -inf have probability 0; a row of nothing else has
- * stats {-inf, 0}, entropy 0 and log probabilities -inf.  A row with a NaN or
+ * stats {-inf, 0}, entropy 0 and log probabilities -inf.  (Scores count as
+ * infinite where z overflows binary32.)  A row with a NaN or
  * +inf has NaN stats, entropy and log probabilities (top_index then orders NaN
  * first).  1 <= vocab <= BFO_VOCAB_MAX. */
 #define BFO_TOP_MAX 128u

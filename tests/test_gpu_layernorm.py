@@ -120,6 +120,38 @@ def test_forward_optional_arguments_strides_and_guards(bfo, dt):
     check_forward(x, w, b, 1e-5, out2, None, None)
 
 
+@pytest.mark.parametrize("rows,cols", [(20001, 520), (70003, 16), (9001, 2049)])
+def test_more_rows_than_workgroups(bfo, rows, cols):
+    x, d, w, b = inputs(rows, cols, torch.bfloat16, torch.bfloat16, 61)
+    out, mean, rstd = run_forward(bfo, x, w, b)
+    check_forward(x, w, b, 1e-5, out, mean, rstd)
+    check_backward(x, d, w, mean, rstd, *run_backward(bfo, x, d, w, mean, rstd))
+
+
+def test_rows_past_32_bit_offsets(bfo):
+    """The last rows of matrices whose element offsets pass 2^32."""
+    cols = 4096
+    rows = (1 << 32) // cols + 100
+    big = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x, d, w, b = inputs(100, cols, torch.bfloat16, torch.bfloat16, 62)
+    big[-100:] = x
+    out = torch.empty_like(big)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    bfo.layernorm_forward(big, w, b, out, mean, rstd)
+    check_forward(x, w, b, 1e-5, out[-100:], mean[-100:], rstd[-100:])
+    assert (out[:-100] == b).all() and (mean[:-100] == 0).all()
+    dout = torch.zeros_like(big)
+    dout[-100:] = d
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    bfo.layernorm_backward(dout, big, w, mean, rstd, out, dw, db,
+                           workspace=bfo.new_layernorm_workspace(rows, cols, DEV))
+    # rows of zero gradient add exact zeros, so the 100 rows are all there is
+    check_backward(x, d, w, mean[-100:], rstd[-100:], out[-100:], dw, db)
+    assert (out[:-100] == 0).all()
+    del big, out, dout
+    torch.cuda.empty_cache()
+
+
 def test_forward_far_offset_and_constant_rows(bfo):
     # The variance comes from differences from the mean, so a large common offset costs only the
     # mean's own rounding.

@@ -207,6 +207,27 @@ def test_masked_scores_nan_inf_and_odd_targets(bfo, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [100, 70000])
+def test_scores_whose_scaled_value_overflows(bfo, dt, V):
+    t = TYPES[dt]
+    low, high = float(torch.finfo(t).min), float(torch.finfo(t).max)
+    logits = torch.zeros(4, V, dtype=t, device=DEV)
+    logits[0] = low                                          # z = -inf throughout: an empty row
+    logits[1, 1:] = low                                      # z = 0 and -inf
+    logits[2, 5] = high                                      # z = +inf somewhere: NaN
+    targets = torch.tensor([1, 0, 5, 7], dtype=torch.int32, device=DEV)
+    out = run_forward(bfo, logits, targets, V, 2.0, 3)
+    assert out["stats"][0].tolist() == [-INF, 0.0] and out["logprob"][0] == -INF and out["entropy"][0] == 0
+    assert out["stats"][1].tolist() == [0.0, 0.0] and out["logprob"][1] == 0 and out["entropy"][1] == 0
+    assert out["stats"][2].isnan().all() and out["logprob"][2].isnan()
+    assert torch.equal(out["top_index"][:3].cpu(), torch.tensor([[0, 1, 2], [0, 1, 2], [5, 0, 1]], dtype=torch.int32))
+    d = torch.full_like(logits, NAN)
+    bfo.token_logprobs_backward(logits, targets, out["stats"], torch.ones(4, device=DEV), d, scale=2.0)
+    assert (d[0] == 0).all() and (d[1] == 0).all() and d[2].isnan().all()
+    near(d[3].double().sum(), torch.zeros((), device=DEV).double(), 0.02, "a row's gradients cancel")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_few_rows_of_a_long_vocabulary(bfo, dt):
     """Rows that are split over workgroups: NaN, +inf and -inf in one stretch of
     the vocabulary only, equal scores across the stretches, targets and teacher
