@@ -176,7 +176,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kLowest = -3.402823466e+38f;
 
 }  // namespace bfo

@@ -17,24 +17,36 @@ namespace {
 constexpr uint32_t kMaxGrid = 1u << 21;
 
 // ---------------------------------------------------------------------------
-// Running softmax statistics of raw (unscaled) scores x over some set:
-//   m = max x, s = sum 2^((x - m) k), t = sum 2^((x - m) k) (x - m),
-// with k = scale * log2(e).  The empty set is {lowest finite, 0, 0}; a set of
-// -inf only has s = 0; a NaN or +inf makes s NaN or infinite.
+// Softmax statistics of raw (unscaled) scores x over some set, with
+// k = scale * log2(e):
+//   m = max x, s = sum 2^(x k - M), t = sum 2^(x k - M) (x k - M).
+// While a row is read, M is m k rounded, so that an exponent is one fma; a
+// finished Stat has M = m k exactly.  The empty set is {lowest finite, 0, 0}; a
+// set of -inf only has s = 0; a NaN or +inf makes s NaN.
 // ---------------------------------------------------------------------------
 struct Stat {
     float m, s, t;
 };
 
-// The same set with its maximum taken as m >= a.m.
-__device__ __forceinline__ Stat raised(const Stat &a, float m, float k) {
-    const float d = a.m - m, r = exp2Fast(d * k);
-    return {m, a.s * r, r == 0.0f ? 0.0f : r * fmaf(a.s, d, a.t)};
+// The rounded M.  Its error is folded into the finished s and t, which needs it
+// to be small: rows with |m k| >= kReferenceMost are read again by exactStat.  A
+// lane that sees only far lower scores than that (masks of the type's lowest
+// value) has them count as 0 by the floor.
+constexpr float kReferenceMost = 1024.0f, kReferenceFloor = -2048.0f;
+__device__ __forceinline__ float referenceOf(float m, float k) { return fmaxf(m * k, kReferenceFloor); }
+
+// The set's s and t for an M that is `up` larger.
+__device__ __forceinline__ Stat raised(const Stat &a, float m, float up) {
+    const float r = exp2Fast(-up);
+    return {m, a.s * r, r == 0.0f ? 0.0f : r * fmaf(a.s, -up, a.t)};
+}
+__device__ __forceinline__ Stat raisedReference(const Stat &a, float m, float k) {
+    return raised(a, m, referenceOf(m, k) - referenceOf(a.m, k));
 }
 // The wavefront's statistics, in every lane.
 __device__ __forceinline__ Stat waveJoined(const Stat &a, float k) {
     const float m = waveMax(a.m);
-    const Stat b = raised(a, m, k);
+    const Stat b = raisedReference(a, m, k);
     return {m, laneSum<64>(b.s), laneSum<64>(b.t)};
 }
 
@@ -191,12 +203,13 @@ __device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint
                 m = top;
             }
         }
-        a = raised(a, m, k);
+        a = raisedReference(a, m, k);
+        const float reference = referenceOf(m, k);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
             for (int e = 0; e < int(E); ++e) {
-                const float d = v[u][e] - m, p = exp2Fast(d * k);
+                const float d = fmaf(v[u][e], k, -reference), p = exp2Fast(d);
                 a.s += p;
                 // p is 0 where d is -inf: their product has to be 0 too
                 if constexpr (kEntropy) a.t = fmaf(p, fmaxf(d, kLowest), a.t);
@@ -217,6 +230,55 @@ __device__ __forceinline__ uint32_t claimOne(uint32_t *counter) {
     uint32_t first = 0;
     if (before == 0) first = atomicAdd(counter, uint32_t(__popcll(active)));
     return uint32_t(__builtin_amdgcn_readfirstlane(int(first))) + before;
+}
+
+// The workgroup's wavefronts joined, in every lane; `stats` may be used again.
+template <int kBlock>
+__device__ __forceinline__ Stat blockJoined(const Stat &wave, Stat (&stats)[kBlock / 64], float k) {
+    if ((threadIdx.x & 63) == 0) stats[threadIdx.x >> 6] = wave;
+    __syncthreads();
+    Stat all = stats[0];
+#pragma unroll
+    for (int w = 1; w < kBlock / 64; ++w) all.m = fmaxf(all.m, stats[w].m);
+    all.s = all.t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kBlock / 64; ++w) {
+        const Stat b = raisedReference(stats[w], all.m, k);
+        all.s += b.s;
+        all.t += b.t;
+    }
+    return all;
+}
+
+// A finished Stat of a row with maximum m by differences from m, which are
+// exact where products with k are not: for the rows that referenceOf is not for.
+template <typename T, int kBlock>
+__device__ __noinline__ Stat exactStat(const T *row, uint32_t V, float m, float k, Stat (&stats)[kBlock / 64]) {
+    Stat a = {m, 0.0f, 0.0f};
+    for (uint32_t c = threadIdx.x; c < V; c += kBlock) {
+        const float d = (toFloat(row[c]) - m) * k, p = exp2Fast(d);
+        a.s += p;
+        a.t = fmaf(p, fmaxf(d, kLowest), a.t);
+    }
+    a.s = laneSum<64>(a.s);
+    a.t = laneSum<64>(a.t);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) stats[threadIdx.x >> 6] = a;
+    __syncthreads();
+    a.s = a.t = 0.0f;
+    for (int w = 0; w < kBlock / 64; ++w) {
+        a.s += stats[w].s;
+        a.t += stats[w].t;
+    }
+    return a;
+}
+
+template <typename T, int kBlock>
+__device__ __forceinline__ Stat finished(const Stat &a, const T *row, uint32_t V, float k,
+                                         Stat (&stats)[kBlock / 64]) {
+    if (a.s == 0.0f || !(fabsf(a.m * k) < kReferenceMost)) return exactStat<T, kBlock>(row, V, a.m, k, stats);
+    // M's rounding error, an exact difference of less than 2^-13
+    return raised(a, a.m, fmaf(a.m, k, -referenceOf(a.m, k)));
 }
 
 // The candidates of the row's top: every score that reaches the bound.  False
@@ -399,7 +461,7 @@ struct RowEnd {
                 a.logprob[r] = target < 0            ? 0.0f
                                : uint32_t(target) >= V ? NAN
                                                        : logProb(res, targetScore, a.scale);
-            if (entropy) a.entropy[r] = res.empty ? 0.0f : res.finite ? res.logs - a.scale * res.t / res.s : NAN;
+            if (entropy) a.entropy[r] = res.empty ? 0.0f : res.finite ? res.logs - kLn2 * (res.t / res.s) : NAN;
         }
         if constexpr (kTeacher) {
             if (threadIdx.x < 64) {
@@ -424,9 +486,8 @@ struct RowEnd {
 // logitsJoinKernel.
 template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop, bool kTeacher, bool kSplit>
 __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, uint32_t perSlot, Segments seg) {
-    constexpr int kWaves = kBlock / 64;
     constexpr uint32_t E = chunkElems<T>();
-    __shared__ Stat stats[kWaves];
+    __shared__ Stat stats[kBlock / 64];
     __shared__ std::conditional_t<kTop, TopShared<kBlock>, Empty> sh;
     const uint32_t first = kSplit ? blockIdx.y * seg.length : 0;  // the segment's columns: V from `first` on
     const uint32_t V = kSplit ? min(seg.length, a.vocab - first) : a.vocab;
@@ -439,7 +500,6 @@ __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, u
         if constexpr (kTop) slotMax = sh.slotMax;
         const Stat mine = laneStat<T, kBlock, kNontemporal, kEntropy, kTop>(row, V, k, perSlot, slotMax);
         const Stat wave = waveJoined(mine, k);
-        if ((threadIdx.x & 63) == 0) stats[threadIdx.x >> 6] = wave;
         if constexpr (kTop) {
             // Lanes without scores hold key 0; one whose maximum may be -inf holds that key.
             const int c = int(threadIdx.x * E) - leadOf(row);  // its first chunk, whole or not, or its second
@@ -449,17 +509,7 @@ __global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, u
             for (int d = 1; d < kBlock / kGroups; d *= 2) key = max(key, uint32_t(__shfl_xor(int(key), d, 64)));
             if (threadIdx.x % (kBlock / kGroups) == 0) sh.groupKey[threadIdx.x / (kBlock / kGroups)] = key;
         }
-        __syncthreads();
-        Stat all = stats[0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) all.m = fmaxf(all.m, stats[w].m);
-        all.s = all.t = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const Stat b = raised(stats[w], all.m, k);
-            all.s += b.s;
-            all.t += b.t;
-        }
+        const Stat all = finished<T, kBlock>(blockJoined<kBlock>(wave, stats, k), row, V, k, stats);
         // The last wavefront writes the row's results while the first one looks for
         // the bound of its top.
         const RowResult res = rowResult(all, a.scale);
@@ -503,7 +553,12 @@ __global__ __launch_bounds__(kJoinBlock) void logitsJoinKernel(LogitsForward a, 
     for (uint32_t i = threadIdx.x; i < count; i += kJoinBlock) keys[i] = seg.keys(a)[r * count + i];
     const uint32_t lane = threadIdx.x & 63;
     const float4 part = lane < seg.count ? seg.stats(a)[r * seg.count + lane] : float4{kLowest, 0.0f, 0.0f, 0.0f};
-    const RowResult res = rowResult(waveJoined({part.x, part.y, part.z}, k), a.scale);
+    // finished statistics: M is m k exactly
+    Stat all = {waveMax(part.x), 0.0f, 0.0f};
+    const Stat mine = raised({part.x, part.y, part.z}, all.m, (all.m - part.x) * k);
+    all.s = laneSum<64>(mine.s);
+    all.t = laneSum<64>(mine.t);
+    const RowResult res = rowResult(all, a.scale);
     end.write(a, r, res, a.entropy != nullptr, kJoinBlock - 64);
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < count; i += kJoinBlock) {
