@@ -483,9 +483,10 @@ struct RowEnd {
 
 // One workgroup per row, or (kSplit) per segment of a row: then the results are
 // the segment's statistics and the keys of its top, in the workspace, for
-// logitsJoinKernel.
+// logitsJoinKernel.  With a top, 72 registers are enough for seven wavefronts a
+// SIMD (odd rows 152 -> 147 us against the compiler's choice; eight lose 4%).
 template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop, bool kTeacher, bool kSplit>
-__global__ __launch_bounds__(kBlock) void logitsForwardKernel(LogitsForward a, uint32_t perSlot, Segments seg) {
+__global__ __launch_bounds__(kBlock, kTop ? 7 : 1) void logitsForwardKernel(LogitsForward a, uint32_t perSlot, Segments seg) {
     constexpr uint32_t E = chunkElems<T>();
     __shared__ Stat stats[kBlock / 64];
     __shared__ std::conditional_t<kTop, TopShared<kBlock>, Empty> sh;
