@@ -192,15 +192,16 @@ __device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint
         float m = a.m;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            float top = kTop ? fmaxf(v[u][0], v[u][1]) : m;
-#pragma unroll
-            for (int e = kTop ? 2 : 0; e < int(E); e += 2) top = max3(top, v[u][e], v[u][e + 1]);
             if constexpr (kTop) {
-                stretch = fmaxf(stretch, top);
+                float top = max3(v[u][0], v[u][1], v[u][2]);
+#pragma unroll
+                for (int e = 3; e < int(E) - 1; e += 2) top = max3(top, v[u][e], v[u][e + 1]);
+                stretch = max3(stretch, top, v[u][E - 1]);
+                m = max3(m, stretch, stretch);  // the stretch's earlier scores are in m already
                 if (++held == perSlot) endStretch();
-                m = fmaxf(m, top);
             } else {
-                m = top;
+#pragma unroll
+                for (int e = 0; e < int(E); e += 2) m = max3(m, v[u][e], v[u][e + 1]);
             }
         }
         a = raisedReference(a, m, k);
@@ -594,7 +595,7 @@ constexpr uint32_t backSegment() {
 // order, so that equal indexes add in a fixed order.
 struct Chains {
     static constexpr uint32_t kNone = 0xFF;
-    uint8_t head[kBackBlock * kBackChunks];
+    alignas(4) uint8_t head[kBackBlock * kBackChunks];
     uint8_t next[BFO_TOP_MAX];
     uint32_t column[BFO_TOP_MAX];  // within the segment
     float value[BFO_TOP_MAX];
@@ -683,7 +684,8 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
         }
         if constexpr (kTeacher) {
             if (live) {
-                reinterpret_cast<uint32_t *>(ch.head)[threadIdx.x] = 0xFFFFFFFFu;
+                for (uint32_t i = threadIdx.x; i < sizeof(ch.head) / 4; i += kBackBlock)
+                    reinterpret_cast<uint32_t *>(ch.head)[i] = 0xFFFFFFFFu;
                 Teacher te;
                 if (threadIdx.x < 64) {
                     te.load(a.teacherIndex + r * a.count, a.teacherLogits + r * a.count, a.count);
