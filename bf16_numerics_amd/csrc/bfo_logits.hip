@@ -2,10 +2,17 @@
 // probabilities with entropy and top alternatives, distillation from a
 // teacher's top logits, and their gradients.
 //
-// Forward: one workgroup per row, one pass over the row with a running
-// maximum, sum of exponentials and sum of their products with the score
-// (for the entropy) per lane, joined at the end.  Backward: one pass that
-// forms every probability again from the row's maximum and log sum.
+// Forward: one workgroup per row (or per segment of a long one, when there are
+// few; a second launch joins those), one pass over the row with a running
+// maximum, sum of exponentials and sum of their products with the score (for the
+// entropy) per lane, joined at the end.  The best scores are picked from the
+// chunks whose kept maximum reaches a bound that at least K scores reach.
+// Backward: one pass that forms every probability again from the row's maximum
+// and log sum.
+//
+// On an MI355X, bf16: 8192 x 50257 scores forward in 124 us (6.6 TB/s, bound by
+// memory), in 143 with entropy and 20 alternatives (bound by the vector ALUs, 85%
+// busy), gradient of 8192 x 50304 in 262 us (6.0 TB/s read and written).
 #include <type_traits>
 
 #include "bfo_device.hpp"
@@ -745,9 +752,9 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
 
 // Few rows of many scores are split, to at most one workgroup a CU and at least
 // 16,384 scores a segment; one workgroup reads its row at little more than 20
-// GB/s.  One row of 262,144 bf16 scores 16.4 -> 5.5 us, with entropy and 20
-// alternatives 24.6 -> 12.6; 64 rows of 131,072 16.7 -> 13.6.  At 50,257 scores
-// the second launch costs what the split gains (9.3 -> 10.3), and above 8
+// GB/s.  One row of 262,144 bf16 scores 15.3 -> 5.6 us, with entropy and 20
+// alternatives 22.8 -> 13.0; so 64 rows of 131,072 16.5 -> 14.7.  At 50,257
+// scores the second launch costs what the split gains (9.3 -> 10.3), and above 8
 // segments joining their tops costs more again (20 us with 16).  A last segment
 // still holds more than BFO_TOP_MAX scores.
 Segments segmentsOf(uint64_t rows, uint32_t vocab) {
@@ -785,13 +792,13 @@ hipError_t forwardKind(const LogitsForward &a, Segments seg, hipStream_t stream)
 }
 
 // Where every CU has a few rows, small workgroups let the ends of some rows hide
-// behind the passes of others: 8192 x 50257 bf16 with 20 alternatives 166 us
-// with 256 lanes, 185 with 512, 405 with 1024 (whose registers leave one row a
-// CU).  With few rows a row's own pass counts: 64 x 131072 23 us with 256 lanes,
-// 17 with 512; 512 x 32000 14 with both.  Scores of over 64 MB are loaded
-// nontemporally: 8192 x 50257 bf16 147 -> 136 us, fp32 4096 x 50257 139 -> 123,
-// 2048 x 32000 bf16 25 -> 23; below that it gave nothing, and up to 4% away where
-// the caches still held them.
+// behind the passes of others: 8192 x 50257 bf16 with 20 alternatives 151 us
+// with 256 lanes, 186 with 512, without 125 and 134.  With few rows a row's own
+// pass counts: 64 x 50257 with 20 alternatives 13.0 us with 256 lanes, 10.6 with
+// 512, one row 12.3 and 9.9; 512 x 32000 13.7 and 13.8.  Scores of over 64 MB are
+// loaded nontemporally: 8192 x 50257 bf16 141 -> 125 us, fp32 4096 x 50257 138 ->
+// 121, 2048 x 32000 bf16 25.5 -> 23.0; below that it gave nothing, and took up to
+// 4% where the caches still held them.
 template <typename T>
 hipError_t forward(const LogitsForward &a, hipStream_t stream) {
     const Segments seg = segmentsOf(a.rows, a.vocab);
