@@ -662,8 +662,8 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
         T *out = static_cast<T *>(a.dlogits.p) + r * a.dlogits.stride;
         // the segment's columns are those of [c0, end) that are not negative
         const int c0 = int(blockIdx.x * segment) - leadOf(out), end = min(c0 + int(segment), int(a.width));
-        const float m = a.stats[2 * r], logs = a.stats[2 * r + 1];
-        // dlogits = scale * (p * (base + slope * log p) + what its tokens get)
+        const float m = a.stats[2 * r], logs2 = a.stats[2 * r + 1] * kLog2e;
+        // dlogits = scale * (p * (base + slope * log2 p) + what its tokens get)
         int target = -1;
         float hard = 0.0f, base = 0.0f, slope = 0.0f, dkl = 0.0f;
         if (a.targets) {
@@ -675,7 +675,7 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
         }
         if constexpr (kEntropy) {
             const float de = a.dentropy[r];
-            slope = -de;
+            slope = -de * kLn2;
             if (de != 0.0f) base -= de * a.entropy[r];
         }
         if constexpr (kTeacher) dkl = a.dkl[r];
@@ -712,9 +712,11 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
             if (live) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    // columns outside the vocabulary hold -inf, so p = 0 there
-                    const float lp = fmaf(v[k][e], a.scale, -m) - logs;
-                    const float p = exp2Fast(lp * kLog2e);
+                    // z is rounded before m, itself a rounded z, is taken from it:
+                    // the largest z leaves 0, however large.  Columns outside the
+                    // vocabulary hold -inf, so p = 0 there.
+                    const float z = v[k][e] * a.scale, lp = fmaf(z - m, kLog2e, -logs2);  // log2 p
+                    const float p = exp2Fast(lp);
                     // p is 0 well above -1e4, where the product has to be 0 too
                     y[e] = p * (kEntropy ? fmaf(slope, fmaxf(lp, -1e4f), base) : base);
                 }

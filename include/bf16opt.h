@@ -577,7 +577,8 @@ int token_logprobs_forward(const void *logits, uint64_t stride, uint64_t rows, u
                            uint32_t top, int32_t *top_index, float *top_logprob, void *workspace, void *stream);
 
 /* Gradient of sum(dlogprob * logprob + dentropy * entropy) with respect to the
- * logits, from the forward pass's stats and entropy.  With p = exp(z - M - log S):
+ * logits, from the forward pass's stats and entropy.  With p = exp(z - M - log S),
+ * z rounded to binary32 first:
  *   dlogits[j] = scale * (dlogprob * ([j == target] - p[j])
  *                         - dentropy * p[j] * (log p[j] + entropy))   j < vocab
  *   dlogits[j] = 0                                                    vocab <= j < width

@@ -8,8 +8,12 @@ rescalings (each of at most 4 u), the exponential of a distance d costs
   log sum:   rel = (n + 4 E|d| + 8) u  absolute
   log prob:  rel + (3 |d| + 4) u
   entropy:   rel + E(|d| (4 |d| + n + 8)) u + E|d| rel + (2 + H) 2 u.
-Gradients are compared with the formula on the very stats they are given: a
-probability is off by (6 |log p| + |z| + 12) u relative.
+Gradients are compared with the formula on the very stats they are given and
+on z as they take it, rounded to binary32.  With d = z - M, |log p| = |d| + log S:
+the roundings of d, of log2(e) (half a u) and of log S * log2(e) and the final
+fma's leave log p within 4 |log p| u, the exponential adds 2 u, so that a
+probability is off by (6 |log p| + 12) u relative and, where log p itself is a
+factor, by 4 |log p| u more.
 """
 import math
 
@@ -311,18 +315,17 @@ def test_forward_outputs_are_optional(bfo):
 def gradient_reference(logits, V, scale, stats, base, slope, ent, sparse):
     """scale * (p * (base + slope * (log p + ent)) + sparse) and its tolerance,
     from the given stats."""
+    z = (logits[:, :V].float() * torch.tensor(scale, device=DEV)).double()
     scale = single(scale)
-    z = logits[:, :V].double() * scale
     s = stats.double()
     logp = z - s[:, :1] - s[:, 1:]
     p = logp.exp()
     lp = torch.where(p > 0, logp, 0.0)
-    z = torch.where(p > 0, z, 0.0)
     b, k, h = base.double()[:, None], slope.double()[:, None], ent.double()[:, None]
     dense = p * (b + k * (lp + h))
     ref = scale * (dense + sparse)
     size = p * (b.abs() + k.abs() * (lp.abs() + h.abs()))
-    tol = scale * (size * (6 * lp.abs() + z.abs() + 16) * U + 4 * U * (size + sparse.abs())) + 2 * U * ref.abs()
+    tol = scale * (size * (6 * lp.abs() + 16) * U + 4 * U * (size + sparse.abs())) + 2 * U * ref.abs()
     return ref, tol
 
 
@@ -352,6 +355,51 @@ def test_logprob_gradient(bfo, dt, with_entropy, with_targets):
         sparse = torch.zeros(rows, V, dtype=torch.float64, device=DEV)
         sparse.scatter_(1, targets.clamp(min=0).long()[:, None], hard.double()[:, None])
         check_gradient(d, V, *gradient_reference(logits, V, scale, out["stats"], -hard, -den, out["entropy"], sparse))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1.0, 0.7, 0.3])
+def test_gradient_of_scores_far_from_zero(bfo, dt, scale):
+    """Rows around large offsets and rows masked by the type's lowest value, in
+    part and throughout, whose scaled scores are rounded to binary32 before
+    anything is subtracted: p = exp(z - M - log S) of those is off by
+    (6 |log p| + 16) u whatever z is."""
+    V, t = 1003, TYPES[dt]
+    low = float(torch.finfo(t).min)
+    rows = []
+    for offset in (0.0, 700.0, -700.0, 1e4, -1e6, 1e10, -1e30):
+        logits, _ = scores(1, V, "f32", 21)
+        rows.append((logits + offset).to(t))
+    rows += [torch.full((1, V), low, dtype=t, device=DEV), rows[0].clone()]
+    rows[-1][:, ::3] = low
+    logits = torch.cat(rows)
+    R = logits.shape[0]
+    targets = torch.arange(R, dtype=torch.int32, device=DEV) * 7 + 1
+    out = run_forward(bfo, logits, targets, V, scale)
+    z = (logits.float() * torch.tensor(scale, device=DEV)).double()
+    stats = out["stats"].double()
+    assert torch.equal(stats[:, 0], z.max(1).values)
+    assert abs(float(stats[-2, 1]) - math.log(V)) <= (V / 64 + 72) * U
+    lp = z - stats[:, :1] - stats[:, 1:]
+    p = lp.exp()
+    lp = torch.where(p > 0, lp, 0.0)
+    one = torch.zeros(R, V, dtype=torch.float64, device=DEV)
+    one.scatter_(1, targets.long()[:, None], 1.0)
+    a, b = torch.full((R,), -0.75, device=DEV), torch.full((R,), 0.5, device=DEV)
+    h = out["entropy"].double()[:, None]
+    size = p * (0.75 + 0.5 * (lp.abs() + h.abs()))
+    d = torch.full_like(logits, NAN)
+    bfo.token_logprobs_backward(logits, targets, out["stats"], a, d, entropy=out["entropy"], dentropy=b, scale=scale)
+    tol = single(scale) * size * (6 * lp.abs() + 24) * U + 4 * U * one
+    check_gradient(d, V, single(scale) * (-0.75 * (one - p) - 0.5 * p * (lp + h)), tol, "with entropy")
+    index, value = teacher(R, V, 9, 22)
+    q, _, live, spread = teacher_reference(index, value, scale)
+    d = torch.full_like(logits, NAN)
+    bfo.distill_backward(logits, index, value, out["stats"], b, d, scale=scale)
+    part = torch.zeros_like(one).scatter_add_(1, index.clamp(min=0).long(), q)
+    off = torch.zeros_like(one).scatter_add_(1, index.clamp(min=0).long(), q * (4 * spread + 88) * U)
+    half = 0.5 * live[:, None]
+    check_gradient(d, V, single(scale) * half * (p - part), half * (p * (6 * lp.abs() + 24) * U + off), "distill")
 
 
 def test_logprob_gradient_in_place_and_strided(bfo):
