@@ -709,7 +709,7 @@ def _workspace_ptr(workspace, need, dev, maker):
         if need:
             raise ValueError(f"workspace must be {maker}(...)")
         return None
-    if workspace.device != dev or not workspace.is_contiguous() or \
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be {maker}(...) for these sizes")
     return workspace.data_ptr()
@@ -750,8 +750,8 @@ def new_layernorm_workspace(rows, cols, device):
 def layernorm_forward(x, weight, bias, out, mean=None, rstd=None, eps=1e-5):
     """out = (x - mean) * rstd * weight + bias per row of x (bias may be None).
     mean, rstd: float32 tensors of x's rows for the backward pass, or None."""
-    dev = x.device
     xp, xs, rows, cols = _matrix(x, "x")
+    dev = x.device
     op, os_ = _matrix_like(out, "out", x.dtype, dev, rows, cols)
     pt = _param_type(weight)
     _launch("layernorm_forward", dev, xp, xs, _vector(weight, pt, cols, "weight", dev),
@@ -764,8 +764,8 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, wor
     """Gradients of layernorm_forward into dx, dweight and dbias (None: not
     wanted).  accumulate_*: add to what they hold.  workspace:
     new_layernorm_workspace(rows, cols, device)."""
-    dev = x.device
     xp, xs, rows, cols = _matrix(x, "x")
+    dev = x.device
     gp, gs = _matrix_like(dout, "dout", x.dtype, dev, rows, cols)
     dp, ds = _matrix_like(dx, "dx", x.dtype, dev, rows, cols)
     pt = _param_type(weight)
@@ -800,6 +800,15 @@ def _vocab(vocab, cols):
     return vocab
 
 
+def _columns(t, name, rows):
+    """The number of columns of a matrix of `rows` rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must have a row of its own for each row of logits")
+    return t.shape[1]
+
+
 def token_logprobs_forward(logits, targets=None, logprob=None, stats=None, entropy=None, top_index=None,
                            top_logprob=None, vocab=None, scale=1.0, workspace=None):
     """Log probabilities of `targets` (int32, negative: masked) under
@@ -807,14 +816,12 @@ def token_logprobs_forward(logits, targets=None, logprob=None, stats=None, entro
     largest scaled score and the log of the sum of exponentials above it),
     entropy, and the top_index.shape[1] best tokens.  Every output but the ones
     wanted may be None."""
-    dev = logits.device
     lp, ls, rows, cols = _matrix(logits, "logits")
+    dev = logits.device
     v = _vocab(vocab, cols)
     top = 0
     if top_index is not None:
-        if top_index.dim() != 2 or top_index.shape[0] != rows:
-            raise ValueError("top_index must have a row of its own for each row of logits")
-        top = top_index.shape[1]
+        top = _columns(top_index, "top_index", rows)
     ws = _workspace_ptr(workspace, logits_workspace_bytes(rows, v, top), dev, "new_logits_workspace")
     _launch("token_logprobs_forward", dev, lp, ls, rows, v, _DTYPE_CODES[logits.dtype], scale,
             _vector(targets, torch.int32, rows, "targets", dev), _vector(logprob, torch.float32, rows, "logprob", dev),
@@ -829,8 +836,8 @@ def token_logprobs_backward(logits, targets, stats, dlogprob, dlogits, entropy=N
     """Gradient of sum(dlogprob * logprob + dentropy * entropy) into dlogits
     (the logits' shape; may be the logits), from the forward pass's stats and
     entropy; columns from vocab on get 0.  targets and dlogprob may both be None."""
-    dev = logits.device
     lp, ls, rows, cols = _matrix(logits, "logits")
+    dev = logits.device
     dp, ds = _matrix_like(dlogits, "dlogits", logits.dtype, dev, rows, cols)
     _launch("token_logprobs_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols, _DTYPE_CODES[logits.dtype], scale,
             _vector(targets, torch.int32, rows, "targets", dev),
@@ -841,9 +848,7 @@ def token_logprobs_backward(logits, targets, stats, dlogprob, dlogits, entropy=N
 
 
 def _teacher(teacher_index, teacher_logits, rows, dev):
-    if teacher_index.dim() != 2 or teacher_index.shape[0] != rows:
-        raise ValueError("teacher_index must have a row of its own for each row of logits")
-    count = teacher_index.shape[1]
+    count = _columns(teacher_index, "teacher_index", rows)
     return (_vector(teacher_index, torch.int32, rows * count, "teacher_index", dev),
             _vector(teacher_logits, torch.float32, rows * count, "teacher_logits", dev), count)
 
@@ -854,8 +859,8 @@ def distill_forward(logits, teacher_index, teacher_logits, kl, stats=None, targe
     int32 indexes, negative: no entry, and float32 logits) from the student's
     softmax(scale * logits[:, :vocab]), per row into kl; targets and logprob
     as in token_logprobs_forward."""
-    dev = logits.device
     lp, ls, rows, cols = _matrix(logits, "logits")
+    dev = logits.device
     v = _vocab(vocab, cols)
     ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
     ws = _workspace_ptr(workspace, logits_workspace_bytes(rows, v, 0), dev, "new_logits_workspace")
@@ -869,8 +874,8 @@ def distill_backward(logits, teacher_index, teacher_logits, stats, dkl, dlogits,
                      vocab=None, scale=1.0):
     """Gradient of sum(dkl * kl + dlogprob * logprob) into dlogits (the logits'
     shape; may be the logits); columns from vocab on get 0."""
-    dev = logits.device
     lp, ls, rows, cols = _matrix(logits, "logits")
+    dev = logits.device
     dp, ds = _matrix_like(dlogits, "dlogits", logits.dtype, dev, rows, cols)
     ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
     _launch("distill_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols, _DTYPE_CODES[logits.dtype], scale, ti,

@@ -618,8 +618,9 @@ __device__ __forceinline__ void buildChains(Chains &ch, const Teacher &te, float
     const uint64_t below = (1ull << lane) - 1;
     const bool bad = __ballot((te.id[0] >= 0 && uint32_t(te.id[0]) >= vocab) ||
                               (te.id[1] >= 0 && uint32_t(te.id[1]) >= vocab)) != 0;
-    const bool in0 = te.id[0] >= 0 && te.id[0] >= c0 && te.id[0] < c1;
-    const bool in1 = te.id[1] >= 0 && te.id[1] >= c0 && te.id[1] < c1;
+    // (without a probability, dkl counts as 0 whatever it is)
+    const bool in0 = te.any && te.id[0] >= 0 && te.id[0] >= c0 && te.id[0] < c1;
+    const bool in1 = te.any && te.id[1] >= 0 && te.id[1] >= c0 && te.id[1] < c1;
     const uint64_t m0 = __ballot(in0), m1 = __ballot(in1);
     const uint32_t n0 = uint32_t(__popcll(m0)), n = n0 + uint32_t(__popcll(m1));
     if (in0) {

@@ -217,7 +217,7 @@ def test_scores_far_from_zero_and_far_apart(bfo, V, rows):
     g = gen(V)
     base = 3 * torch.empty(rows, V, device=DEV).normal_(generator=g)
     targets = torch.randint(0, V, (rows,), generator=g, device=DEV).to(torch.int32)
-    for scale in (1.0, 0.25):
+    for scale in (1.0, 0.25, 0.7):
         for offset in (0.0, 700.0, -700.0, 712.0, 3000.0, -3000.0, 1e6, -1e6, 1e30):
             logits = base + offset
             check_forward(run_forward(bfo, logits, targets, V, scale, 20), logits, targets, V, scale, 20)
@@ -536,6 +536,24 @@ def test_distill_odd_entries(bfo):
         assert torch.equal(torch.nan_to_num(d, 9.0), torch.nan_to_num(again, 9.0))
 
 
+def test_factor_of_a_row_without_entries_counts_as_zero(bfo):
+    """Whatever it is, and also where the true token's factor is not zero."""
+    V = 2003
+    logits, _ = scores(3, V, "f32", 14)
+    targets = torch.tensor([5, 5, -1], dtype=torch.int32, device=DEV)
+    index = torch.arange(6, dtype=torch.int32, device=DEV).repeat(3, 1)
+    index[0] = -1
+    value = torch.full((3, 6), -INF, device=DEV)
+    _, stats, _ = run_distill(bfo, logits, index, value, V, 1.0)
+    factor = torch.full((3,), 0.5, device=DEV)
+    plain, d = torch.full_like(logits, NAN), torch.full_like(logits, NAN)
+    bfo.token_logprobs_backward(logits, targets, stats, factor, plain)
+    for dkl in (0.25, INF, NAN):
+        bfo.distill_backward(logits, index, value, stats, torch.full((3,), dkl, device=DEV), d, targets=targets,
+                             dlogprob=factor)
+        assert torch.equal(d, plain), dkl
+
+
 def test_teacher_side_feeds_the_student_side(bfo):
     """A teacher's top log probabilities serve as its logits."""
     V, K = 4001, 20
@@ -653,6 +671,10 @@ def test_binding_refusals(bfo):
                                    top_logprob=torch.empty(4, 2, device=DEV))
     with pytest.raises(ValueError, match="shape"):
         bfo.token_logprobs_backward(logits, targets, torch.empty(4, 2, device=DEV), f, logits[:, :99])
+    with pytest.raises(TypeError, match="teacher_index must be a torch.Tensor"):
+        bfo.distill_forward(logits, None, f, f)
+    with pytest.raises(ValueError, match="workspace must be"):
+        bfo.token_logprobs_forward(logits, targets, f, workspace=16)
     index = torch.zeros(4, 0, dtype=torch.int32, device=DEV)
     with pytest.raises(bfo.BfoError):
         bfo.distill_forward(logits, index, torch.empty(4, 0, device=DEV), f)

@@ -202,6 +202,11 @@ def test_binding_names_what_is_wrong(bfo):
         bfo.layernorm_forward(torch.zeros(8, 4, dtype=torch.bfloat16).t(), w, w, x)
     with pytest.raises(ValueError, match="expected a GPU"):
         bfo.token_logprobs_forward(x)
+    for call in (lambda: bfo.layernorm_forward(None, w, w, x), lambda: bfo.token_logprobs_forward(None),
+                 lambda: bfo.layernorm_backward(x.tolist(), None, w, w, w, x, w),
+                 lambda: bfo.distill_backward(None, None, None, None, None, x)):
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            call()
     with pytest.raises(ValueError, match="expected a GPU"):
         bfo.distill_forward(x, None, None, None)
     with pytest.raises(bfo.BfoError):
