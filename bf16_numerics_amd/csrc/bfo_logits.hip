@@ -189,7 +189,11 @@ __device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint
     };
     const int lead = leadOf(row), end = int(V) + lead, c = int(threadIdx.x * E);  // columns from the row's line on
     const T *line = row - lead;
-    for (int c0 = 0; c0 + c < end; c0 += kBlock * E * kUnroll) {
+    // The wavefront has scores in the chunks that start before waveEnd; in its
+    // last step it passes over the others.
+    const int waveEnd = end - int(__builtin_amdgcn_readfirstlane(int(threadIdx.x & ~63u)) * E);
+    auto step = [&](int c0, auto last) {
+        auto gone = [&](int u) { return decltype(last)::value && c0 + int(kBlock * E) * u >= waveEnd; };
         Chunk<T, E> v[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -199,6 +203,7 @@ __device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint
         float m = a.m;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
+            if (gone(u)) continue;
             if constexpr (kTop) {
                 float top = max3(v[u][0], v[u][1], v[u][2]);
 #pragma unroll
@@ -214,7 +219,8 @@ __device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint
         a = raisedReference(a, m, k);
         const float reference = referenceOf(m, k);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int u = 0; u < kUnroll; ++u) {
+            if (gone(u)) continue;
 #pragma unroll
             for (int e = 0; e < int(E); ++e) {
                 const float d = fmaf(v[u][e], k, -reference), p = exp2Fast(d);
@@ -222,7 +228,12 @@ __device__ __forceinline__ Stat laneStat(const T *row, uint32_t V, float k, uint
                 // p is 0 where d is -inf: their product has to be 0 too
                 if constexpr (kEntropy) a.t = fmaf(p, fmaxf(d, kLowest), a.t);
             }
-    }
+        }
+    };
+    constexpr int kStep = int(kBlock * E) * kUnroll;
+    int c0 = 0;
+    for (; c0 + kStep - int(kBlock * E) < waveEnd; c0 += kStep) step(c0, std::false_type{});
+    if (c0 < waveEnd) step(c0, std::true_type{});
     if constexpr (kTop) {
         if (held) endStretch();
         for (; slot < uint32_t(kSlots); ++slot) slotMax[slot * kBlock + threadIdx.x] = uint16_t(kNoScores);
