@@ -11,7 +11,7 @@
 // and log sum.
 //
 // On an MI355X, bf16: 8192 x 50257 scores forward in 124 us (6.6 TB/s, bound by
-// memory), in 143 with entropy and 20 alternatives (bound by the vector ALUs, 85%
+// memory), in 142 with entropy and 20 alternatives (bound by the vector ALUs, 85%
 // busy), gradient of 8192 x 50304 in 262 us (6.0 TB/s read and written).
 #include <type_traits>
 
@@ -503,9 +503,11 @@ struct RowEnd {
 // One workgroup per row, or (kSplit) per segment of a row: then the results are
 // the segment's statistics and the keys of its top, in the workspace, for
 // logitsJoinKernel.  With a top, 72 registers are enough for seven wavefronts a
-// SIMD (odd rows 152 -> 147 us against the compiler's choice; eight lose 4%).
+// SIMD (odd rows 152 -> 147 us against the compiler's choice; eight lose 4%), but
+// with 512 lanes, where two rows a CU are the most, they spill (512 x 32000 13.9
+// against 14.6).
 template <typename T, int kBlock, bool kNontemporal, bool kEntropy, bool kTop, bool kTeacher, bool kSplit>
-__global__ __launch_bounds__(kBlock, kTop ? 7 : 1) void logitsForwardKernel(LogitsForward a, uint32_t perSlot, Segments seg) {
+__global__ __launch_bounds__(kBlock, kTop ? (kBlock > 256 ? 4 : 7) : 1) void logitsForwardKernel(LogitsForward a, uint32_t perSlot, Segments seg) {
     constexpr uint32_t E = chunkElems<T>();
     __shared__ Stat stats[kBlock / 64];
     __shared__ std::conditional_t<kTop, TopShared<kBlock>, Empty> sh;
