@@ -232,11 +232,10 @@ __global__ __launch_bounds__(kBlock) void lnBackwardKernel(LayerNormBackward a) 
 }
 
 // Few rows, in one launch and without partials: mean and rstd are given, so
-// dweight and dbias need nothing of dx.  The first workgroups sum 32 columns
-// each over all rows (8 lanes a row, kBlock / 8 rows at a time), the others
-// form dx; both read x and dout, which the caches hold.
-constexpr int kSlabCols = 32;
-template <typename T, typename W, int kLanes, int kChunks, int kBlock>
+// dweight and dbias need nothing of dx.  The first workgroups sum kSlabCols
+// columns each over all rows (4 columns a lane), the others form dx; both read x
+// and dout, which the caches hold.
+template <typename T, typename W, int kLanes, int kChunks, int kBlock, int kSlabCols>
 __global__ __launch_bounds__(kBlock) void lnBackwardFewKernel(LayerNormBackward a, uint32_t slabs) {
     constexpr int kRows = kBlock / kLanes;
     constexpr int N = 4, kRowLanes = kSlabCols / N, kGroups = kBlock / kRowLanes, kAtOnce = 4;
@@ -348,11 +347,15 @@ struct BackwardShape {
     static constexpr int kRows = kBlock / kLanes;
 };
 
-// Up to here one launch for all gradients is faster than rows and partials: 512
-// rows of 1,600 bf16 5.2 us against 8.9, 256 rows of 4,096 3.6 against 11.1, one
-// row 2.7 against 5.0.  With 1,024 rows it is even (10.0), with 2,048 slower
-// (18.8 against 11.4): a column workgroup walks all rows by itself.
-constexpr uint64_t kFewRows = 512;
+// Up to here one launch for all gradients is faster than rows and partials: 1,024
+// rows of 1,600 bf16 7.6 us against 9.9, of 768 6.2 against 8.2, 512 rows of 4,096
+// 6.8 against 12, one row 2.7 against 5.0.  2,048 rows of 1,600 are slower (13.4
+// against 11.2), and so are 1,024 of 8,192 (22.0 against 19.4): a column workgroup
+// walks all rows by itself.  Slabs of 16 columns make it walk twice as many at a
+// time (32: 1,024 rows of 1,600 10.0 us); of wide rows they are too many workgroups
+// for that (512 rows of 4,096 8.1 us with 16, 6.8 with 32).
+constexpr uint32_t kNarrow = 2048;
+uint64_t fewRows(uint32_t cols) { return cols <= kNarrow ? 1024 : 512; }
 
 template <typename F>
 auto byWidth(uint32_t cols, F f) {
@@ -383,7 +386,7 @@ hipError_t byTypes(int dtype, int paramDtype, F f) {
 // CU has registers for one workgroup (4096 x 8192 bf16: 50 us against 55 with
 // 512, whose partials are twice as many).
 uint32_t lnBackwardBlocks(uint64_t rows, uint32_t cols) {
-    if (rows <= kFewRows) return 0;
+    if (rows <= fewRows(cols)) return 0;
     const int perBlock = byWidth(cols, [](auto width) {
         constexpr int kWidth = decltype(width)::value;
         static_assert(BackwardShape<kWidth, bf16_t>::kRows == BackwardShape<kWidth, float>::kRows,
@@ -410,12 +413,14 @@ hipError_t launchLayerNormForward(const LayerNormForward &a, hipStream_t stream)
 
 hipError_t launchLayerNormBackward(const LayerNormBackward &a, hipStream_t stream) {
     const uint32_t blocks = lnBackwardBlocks(a.rows, a.cols);
-    if (a.rows && a.rows <= kFewRows)
+    if (a.rows && a.rows <= fewRows(a.cols))
         return byTypes(a.dtype, a.paramDtype, [&](auto t, auto w) {
             byWidth(a.cols, [&](auto width) {
                 using S = BackwardShape<decltype(width)::value, decltype(t)>;
+                constexpr int kSlabCols = S::kCols <= int(kNarrow) ? 16 : 32;
                 const uint32_t slabs = (a.cols + kSlabCols - 1) / kSlabCols;
-                hipLaunchKernelGGL((lnBackwardFewKernel<decltype(t), decltype(w), S::kLanes, S::kChunks, S::kBlock>),
+                hipLaunchKernelGGL((lnBackwardFewKernel<decltype(t), decltype(w), S::kLanes, S::kChunks, S::kBlock,
+                                                        kSlabCols>),
                                    dim3(slabs + gridFor(a.rows, S::kRows, 1024)), dim3(S::kBlock), 0, stream, a, slabs);
             });
         });

@@ -192,7 +192,7 @@ def backward_reference(x, d, w, mean, rstd):
 def param_depth(rows):
     """Additions in a chain of the parameter sums: rows per group of lanes (at least 512 groups once
     there are that many rows), up to 16 groups of a workgroup, 16 partial rows per lane group, 32 groups.
-    (Up to 512 rows: 16 rows per group of lanes, 8 groups, 4 exchanges -- fewer.)"""
+    (Few rows: 16 rows per group of lanes, 8 groups, 4 exchanges -- fewer.)"""
     return rows // 512 + 1 + 16 + 16 + 32 + 4
 
 
@@ -227,7 +227,8 @@ def stats_of(x, eps=1e-5):
 
 @pytest.mark.parametrize("dt,pdt", COMBOS)
 def test_backward_sizes(bfo, dt, pdt):
-    for k, (rows, cols) in enumerate(SHAPES + [(2048, 64), (2049, 768), (5000, 33), (512, 300), (513, 300), (511, 2049), (700, 9000)]):
+    for k, (rows, cols) in enumerate(SHAPES + [(2048, 64), (2049, 768), (5000, 33), (512, 300), (513, 300), (511, 2049), (700, 9000),
+                                             (1024, 801), (1025, 801), (1024, 2048), (512, 2049), (513, 2049)]):
         print(dt, pdt, rows, cols, flush=True)
         x, d, w, _ = inputs(rows, cols, TYPES[dt], TYPES[pdt], 200 + k, pad=k % 3)
         mean, rstd = stats_of(x)
@@ -235,7 +236,7 @@ def test_backward_sizes(bfo, dt, pdt):
 
 
 @pytest.mark.parametrize("dt,pdt", COMBOS)
-@pytest.mark.parametrize("rows,cols", [(77, 96), (600, 1600), (5, 5000)])
+@pytest.mark.parametrize("rows,cols", [(77, 96), (600, 1600), (5, 5000), (1100, 1600)])
 def test_backward_accumulates(bfo, dt, pdt, rows, cols):
     x, d, w, _ = inputs(rows, cols, TYPES[dt], TYPES[pdt], 31)
     mean, rstd = stats_of(x)
