@@ -234,7 +234,23 @@ __global__ __launch_bounds__(kBlock) void lnBackwardKernel(LayerNormBackward a) 
 // Few rows, in one launch and without partials: mean and rstd are given, so
 // dweight and dbias need nothing of dx.  The first workgroups sum kSlabCols
 // columns each over all rows (4 columns a lane), the others form dx; both read x
-// and dout, which the caches hold.
+// and dout, which the caches hold.  Workgroups go to the XCDs in turn: the slabs
+// that share a row's 128-byte lines are given to one XCD, whose L2 then reads them
+// once.
+constexpr uint32_t kXcds = 8;
+template <typename T, int kSlabCols>
+struct Slabs {
+    static constexpr uint32_t kShare = 128 / (kSlabCols * sizeof(T));  // slabs of a line
+    static __host__ __device__ uint32_t workgroups(uint32_t cols) {
+        const uint32_t lines = (cols + kSlabCols * kShare - 1) / (kSlabCols * kShare);
+        return (lines + kXcds - 1) / kXcds * kXcds * kShare;
+    }
+    static __device__ uint32_t firstColumn(uint32_t workgroup) {
+        const uint32_t line = workgroup / (kXcds * kShare) * kXcds + workgroup % kXcds;
+        return (line * kShare + workgroup / kXcds % kShare) * kSlabCols;
+    }
+};
+
 template <typename T, typename W, int kLanes, int kChunks, int kBlock, int kSlabCols>
 __global__ __launch_bounds__(kBlock) void lnBackwardFewKernel(LayerNormBackward a, uint32_t slabs) {
     constexpr int kRows = kBlock / kLanes;
@@ -248,7 +264,8 @@ __global__ __launch_bounds__(kBlock) void lnBackwardFewKernel(LayerNormBackward 
                                                            uint64_t(gridDim.x - slabs) * kRows, red, none, none);
         return;
     }
-    const int c0 = int(blockIdx.x) * kSlabCols, left = int(a.cols) - c0;
+    const int c0 = int(Slabs<T, kSlabCols>::firstColumn(blockIdx.x)), left = int(a.cols) - c0;
+    if (left <= 0) return;
     const int c = int(threadIdx.x % kRowLanes) * N;
     const uint32_t group = threadIdx.x / kRowLanes;
     float dw[N] = {}, db[N] = {};
@@ -347,15 +364,23 @@ struct BackwardShape {
     static constexpr int kRows = kBlock / kLanes;
 };
 
-// Up to here one launch for all gradients is faster than rows and partials: 1,024
-// rows of 1,600 bf16 7.6 us against 9.9, of 768 6.2 against 8.2, 512 rows of 4,096
-// 6.8 against 12, one row 2.7 against 5.0.  2,048 rows of 1,600 are slower (13.4
-// against 11.2), and so are 1,024 of 8,192 (22.0 against 19.4): a column workgroup
-// walks all rows by itself.  Slabs of 16 columns make it walk twice as many at a
-// time (32: 1,024 rows of 1,600 10.0 us); of wide rows they are too many workgroups
-// for that (512 rows of 4,096 8.1 us with 16, 6.8 with 32).
-constexpr uint32_t kNarrow = 2048;
-uint64_t fewRows(uint32_t cols) { return cols <= kNarrow ? 1024 : 512; }
+// Up to here one launch for all gradients is faster than rows and partials: 2,048
+// rows of 1,600 bf16 9.3 us against 11.3 (fp32 12.3 against 12.8; of 801 11.5
+// against 10.4), 1,024 of 4,096 9.3 against 16.1 (fp32 14.0 and 16.3), 512 of 8,192
+// 10.1 against 12, one row of 1,600 2.9 against 5.0.  Twice as many are slower: a
+// column workgroup walks all rows by itself.
+uint64_t fewRows(uint32_t cols) { return cols <= 2048 ? 2048 : cols <= 4096 ? 1024 : 512; }
+// Workgroups of narrow slabs walk more rows at a time, and are more: 1,024 rows of 1,600 bf16 6.3 us with 16 columns,
+// 5.7 with 8, but 256 rows 3.2 and 3.6; 512 rows of 4,096 6.4 with 32, 5.4 with 16;
+// 512 rows of 8,192 10.1 with 32, 13.4 with 16.  The slabs of a line on one XCD: 16
+// columns, 1,024 x 768 6.2 -> 4.6 us, 1,024 x 1,600 7.6 -> 6.3.
+template <int kCols, typename F>
+void bySlab(uint64_t rows, F f) {
+    if constexpr (kCols > 4096) f(std::integral_constant<int, 32>{});
+    else if constexpr (kCols > 2048) f(std::integral_constant<int, 16>{});
+    else if (rows <= 512) f(std::integral_constant<int, 16>{});
+    else f(std::integral_constant<int, 8>{});
+}
 
 template <typename F>
 auto byWidth(uint32_t cols, F f) {
@@ -417,11 +442,14 @@ hipError_t launchLayerNormBackward(const LayerNormBackward &a, hipStream_t strea
         return byTypes(a.dtype, a.paramDtype, [&](auto t, auto w) {
             byWidth(a.cols, [&](auto width) {
                 using S = BackwardShape<decltype(width)::value, decltype(t)>;
-                constexpr int kSlabCols = S::kCols <= int(kNarrow) ? 16 : 32;
-                const uint32_t slabs = (a.cols + kSlabCols - 1) / kSlabCols;
-                hipLaunchKernelGGL((lnBackwardFewKernel<decltype(t), decltype(w), S::kLanes, S::kChunks, S::kBlock,
-                                                        kSlabCols>),
-                                   dim3(slabs + gridFor(a.rows, S::kRows, 1024)), dim3(S::kBlock), 0, stream, a, slabs);
+                bySlab<S::kCols>(a.rows, [&](auto columns) {
+                    constexpr int kSlabCols = decltype(columns)::value;
+                    const uint32_t slabs = Slabs<decltype(t), kSlabCols>::workgroups(a.cols);
+                    hipLaunchKernelGGL((lnBackwardFewKernel<decltype(t), decltype(w), S::kLanes, S::kChunks, S::kBlock,
+                                                            kSlabCols>),
+                                       dim3(slabs + gridFor(a.rows, S::kRows, 1024)), dim3(S::kBlock), 0, stream, a,
+                                       slabs);
+                });
             });
         });
     return byTypes(a.dtype, a.paramDtype, [&](auto t, auto w) {

@@ -530,9 +530,9 @@ int layernorm_forward(const void *x, uint64_t x_stride, const void *weight, cons
                       uint64_t out_stride, float *mean, float *rstd, uint64_t rows, uint32_t cols, float eps,
                       int dtype, int param_dtype, void *stream);
 
-/* *bytes = the workspace layernorm_backward needs; 0 for few rows (1,024 of
- * at most 2,048 columns, 512 of more), and workspace may then be NULL.  Host
- * only. */
+/* *bytes = the workspace layernorm_backward needs; 0 for few rows (up to
+ * 2,048 of at most 2,048 columns, 1,024 of at most 4,096, 512 of more), and
+ * workspace may then be NULL.  Host only. */
 int bfo_layernorm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t *bytes);
 
 /* Gradients of layernorm_forward, from its mean and rstd.  With
