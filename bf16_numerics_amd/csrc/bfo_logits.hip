@@ -42,6 +42,13 @@ struct Stat {
 constexpr float kReferenceMost = 1024.0f, kReferenceFloor = -2048.0f;
 __device__ __forceinline__ float referenceOf(float m, float k) { return fmaxf(m * k, kReferenceFloor); }
 
+// d k for a difference d of scores.  From scales of 2^128 / log2(e) on k is
+// infinite, and no reference holds (m k is infinite or, for m = 0, NaN): such rows
+// are exactStat's, by this product in its parts.
+__device__ __forceinline__ float timesK(float d, float k, float scale) {
+    return k < INFINITY ? d * k : d * scale * kLog2e;
+}
+
 // The set's s and t for an M that is `up` larger.
 __device__ __forceinline__ Stat raised(const Stat &a, float m, float up) {
     const float r = exp2Fast(-up);
@@ -272,10 +279,11 @@ __device__ __forceinline__ Stat blockJoined(const Stat &wave, Stat (&stats)[kBlo
 // A finished Stat of a row with maximum m by differences from m, which are
 // exact where products with k are not: for the rows that referenceOf is not for.
 template <typename T, int kBlock>
-__device__ __noinline__ Stat exactStat(const T *row, uint32_t V, float m, float k, Stat (&stats)[kBlock / 64]) {
+__device__ __noinline__ Stat exactStat(const T *row, uint32_t V, float m, float k, float scale,
+                                       Stat (&stats)[kBlock / 64]) {
     Stat a = {m, 0.0f, 0.0f};
     for (uint32_t c = threadIdx.x; c < V; c += kBlock) {
-        const float d = (toFloat(row[c]) - m) * k, p = exp2Fast(d);
+        const float d = timesK(toFloat(row[c]) - m, k, scale), p = exp2Fast(d);
         a.s += p;
         a.t = fmaf(p, fmaxf(d, kLowest), a.t);
     }
@@ -293,9 +301,9 @@ __device__ __noinline__ Stat exactStat(const T *row, uint32_t V, float m, float 
 }
 
 template <typename T, int kBlock>
-__device__ __forceinline__ Stat finished(const Stat &a, const T *row, uint32_t V, float k,
+__device__ __forceinline__ Stat finished(const Stat &a, const T *row, uint32_t V, float k, float scale,
                                          Stat (&stats)[kBlock / 64]) {
-    if (a.s == 0.0f || !(fabsf(a.m * k) < kReferenceMost)) return exactStat<T, kBlock>(row, V, a.m, k, stats);
+    if (a.s == 0.0f || !(fabsf(a.m * k) < kReferenceMost)) return exactStat<T, kBlock>(row, V, a.m, k, scale, stats);
     // M's rounding error, an exact difference of less than 2^-13
     return raised(a, a.m, fmaf(a.m, k, -referenceOf(a.m, k)));
 }
@@ -531,7 +539,7 @@ __global__ __launch_bounds__(kBlock, kTop ? (kBlock > 256 ? 4 : 7) : 1) void log
             for (int d = 1; d < kBlock / kGroups; d *= 2) key = max(key, uint32_t(__shfl_xor(int(key), d, 64)));
             if (threadIdx.x % (kBlock / kGroups) == 0) sh.groupKey[threadIdx.x / (kBlock / kGroups)] = key;
         }
-        const Stat all = finished<T, kBlock>(blockJoined<kBlock>(wave, stats, k), row, V, k, stats);
+        const Stat all = finished<T, kBlock>(blockJoined<kBlock>(wave, stats, k), row, V, k, a.scale, stats);
         // The last wavefront writes the row's results while the first one looks for
         // the bound of its top.
         const RowResult res = rowResult(all, a.scale);
@@ -577,7 +585,7 @@ __global__ __launch_bounds__(kJoinBlock) void logitsJoinKernel(LogitsForward a, 
     const float4 part = lane < seg.count ? seg.stats(a)[r * seg.count + lane] : float4{kLowest, 0.0f, 0.0f, 0.0f};
     // finished statistics: M is m k exactly
     Stat all = {waveMax(part.x), 0.0f, 0.0f};
-    const Stat mine = raised({part.x, part.y, part.z}, all.m, (all.m - part.x) * k);
+    const Stat mine = raised({part.x, part.y, part.z}, all.m, timesK(all.m - part.x, k, a.scale));
     all.s = laneSum<64>(mine.s);
     all.t = laneSum<64>(mine.t);
     const RowResult res = rowResult(all, a.scale);

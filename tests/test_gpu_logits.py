@@ -679,3 +679,33 @@ def test_binding_refusals(bfo):
     with pytest.raises(bfo.BfoError):
         bfo.distill_forward(logits, index, torch.empty(4, 0, device=DEV), f)
     assert math.isfinite(bfo.logits_workspace_bytes(1, 1 << 28, 128))
+
+
+@pytest.mark.parametrize("rows,V", [(5, 100), (600, 9001), (3, 70001)])
+@pytest.mark.parametrize("scale", [1e37, 2.3e38, 2.4e38, 3.4028234663852886e38])
+def test_largest_scales(bfo, rows, V, scale):
+    """Scales up to binary32's largest, whose product with log2(e) is past it:
+    rows of zeros, rows of equal scores and scores so small that z is of
+    ordinary size.  (x - M) is exact on the subnormals' grid, so the counted
+    roundings are the usual ones."""
+    g = gen(rows)
+    z = 3 * torch.empty(rows, V, device=DEV).normal_(generator=g)
+    logits = (z.double() / single(scale)).float()
+    logits[0] = 0.0
+    logits[1] = 0.25 / single(scale)
+    targets = torch.randint(0, V, (rows,), generator=g, device=DEV).to(torch.int32)
+    out = run_forward(bfo, logits, targets, V, scale, 20)
+    check_forward(out, logits, targets, V, scale, 20)
+    factor = torch.full((rows,), 0.125, device=DEV)
+    d = torch.full_like(logits, NAN)
+    bfo.token_logprobs_backward(logits, targets, out["stats"], factor, d, entropy=out["entropy"], dentropy=factor,
+                                scale=scale)
+    sparse = torch.zeros(rows, V, dtype=torch.float64, device=DEV)
+    sparse.scatter_(1, targets.long()[:, None], 0.125)
+    check_gradient(d, V, *gradient_reference(logits, V, scale, out["stats"], -factor, -factor, out["entropy"], sparse))
+    index, _ = teacher(rows, V, 20, 41)
+    value = torch.gather(logits, 1, index.clamp(min=0).long()).contiguous()
+    kl, _, lp = run_distill(bfo, logits, index, value, V, scale, targets)
+    ref, _, _, _, want, tol = distill_reference(logits, V, scale, index, value, targets)
+    near(kl, want, tol, "kl")
+    near(lp, ref["at"], ref["at_tol"], "logprob")
