@@ -52,6 +52,7 @@ ACCUMULATE_DX, ACCUMULATE_PARAMS = 1, 2
 LAYERNORM_MAX_COLS = 16384
 TOP_MAX = 128
 VOCAB_MAX = 1 << 28
+SPLIT_ROWS = 128  # forward passes over the vocabulary use a workspace up to here only
 
 
 class BfoTensor(ctypes.Structure):
@@ -736,14 +737,14 @@ def _launch(name, dev, *args):
 
 @functools.lru_cache(maxsize=4096)
 def layernorm_workspace_bytes(rows, cols):
-    """Device bytes layernorm_backward needs as workspace."""
+    """Device bytes layernorm_backward of these sizes, or of smaller ones, needs as workspace."""
     out = ctypes.c_uint64(0)
     _check("bfo_layernorm_workspace_bytes", _lib().bfo_layernorm_workspace_bytes(rows, cols, ctypes.byref(out)))
     return out.value
 
 
 def new_layernorm_workspace(rows, cols, device):
-    """A device buffer for layernorm_backward of rows x cols matrices (at least 16 bytes)."""
+    """A device buffer for layernorm_backward of up to rows x cols matrices (at least 16 bytes)."""
     return torch.empty(max(16, layernorm_workspace_bytes(rows, cols)), dtype=torch.uint8, device=device)
 
 
@@ -781,7 +782,8 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, wor
 
 @functools.lru_cache(maxsize=4096)
 def logits_workspace_bytes(rows, vocab, top=0):
-    """Device bytes token_logprobs_forward (`top` alternatives) and distill_forward (top 0) need."""
+    """Device bytes token_logprobs_forward (`top` alternatives) and distill_forward (top 0) of these
+    sizes, or of smaller ones, need."""
     out = ctypes.c_uint64(0)
     _check("bfo_logits_workspace_bytes", _lib().bfo_logits_workspace_bytes(rows, vocab, top, ctypes.byref(out)))
     return out.value
@@ -790,6 +792,11 @@ def logits_workspace_bytes(rows, vocab, top=0):
 def new_logits_workspace(rows, vocab, top, device):
     """A device buffer of logits_workspace_bytes(rows, vocab, top) bytes (at least 16)."""
     return torch.empty(max(16, logits_workspace_bytes(rows, vocab, top)), dtype=torch.uint8, device=device)
+
+
+def _logits_workspace(workspace, rows, vocab, top, dev):
+    need = logits_workspace_bytes(rows, vocab, top) if rows <= SPLIT_ROWS else 0
+    return _workspace_ptr(workspace, need, dev, "new_logits_workspace")
 
 
 def _vocab(vocab, cols):
@@ -822,7 +829,7 @@ def token_logprobs_forward(logits, targets=None, logprob=None, stats=None, entro
     top = 0
     if top_index is not None:
         top = _columns(top_index, "top_index", rows)
-    ws = _workspace_ptr(workspace, logits_workspace_bytes(rows, v, top), dev, "new_logits_workspace")
+    ws = _logits_workspace(workspace, rows, v, top, dev)
     _launch("token_logprobs_forward", dev, lp, ls, rows, v, _DTYPE_CODES[logits.dtype], scale,
             _vector(targets, torch.int32, rows, "targets", dev), _vector(logprob, torch.float32, rows, "logprob", dev),
             _vector(stats, torch.float32, 2 * rows, "stats", dev),
@@ -863,7 +870,7 @@ def distill_forward(logits, teacher_index, teacher_logits, kl, stats=None, targe
     dev = logits.device
     v = _vocab(vocab, cols)
     ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
-    ws = _workspace_ptr(workspace, logits_workspace_bytes(rows, v, 0), dev, "new_logits_workspace")
+    ws = _logits_workspace(workspace, rows, v, 0, dev)
     _launch("distill_forward", dev, lp, ls, rows, v, _DTYPE_CODES[logits.dtype], scale, ti, tl, count,
             _vector(targets, torch.int32, rows, "targets", dev), _vector(kl, torch.float32, rows, "kl", dev),
             _vector(logprob, torch.float32, rows, "logprob", dev),

@@ -421,6 +421,13 @@ uint32_t lnBackwardBlocks(uint64_t rows, uint32_t cols) {
     return gridFor(rows, perBlock, cols <= 4096 ? 512 : 256);
 }
 
+// Up to 4,096 columns the size grows with both: more columns mean no fewer
+// workgroups, from no more rows on.  Above, there are half as many workgroups.
+uint64_t lnWorkspaceBound(uint64_t rows, uint32_t cols) {
+    const uint64_t own = lnWorkspaceBytes(rows, cols), narrower = cols > 4096 ? lnWorkspaceBytes(rows, 4096) : 0;
+    return own > narrower ? own : narrower;
+}
+
 hipError_t launchLayerNormForward(const LayerNormForward &a, hipStream_t stream) {
     if (!a.rows) return hipSuccess;
     return byTypes(a.dtype, a.paramDtype, [&](auto t, auto w) {

@@ -781,10 +781,14 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
 // scores the second launch costs what the split gains (9.3 -> 10.3), and above 8
 // segments joining their tops costs more again (20 us with 16).  A last segment
 // still holds more than BFO_TOP_MAX scores.
+constexpr uint32_t kSplitRows = 128, kSplitVocab = 65536, kSplitBlocks = 256;
+uint32_t mostSegments(uint32_t vocab) {
+    if (vocab < kSplitVocab) return 1;
+    return vocab / 16384 < kMaxSegments ? vocab / 16384 : kMaxSegments;
+}
 Segments segmentsOf(uint64_t rows, uint32_t vocab) {
-    uint32_t n = vocab < 65536 || rows > 128 ? 1 : vocab / 16384;
-    if (n > kMaxSegments) n = kMaxSegments;
-    if (n * rows > 256) n = uint32_t(256 / rows);
+    uint32_t n = rows > kSplitRows ? 1 : mostSegments(vocab);
+    if (n * rows > kSplitBlocks) n = uint32_t(kSplitBlocks / rows);
     if (n < 2) return {1, vocab};
     const uint32_t length = ((vocab + n - 1) / n + 63) / 64 * 64;
     return {(vocab + length - 1) / length, length};
@@ -848,9 +852,18 @@ hipError_t backward(const LogitsBackward &a, hipStream_t stream) {
 
 }  // namespace
 
+constexpr uint64_t segmentBytes(uint32_t top) { return sizeof(float4) + top * sizeof(uint64_t); }
+
 uint64_t logitsWorkspaceBytes(uint64_t rows, uint32_t vocab, uint32_t top) {
     const Segments seg = segmentsOf(rows, vocab);
-    return seg.count > 1 ? rows * seg.count * (sizeof(float4) + top * sizeof(uint64_t)) : 0;
+    return seg.count > 1 ? rows * seg.count * segmentBytes(top) : 0;
+}
+
+// More rows than are split still cover fewer that are.
+uint64_t logitsWorkspaceBound(uint64_t rows, uint32_t vocab, uint32_t top) {
+    if (vocab < kSplitVocab) return 0;
+    const uint64_t segments = rows * mostSegments(vocab);
+    return (segments < kSplitBlocks ? segments : kSplitBlocks) * segmentBytes(top);
 }
 
 hipError_t launchLogitsForward(const LogitsForward &a, int dtype, hipStream_t stream) {

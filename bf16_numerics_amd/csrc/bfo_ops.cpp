@@ -154,7 +154,7 @@ int layernorm_forward(const void *x, uint64_t x_stride, const void *weight, cons
 int bfo_layernorm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t *bytes) {
     if (!bytes || cols == 0) return BFO_EINVAL;
     if (cols > BFO_LAYERNORM_MAX_COLS || rows > kMaxRows) return BFO_ERANGE;
-    *bytes = bfo::lnWorkspaceBytes(rows, cols);
+    *bytes = bfo::lnWorkspaceBound(rows, cols);
     return BFO_OK;
 }
 
@@ -195,7 +195,7 @@ int layernorm_backward(const void *dout, uint64_t dout_stride, const void *x, ui
 int bfo_logits_workspace_bytes(uint64_t rows, uint32_t vocab, uint32_t top, uint64_t *bytes) {
     if (!bytes || vocab == 0 || top > vocab) return BFO_EINVAL;
     if (vocab > BFO_VOCAB_MAX || top > BFO_TOP_MAX || rows > kMaxRows) return BFO_ERANGE;
-    *bytes = bfo::logitsWorkspaceBytes(rows, vocab, top);
+    *bytes = bfo::logitsWorkspaceBound(rows, vocab, top);
     return BFO_OK;
 }
 

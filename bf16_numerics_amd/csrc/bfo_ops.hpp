@@ -28,6 +28,8 @@ uint32_t lnBackwardBlocks(uint64_t rows, uint32_t cols);
 inline uint64_t lnWorkspaceBytes(uint64_t rows, uint32_t cols) {
     return uint64_t(lnBackwardBlocks(rows, cols)) * 2 * cols * sizeof(float);
 }
+// What no call of at most so many rows and columns exceeds.
+uint64_t lnWorkspaceBound(uint64_t rows, uint32_t cols);
 
 struct LayerNormForward {
     ConstMatrix x;
@@ -73,6 +75,7 @@ struct LogitsForward {
     void *workspace;
 };
 uint64_t logitsWorkspaceBytes(uint64_t rows, uint32_t vocab, uint32_t top);
+uint64_t logitsWorkspaceBound(uint64_t rows, uint32_t vocab, uint32_t top);  // as lnWorkspaceBound
 hipError_t launchLogitsForward(const LogitsForward &a, int dtype, hipStream_t stream);
 
 struct LogitsBackward {

@@ -509,7 +509,8 @@ int bfo_spread_layout(const uint64_t *bytes, uint32_t count, uint64_t *offsets, 
  *   - Outputs may not overlap an input or one another, except where a call
  *     says so (BFO_EINVAL).  Only the rows' own elements are written.
  *   - Workspaces are device memory, 16-byte aligned, of the size the matching
- *     *_workspace_bytes gives, owned by the caller and used by this call only;
+ *     *_workspace_bytes gives for the call's sizes or larger ones (it never falls
+ *     as one of them grows), owned by the caller and used by this call only;
  *     calls with separate workspaces may run at the same time, and graphs that
  *     may run at the same time need a workspace each.  Calls allocate nothing
  *     and can be recorded into a HIP graph.
@@ -551,8 +552,9 @@ int layernorm_backward(const void *dout, uint64_t dout_stride, const void *x, ui
                        void *dweight, void *dbias, uint64_t rows, uint32_t cols, int dtype, int param_dtype,
                        int accumulate, void *workspace, void *stream);
 
-/* *bytes = the workspace token_logprobs_forward (top tokens asked for) and
- * distill_forward (top 0) need; may be 0, and workspace then NULL.  Host only. */
+/* *bytes = the workspace of token_logprobs_forward (top tokens asked for) and
+ * distill_forward (top 0), which calls of up to 128 rows of at least 65,536
+ * scores need; to others workspace may be NULL.  Host only. */
 int bfo_logits_workspace_bytes(uint64_t rows, uint32_t vocab, uint32_t top, uint64_t *bytes);
 
 /* Log probabilities of given tokens.  Row r of logits holds vocab scores (a

@@ -356,3 +356,15 @@ def test_binding_refusals(bfo):
     with pytest.raises(bfo.BfoError):
         bfo.layernorm_backward(d, x, w, mean, rstd, d, w.clone(), b.clone(),
                                workspace=bfo.new_layernorm_workspace(8, 64, DEV))
+
+
+def test_workspace_of_a_larger_call(bfo):
+    """The widest layer's workspace serves a narrower one, whose partial sums are more."""
+    ws = bfo.new_layernorm_workspace(2100, 4097, DEV)
+    x, d, w, _ = inputs(2100, 4096, torch.bfloat16, torch.bfloat16, 71)
+    mean, rstd = stats_of(x)
+    own = run_backward(bfo, x, d, w, mean, rstd)
+    got = [torch.full_like(t, float("nan")) for t in own]
+    bfo.layernorm_backward(d, x, w, mean, rstd, *got, workspace=ws)
+    for a, b in zip(own, got):
+        assert torch.equal(a, b)

@@ -709,3 +709,25 @@ def test_largest_scales(bfo, rows, V, scale):
     ref, _, _, _, want, tol = distill_reference(logits, V, scale, index, value, targets)
     near(kl, want, tol, "kl")
     near(lp, ref["at"], ref["at_tol"], "logprob")
+
+
+def test_workspace_of_a_larger_call(bfo):
+    """A full micro-batch's workspace serves its ragged last batch, which is split over workgroups."""
+    V = 70001
+    logits, targets = scores(64, V, "bf16", 61)
+    ws = bfo.new_logits_workspace(8192, V + 5, 128, DEV)
+    st, lp = torch.empty(64, 2, device=DEV), torch.empty(64, device=DEV)
+    ti, tl = torch.empty(64, 20, dtype=torch.int32, device=DEV), torch.empty(64, 20, device=DEV)
+    bfo.token_logprobs_forward(logits, targets, lp, st, top_index=ti, top_logprob=tl, workspace=ws)
+    own = run_forward(bfo, logits, targets, V, 1.0, 20)
+    for k, t in (("logprob", lp), ("stats", st), ("top_index", ti), ("top_logprob", tl)):
+        assert torch.equal(t, own[k]), k
+    index, value = teacher(64, V, 20, 62)
+    kl = torch.empty(64, device=DEV)
+    bfo.distill_forward(logits, index, value, kl, workspace=ws)
+    assert torch.equal(kl, run_distill(bfo, logits, index, value, V, 1.0)[0])
+    # calls that use none take none
+    many, t = scores(129, V, "bf16", 63)
+    lp = torch.empty(129, device=DEV)
+    bfo.token_logprobs_forward(many, t, lp)
+    assert torch.equal(lp, run_forward(bfo, many, t, V)["logprob"])

@@ -213,3 +213,28 @@ def test_binding_names_what_is_wrong(bfo):
         bfo.layernorm_workspace_bytes(4, 1 << 20)
     with pytest.raises(bfo.BfoError):
         bfo.logits_workspace_bytes(4, 100, 300)
+
+
+def test_workspace_of_the_largest_call_serves_every_smaller_one(bfo):
+    """Sizes never fall as rows, columns, vocabulary or top grow, so a buffer of the largest call's size
+    holds those of a ragged last batch or a narrower layer."""
+    rows = sorted({1, 2, 3, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1023, 1024, 1025,
+                   2047, 2048, 2049, 2100, 4096, 8191, 8192, 16384, 1 << 20, 1 << 31})
+    cols = sorted({1, 128, 129, 512, 513, 801, 1024, 1025, 1600, 2048, 2049, 4095, 4096, 4097, 5000, 8192, 8193,
+                   9000, 16384})
+    vocabs = sorted({1, 128, 50257, 65535, 65536, 65537, 81920, 98304, 100000, 128256, 131071, 131072, 131073, 1 << 20,
+                     1 << 28})
+
+    def rising(axes, f):
+        """f at every point is at least f one step back along each axis."""
+        import itertools
+        for at in itertools.product(*(range(len(a)) for a in axes)):
+            here = f(*(a[i] for a, i in zip(axes, at)))
+            for k in range(len(axes)):
+                if at[k]:
+                    back = at[:k] + (at[k] - 1,) + at[k + 1:]
+                    less = tuple(a[i] for a, i in zip(axes, back))
+                    assert f(*less) <= here, (less, tuple(a[i] for a, i in zip(axes, at)))
+
+    rising((rows, cols), bfo.layernorm_workspace_bytes)
+    rising((rows, vocabs, (0, 1, 20, 128)), lambda r, v, t: bfo.logits_workspace_bytes(r, v, min(t, v)))
