@@ -731,3 +731,23 @@ def test_workspace_of_a_larger_call(bfo):
     lp = torch.empty(129, device=DEV)
     bfo.token_logprobs_forward(many, t, lp)
     assert torch.equal(lp, run_forward(bfo, many, t, V)["logprob"])
+
+
+def test_rows_of_more_columns_than_32_bits(bfo):
+    """A vocabulary or a width past 2^32 is out of range; a short vocabulary at the start of such a row is not."""
+    wide = torch.zeros(1, (1 << 32) + 5, dtype=torch.bfloat16, device=DEV)
+    st, one = torch.empty(1, 2, device=DEV), torch.ones(1, device=DEV)
+    t = torch.zeros(1, dtype=torch.int32, device=DEV)
+    index, value = torch.zeros(1, 2, dtype=torch.int32, device=DEV), torch.zeros(1, 2, device=DEV)
+    for call in (lambda: bfo.token_logprobs_forward(wide, stats=st),
+                 lambda: bfo.token_logprobs_backward(wide, t, st, one, wide, vocab=5),
+                 lambda: bfo.distill_forward(wide, index, value, one.clone()),
+                 lambda: bfo.distill_backward(wide, index, value, st, one, wide, vocab=5),
+                 lambda: bfo.layernorm_forward(wide, wide[0], None, torch.empty_like(wide))):
+        with pytest.raises(bfo.BfoError) as e:
+            call()
+        assert e.value.status == bfo.ERANGE
+    bfo.token_logprobs_forward(wide, stats=st, vocab=5)
+    near(st[0, 1], torch.tensor(5.0, device=DEV).double().log(), 4 * U, "log sum of five zeros")
+    del wide
+    torch.cuda.empty_cache()

@@ -238,3 +238,19 @@ def test_workspace_of_the_largest_call_serves_every_smaller_one(bfo):
 
     rising((rows, cols), bfo.layernorm_workspace_bytes)
     rising((rows, vocabs, (0, 1, 20, 128)), lambda r, v, t: bfo.logits_workspace_bytes(r, v, min(t, v)))
+
+
+def test_binding_passes_no_size_modulo_two_to_the_32(bfo):
+    """Column counts are 32-bit arguments of the C ABI: larger ones are out of range, not their low words."""
+    def status(f, *sizes):
+        with pytest.raises(bfo.BfoError) as e:
+            f(*sizes)
+        return e.value.status
+
+    for cols in ((1 << 32) + 64, 1 << 32, -(1 << 32) + 64):
+        assert status(bfo.layernorm_workspace_bytes, 4, cols) == bfo.ERANGE
+        assert status(bfo.logits_workspace_bytes, 4, cols, 0) == bfo.ERANGE
+        assert status(bfo.logits_workspace_bytes, 4, 1000, cols) in (bfo.ERANGE, bfo.EINVAL)
+    for rows in ((1 << 64) + 4, -(1 << 64) + 4):
+        assert status(bfo.layernorm_workspace_bytes, rows, 64) == bfo.ERANGE
+        assert status(bfo.logits_workspace_bytes, rows, 1000, 0) == bfo.ERANGE
