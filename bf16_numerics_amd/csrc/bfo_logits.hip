@@ -85,8 +85,9 @@ constexpr uint32_t chunkElems() {
     return 16 / sizeof(T);
 }
 
-// Chunks are cut on 128-byte lines of memory, not from the row's first column:
-// the columns of a row's first line that come before the row.
+// Chunks are cut on 128-byte lines of memory, not from the row's first column
+// (odd rows 145 us for 167-172): the columns of a row's first line that come
+// before the row.  Which lane sums which column thus depends on the row's start.
 template <typename T>
 __device__ __forceinline__ int leadOf(const T *row) {
     return int((reinterpret_cast<uintptr_t>(row) & 127u) / sizeof(T));

@@ -504,8 +504,12 @@ int bfo_spread_layout(const uint64_t *bytes, uint32_t count, uint64_t *offsets, 
  *     BFO_EINVAL.  All arithmetic is binary32; an output in bf16 is rounded
  *     once, to nearest even.
  *   - rows may be 0 (the matrices may then be NULL).
- *   - Results are the same bits from call to call: sums run in an order that
- *     depends on the sizes only, and there are no atomics in them.
+ *   - Results are the same bits from call to call on the same arrays: sums run
+ *     in an order that depends on the sizes only, and there are no atomics in
+ *     them.  In the forward passes over a vocabulary the order depends also on
+ *     where in a 128-byte line of memory each row starts, so that the same scores
+ *     at another start (or as another row of an odd stride) may differ within
+ *     binary32 rounding; top_index and the gradients of given stats do not.
  *   - Outputs may not overlap an input or one another, except where a call
  *     says so (BFO_EINVAL).  Only the rows' own elements are written.
  *   - Workspaces are device memory, 16-byte aligned, of the size the matching

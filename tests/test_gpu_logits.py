@@ -751,3 +751,34 @@ def test_rows_of_more_columns_than_32_bits(bfo):
     near(st[0, 1], torch.tensor(5.0, device=DEV).double().log(), 4 * U, "log sum of five zeros")
     del wide
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V,pad", [(7, 5003, 2), (600, 2051, 0), (3, 70001, 1)])
+def test_order_of_sums_and_where_rows_start(bfo, dt, rows, V, pad):
+    """Sums over the vocabulary run in an order given by the sizes and by where
+    in a 128-byte line the rows start: the same bits at starts that are equal
+    modulo 128 bytes, the same values within the counted roundings at others,
+    and the same tokens anywhere."""
+    line = 128 // TYPES[dt].itemsize
+    logits, targets = scores(rows, V, dt, 81, pad=pad)
+    index, value = teacher(rows, V, 20, 82)
+    flat = torch.empty(rows * (V + pad) + 4 * line, dtype=TYPES[dt], device=DEV)
+
+    def at(start):
+        view = flat[start:start + rows * (V + pad)].view(rows, V + pad)
+        view.copy_(logits)
+        out = run_forward(bfo, view, targets, V, 1.0, 20)
+        out["kl"] = run_distill(bfo, view, index, value, V, 1.0)[0]
+        return out
+
+    first = at(0)
+    for start in (line, 3 * line):
+        again = at(start)
+        for k in first:
+            assert torch.equal(first[k], again[k]), (start, k)
+    _, _, _, _, want, tol = distill_reference(logits, V, 1.0, index, value, targets)
+    for start in (1, 2, line // 2, line - 1, line + 3):
+        other = at(start)
+        check_forward(other, logits, targets, V, 1.0, 20)
+        near(other["kl"], want, tol, "kl")
