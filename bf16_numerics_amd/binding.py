@@ -878,7 +878,8 @@ def distill_forward(logits, teacher_index, teacher_logits, kl, stats=None, targe
     """KL divergence of the teacher's softmax over its top logits (rows x count
     int32 indexes, negative: no entry, and float32 logits) from the student's
     softmax(scale * logits[:, :vocab]), per row into kl; targets and logprob
-    as in token_logprobs_forward."""
+    as in token_logprobs_forward.  teacher_logits are scaled here too, so they
+    are unscaled scores, or top_logprob of a pass at scale 1."""
     lp, ls, rows, cols = _matrix(logits, "logits")
     dev = logits.device
     v = _vocab(vocab, cols)

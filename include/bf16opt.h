@@ -607,9 +607,13 @@ int token_logprobs_backward(const void *logits, uint64_t stride, uint64_t rows, 
  * vocabulary, as in token_logprobs_forward:
  *   kl[r] = sum_k q[k] * (log q[k] - log p[teacher_index[k]])
  * (0 for a row without entries, or with entries of -inf only; an entry of
- * probability 0 adds nothing).  Any
- * per-row constant in the teacher's logits drops out, so top_logprob of the
- * teacher's token_logprobs_forward serves too.  A token named twice counts with
+ * probability 0 adds nothing).  One scale
+ * serves the teacher, the student and the true tokens' logprob.  Any per-row
+ * constant in the teacher's logits drops out, so top_logprob of the teacher's
+ * token_logprobs_forward serves too if that ran at scale 1; at another scale s it
+ * holds scaled scores, and q would be softmax(scale * s * logits): such a caller
+ * takes the scores themselves, logits[r][top_index[r][k]], or top_logprob / s.
+ * A token named twice counts with
  * both probabilities.  An index >= vocab, or a NaN or +inf among the entries,
  * gives NaN.  stats, targets and logprob as in token_logprobs_forward (all may
  * be NULL), so that a loss on the true tokens takes no second pass.

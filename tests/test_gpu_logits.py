@@ -782,3 +782,27 @@ def test_order_of_sums_and_where_rows_start(bfo, dt, rows, V, pad):
         other = at(start)
         check_forward(other, logits, targets, V, 1.0, 20)
         near(other["kl"], want, tol, "kl")
+
+
+@pytest.mark.parametrize("scale", [0.5, 1.7])
+def test_teacher_side_at_a_temperature(bfo, scale):
+    """At a temperature, the teacher's log probabilities at scale 1 serve, its scores do, and those at the
+    temperature itself do once divided by it; undivided they are another teacher's."""
+    V, K, R = 4001, 20, 50
+    z, t = scores(R, V, "bf16", 21)
+    student, _ = scores(R, V, "bf16", 22)
+    plain, scaled = run_forward(bfo, z, t, V, 1.0, K), run_forward(bfo, z, t, V, scale, K)
+    index = plain["top_index"]
+    assert torch.equal(index, scaled["top_index"])
+    raw = torch.gather(z.float(), 1, index.long())
+    _, _, _, _, want, tol = distill_reference(student, V, scale, index, raw, t)
+    s = single(scale)
+    # a log probability is off by at most (V / 64 + 100) u and half a step of its size, below 2^6; kl moves by
+    # s q (log q - log p - kl) per unit of a teacher's score, in all by at most s (2 kl + 1)
+    off = 4 * max(s, 1 / s) * (V / 64 + 100 + 64) * U * (1 + want.abs())
+    for value in (raw, plain["top_logprob"], scaled["top_logprob"] / s):
+        near(run_distill(bfo, student, index, value.contiguous(), V, scale)[0], want, tol + off, "kl")
+    again = run_distill(bfo, student, index, scaled["top_logprob"], V, scale)[0].double()
+    _, _, _, _, other, tol = distill_reference(student, V, scale, index, raw * s, t)
+    near(again, other, tol + off * (1 + other.abs()), "kl of the teacher scaled twice")
+    assert ((again - want).abs() > 0.01).any()
