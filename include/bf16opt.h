@@ -529,7 +529,11 @@ enum { BFO_BF16 = 0, BFO_F32 = 1 };
  * weight and bias hold cols values of param_dtype; bias may be NULL (0).
  * out has x's type.  mean and rstd (rows floats each, for the backward pass)
  * may be NULL.  1 <= cols <= BFO_LAYERNORM_MAX_COLS (0 -> BFO_EINVAL, above ->
- * BFO_ERANGE); eps >= 0 and finite.  A row with an infinity or NaN gives NaN. */
+ * BFO_ERANGE); eps >= 0 and finite.  A row with an infinity or NaN gives NaN.
+ * The sums are binary32's, which holds them for |x| < 2^113 and differences from
+ * the mean below 2^56; a row beyond that overflows (a sum of squares that does
+ * gives rstd 0 and out = bias).  Where eps = 0, a row whose differences are all
+ * below 2^-56 may lose their squares, and a constant row has no finite result. */
 #define BFO_LAYERNORM_MAX_COLS 16384u
 int layernorm_forward(const void *x, uint64_t x_stride, const void *weight, const void *bias, void *out,
                       uint64_t out_stride, float *mean, float *rstd, uint64_t rows, uint32_t cols, float eps,

@@ -368,3 +368,25 @@ def test_workspace_of_a_larger_call(bfo):
     bfo.layernorm_backward(d, x, w, mean, rstd, *got, workspace=ws)
     for a, b in zip(own, got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cols", [1, 37, 1600, 16384])
+def test_range_of_the_sums(bfo, cols):
+    """Rows at the ends of the range in which binary32 holds their sums: differences from the mean just
+    below 2^56, values just below 2^113, and differences of 2^-56 with eps 0."""
+    x, _, w, b = inputs(6, cols, torch.float32, torch.float32, 81)
+    sign = torch.where(torch.arange(cols, device=DEV) % 2 == 0, 1.0, -1.0)
+    top = 1 - 2.0 ** -20
+    far = x.clone()
+    far[0] = sign * 2.0 ** 56 * top                         # the sum of squares reaches 2^112 cols
+    far[1] = x[1] * 2.0 ** 50
+    far[2] = 2.0 ** 113 * (1 - 2.0 ** -10)                  # a constant row: a difference of at most 4 u 2^113
+    if cols > 1:
+        check_forward(far[:2], w, b, 1e-5, *(t[:2] for t in run_forward(bfo, far, w, b)))
+        near = x * 2.0 ** -60
+        near[0] = sign * 2.0 ** -56
+        near[:, 0] = 2.0 ** -56
+        near[:, 1] = -2.0 ** -56
+        check_forward(near, w, b, 0.0, *run_forward(bfo, near, w, b, 0.0))
+    mean = run_forward(bfo, far, w, b)[1]
+    assert ((mean[2].double() - far[2, 0].double()).abs() <= (DEPTH + 3) * U * 2.0 ** 113)
