@@ -806,3 +806,64 @@ def test_teacher_side_at_a_temperature(bfo, scale):
     _, _, _, _, other, tol = distill_reference(student, V, scale, index, raw * s, t)
     near(again, other, tol + off * (1 + other.abs()), "kl of the teacher scaled twice")
     assert ((again - want).abs() > 0.01).any()
+
+
+def special_rows(logits, V):
+    """Rows that are hard to pick the best of, over the first nine rows."""
+    i = torch.arange(V, device=DEV)
+    t = logits.dtype
+    logits = logits.clone()
+    logits[0, :V] = (i * 2.0 ** -6).to(t)                    # all the best in the last stretch (with ties in bf16)
+    logits[1, :V] = (i * -2.0 ** -6).to(t)                   # in the first
+    logits[2, :V] = (i % 5).to(t)                            # ties everywhere
+    logits[3, :V] = torch.where(i >= V - 3, logits[3, :V].float(), -INF).to(t)   # fewer scores than asked for
+    logits[4, : V - V // 3] = float(torch.finfo(t).min)
+    logits[5, :V] = torch.where(i // 8 % 512 == 17, i % 89 * 0.25, -1.0).to(t)   # in one lane's columns
+    logits[6, :V] += 100.0                                   # a common offset
+    logits[7, :V] -= 100.0
+    logits[8, V // 2] = NAN
+    return logits
+
+
+# (rows, vocabulary, type): a kept maximum covers two or three chunks of a lane's columns, with 512 lanes, with 256, with
+# 256 and nontemporal loads, and in segments; then one chunk with nontemporal loads in binary32.
+LONG = [(130, 131072, "bf16"), (200, 131071, "f32"), (520, 60001, "bf16"), (520, 30001, "f32"), (600, 65537, "bf16"),
+        (600, 50257, "f32"), (9, 1 << 20, "bf16"), (9, (1 << 20) + 77, "f32"), (3001, 20011, "f32")]
+
+
+@pytest.mark.parametrize("rows,V,dt", LONG)
+def test_top_of_stretches_of_several_chunks(bfo, rows, V, dt):
+    for k, top in enumerate((1, 20, 128)):
+        scale = (1.0, 0.7, 1.7)[k]
+        logits, targets = scores(rows, V, dt, 90 + k, pad=(0, 7, 64)[k])
+        logits = special_rows(logits, V)
+        targets[3] = V - 2
+        out = run_forward(bfo, logits, targets, V, scale, top)
+        index = top_reference_nan_first(logits[8:9], V, top)
+        assert torch.equal(out["top_index"][8:9].long(), index)
+        assert out["stats"][8].isnan().all() and out["top_logprob"][8].isnan().all()
+        assert torch.equal(out["top_index"][3:4].long(), top_reference(logits[3:4], V, top))
+        assert (out["top_logprob"][3, 3:] == -INF).all()
+        # a target whose scaled score is past binary32 counts as -inf: the lowest bf16 or binary32 value times 1.7 is
+        at = logits.gather(1, targets.clamp(min=0).long()[:, None])[:, 0].double() * single(scale)
+        past = (targets >= 0) & (at < -float(torch.finfo(torch.float32).max))
+        assert (out["logprob"][past] == -INF).all()
+        targets, out["logprob"] = torch.where(past, -1, targets), torch.where(past, 0.0, out["logprob"])
+        keep = torch.tensor([r for r in range(rows) if r not in (3, 8)], device=DEV)
+        for part in keep.split(128):
+            check_forward({n: t[part] for n, t in out.items()}, logits[part], targets[part], V, scale, top)
+        check_forward({n: t[3:4] for n, t in out.items() if not n.startswith("top")}, logits[3:4], targets[3:4], V,
+                      scale, 0)
+
+
+@pytest.mark.parametrize("rows,V,dt", [(700, 50257, "bf16"), (600, 50257, "f32"), (2100, 20011, "bf16")])
+def test_distill_of_more_scores_than_caches_hold(bfo, rows, V, dt):
+    logits, targets = scores(rows, V, dt, 97, pad=3)
+    index, value = teacher(rows, V, 65, 98)
+    kl, stats, lp = run_distill(bfo, logits, index, value, V, 0.7, targets)
+    for part in torch.arange(rows, device=DEV).split(128):
+        ref, _, _, _, want, tol = distill_reference(logits[part], V, 0.7, index[part], value[part], targets[part])
+        near(kl[part], want, tol, "kl")
+        near(stats[part, 0], ref["m"], U * ref["m"].abs(), "max")
+        near(stats[part, 1], ref["logs"], ref["rel"], "log sum")
+        near(lp[part], ref["at"], ref["at_tol"], "logprob")
