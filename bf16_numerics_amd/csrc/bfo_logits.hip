@@ -42,11 +42,17 @@ struct Stat {
 constexpr float kReferenceMost = 1024.0f, kReferenceFloor = -2048.0f;
 __device__ __forceinline__ float referenceOf(float m, float k) { return fmaxf(m * k, kReferenceFloor); }
 
-// d k for a difference d of scores.  From scales of 2^128 / log2(e) on k is
-// infinite, and no reference holds (m k is infinite or, for m = 0, NaN): such rows
-// are exactStat's, by this product in its parts.
-__device__ __forceinline__ float timesK(float d, float k, float scale) {
-    return k < INFINITY ? d * k : d * scale * kLog2e;
+// (x - m) f, also where only the difference is past binary32 (scores of 2^127
+// and more with both signs, and a small factor).
+__device__ __forceinline__ float scaledDifference(float x, float m, float f) {
+    const float d = x - m;
+    return fabsf(d) < INFINITY ? d * f : (0.5f * x - 0.5f * m) * f * 2.0f;
+}
+// (x - m) k.  From scales of 2^128 / log2(e) on k is infinite, and no reference
+// holds (m k is infinite or, for m = 0, NaN): such rows are exactStat's, by this
+// product in its parts.
+__device__ __forceinline__ float differenceTimesK(float x, float m, float k, float scale) {
+    return k < INFINITY ? scaledDifference(x, m, k) : (x - m) * scale * kLog2e;
 }
 
 // The set's s and t for an M that is `up` larger.
@@ -284,7 +290,7 @@ __device__ __noinline__ Stat exactStat(const T *row, uint32_t V, float m, float 
                                        Stat (&stats)[kBlock / 64]) {
     Stat a = {m, 0.0f, 0.0f};
     for (uint32_t c = threadIdx.x; c < V; c += kBlock) {
-        const float d = timesK(toFloat(row[c]) - m, k, scale), p = exp2Fast(d);
+        const float d = differenceTimesK(toFloat(row[c]), m, k, scale), p = exp2Fast(d);
         a.s += p;
         a.t = fmaf(p, fmaxf(d, kLowest), a.t);
     }
@@ -376,7 +382,7 @@ __device__ __forceinline__ RowResult rowResult(const Stat &a, float scale) {
 // log probability of score x.
 __device__ __forceinline__ float logProb(const RowResult &r, float x, float scale) {
     if (r.empty) return -INFINITY;
-    return r.finite ? (x - r.m) * scale - r.logs : NAN;
+    return r.finite ? scaledDifference(x, r.m, scale) - r.logs : NAN;
 }
 
 __device__ __forceinline__ void writeTop(const LogitsForward &a, uint64_t r, const RowResult &res, uint64_t key,
@@ -439,7 +445,7 @@ struct Teacher {
         float e[2], s = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            e[i] = exp2Fast((x[i] - m) * scale * kLog2e);
+            e[i] = exp2Fast(scaledDifference(x[i], m, scale) * kLog2e);
             s += e[i];
         }
         s = laneSum<64>(s);
@@ -450,7 +456,7 @@ struct Teacher {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             q[i] = any && id[i] >= 0 ? e[i] / s : 0.0f;
-            logq[i] = (x[i] - m) * scale - ls;
+            logq[i] = scaledDifference(x[i], m, scale) - ls;
         }
     }
 };
@@ -586,7 +592,7 @@ __global__ __launch_bounds__(kJoinBlock) void logitsJoinKernel(LogitsForward a, 
     const float4 part = lane < seg.count ? seg.stats(a)[r * seg.count + lane] : float4{kLowest, 0.0f, 0.0f, 0.0f};
     // finished statistics: M is m k exactly
     Stat all = {waveMax(part.x), 0.0f, 0.0f};
-    const Stat mine = raised({part.x, part.y, part.z}, all.m, timesK(all.m - part.x, k, a.scale));
+    const Stat mine = raised({part.x, part.y, part.z}, all.m, -differenceTimesK(part.x, all.m, k, a.scale));
     all.s = laneSum<64>(mine.s);
     all.t = laneSum<64>(mine.t);
     const RowResult res = rowResult(all, a.scale);

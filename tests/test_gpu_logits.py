@@ -867,3 +867,21 @@ def test_distill_of_more_scores_than_caches_hold(bfo, rows, V, dt):
         near(stats[part, 0], ref["m"], U * ref["m"].abs(), "max")
         near(stats[part, 1], ref["logs"], ref["rel"], "log sum")
         near(lp[part], ref["at"], ref["at_tol"], "logprob")
+
+
+@pytest.mark.parametrize("V", [100, 70001])
+@pytest.mark.parametrize("scale", [1e-45, 1e-40, 1e-38, 1e-30])
+def test_smallest_scales(bfo, V, scale):
+    """Down to subnormal scales, whose product with log2(e) is off by up to 2^-150: 2^-22 of an exponent."""
+    logits = torch.full((3, V), 1e30, device=DEV)
+    logits[1] = torch.linspace(-3e38, 3e38, V, dtype=torch.float64).float().to(DEV)
+    logits[2] = torch.linspace(-1, 1, V, device=DEV)
+    targets = torch.tensor([0, 7, -1], dtype=torch.int32, device=DEV)
+    check_forward(run_forward(bfo, logits, targets, V, scale, 20), logits, targets, V, scale, 20)
+    # a teacher of such scores
+    index = torch.arange(30, dtype=torch.int32, device=DEV).repeat(3, 1) * 3
+    value = torch.gather(logits, 1, index.long()).neg().contiguous()
+    kl, _, lp = run_distill(bfo, logits, index, value, V, scale, targets)
+    ref, _, _, _, want, tol = distill_reference(logits, V, scale, index, value, targets)
+    near(kl, want, tol, "kl")
+    near(lp, ref["at"], ref["at_tol"], "logprob")
