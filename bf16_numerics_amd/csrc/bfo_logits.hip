@@ -42,17 +42,16 @@ struct Stat {
 constexpr float kReferenceMost = 1024.0f, kReferenceFloor = -2048.0f;
 __device__ __forceinline__ float referenceOf(float m, float k) { return fmaxf(m * k, kReferenceFloor); }
 
-// (x - m) f, also where only the difference is past binary32 (scores of 2^127
-// and more with both signs, and a small factor).
-__device__ __forceinline__ float scaledDifference(float x, float m, float f) {
-    const float d = x - m;
-    return fabsf(d) < INFINITY ? d * f : (0.5f * x - 0.5f * m) * f * 2.0f;
+// (x - m) times the scale.
+__device__ __forceinline__ float scaledDifference(float x, float m, const DifferenceScale &by) {
+    return fmaf(x, by.part, -(m * by.part)) * by.rest;
 }
 // (x - m) k.  From scales of 2^128 / log2(e) on k is infinite, and no reference
 // holds (m k is infinite or, for m = 0, NaN): such rows are exactStat's, by this
 // product in its parts.
 __device__ __forceinline__ float differenceTimesK(float x, float m, float k, float scale) {
-    return k < INFINITY ? scaledDifference(x, m, k) : (x - m) * scale * kLog2e;
+    const float d = x - m;
+    return k < INFINITY ? d * k : d * scale * kLog2e;
 }
 
 // The set's s and t for an M that is `up` larger.
@@ -285,6 +284,8 @@ __device__ __forceinline__ Stat blockJoined(const Stat &wave, Stat (&stats)[kBlo
 
 // A finished Stat of a row with maximum m by differences from m, which are
 // exact where products with k are not: for the rows that referenceOf is not for.
+// (One past binary32 is right as -inf: |m k| >= kReferenceMost leaves no k small
+// enough for its exponential to be above 0.)
 template <typename T, int kBlock>
 __device__ __noinline__ Stat exactStat(const T *row, uint32_t V, float m, float k, float scale,
                                        Stat (&stats)[kBlock / 64]) {
@@ -380,15 +381,15 @@ __device__ __forceinline__ RowResult rowResult(const Stat &a, float scale) {
     return r;
 }
 // log probability of score x.
-__device__ __forceinline__ float logProb(const RowResult &r, float x, float scale) {
+__device__ __forceinline__ float logProb(const RowResult &r, float x, const DifferenceScale &by) {
     if (r.empty) return -INFINITY;
-    return r.finite ? scaledDifference(x, r.m, scale) - r.logs : NAN;
+    return r.finite ? scaledDifference(x, r.m, by) - r.logs : NAN;
 }
 
 __device__ __forceinline__ void writeTop(const LogitsForward &a, uint64_t r, const RowResult &res, uint64_t key,
                                          uint32_t place) {
     a.topIndex[r * a.top + place] = int32_t(0xFFFFFFFFu - uint32_t(key));
-    a.topLogprob[r * a.top + place] = logProb(res, ofKey(uint32_t(key >> 32)), a.scale);
+    a.topLogprob[r * a.top + place] = logProb(res, ofKey(uint32_t(key >> 32)), a.difference);
 }
 
 // Calls put(key, place) for the top: keys are unique, so a candidate's place
@@ -439,13 +440,13 @@ struct Teacher {
             x[i] = id[i] >= 0 ? logits[j] : -INFINITY;
         }
     }
-    __device__ __forceinline__ void softmax(float scale) {
+    __device__ __forceinline__ void softmax(const DifferenceScale &by) {
         any = __ballot(id[0] >= 0 || id[1] >= 0) != 0;
         const float m = fmaxf(waveMax(fmaxf(x[0], x[1])), kLowest);
         float e[2], s = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            e[i] = exp2Fast(scaledDifference(x[i], m, scale) * kLog2e);
+            e[i] = exp2Fast(scaledDifference(x[i], m, by) * kLog2e);
             s += e[i];
         }
         s = laneSum<64>(s);
@@ -456,7 +457,7 @@ struct Teacher {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             q[i] = any && id[i] >= 0 ? e[i] / s : 0.0f;
-            logq[i] = scaledDifference(x[i], m, scale) - ls;
+            logq[i] = scaledDifference(x[i], m, by) - ls;
         }
     }
 };
@@ -494,19 +495,19 @@ struct RowEnd {
             if (a.logprob)
                 a.logprob[r] = target < 0            ? 0.0f
                                : uint32_t(target) >= V ? NAN
-                                                       : logProb(res, targetScore, a.scale);
+                                                       : logProb(res, targetScore, a.difference);
             if (entropy) a.entropy[r] = res.empty ? 0.0f : res.finite ? res.logs - kLn2 * (res.t / res.s) : NAN;
         }
         if constexpr (kTeacher) {
             if (threadIdx.x < 64) {
-                teacher.softmax(a.scale);
+                teacher.softmax(a.difference);
                 float kl = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (teacher.id[i] < 0) continue;
                     if (uint32_t(teacher.id[i]) >= V) kl = NAN;
                     else if (teacher.q[i] != 0.0f)
-                        kl += teacher.q[i] * (teacher.logq[i] - logProb(res, teacherScore[i], a.scale));
+                        kl += teacher.q[i] * (teacher.logq[i] - logProb(res, teacherScore[i], a.difference));
                 }
                 kl = laneSum<64>(kl);
                 if (threadIdx.x == 0) a.kl[r] = kl;
@@ -592,7 +593,9 @@ __global__ __launch_bounds__(kJoinBlock) void logitsJoinKernel(LogitsForward a, 
     const float4 part = lane < seg.count ? seg.stats(a)[r * seg.count + lane] : float4{kLowest, 0.0f, 0.0f, 0.0f};
     // finished statistics: M is m k exactly
     Stat all = {waveMax(part.x), 0.0f, 0.0f};
-    const Stat mine = raised({part.x, part.y, part.z}, all.m, -differenceTimesK(part.x, all.m, k, a.scale));
+    const float d = all.m - part.x, up = d < INFINITY ? differenceTimesK(all.m, part.x, k, a.scale)
+                                                      : scaledDifference(all.m, part.x, a.difference) * kLog2e;
+    const Stat mine = raised({part.x, part.y, part.z}, all.m, up);
     all.s = laneSum<64>(mine.s);
     all.t = laneSum<64>(mine.t);
     const RowResult res = rowResult(all, a.scale);
@@ -725,7 +728,7 @@ __global__ __launch_bounds__(kBackBlock) void logitsBackwardKernel(LogitsBackwar
                 Teacher te;
                 if (threadIdx.x < 64) {
                     te.load(a.teacherIndex + r * a.count, a.teacherLogits + r * a.count, a.count);
-                    te.softmax(a.scale);
+                    te.softmax(a.difference);
                 }
                 __syncthreads();
                 if (threadIdx.x < 64) buildChains(ch, te, dkl, uint32_t(V), c0, end, E);

@@ -56,6 +56,15 @@ struct LayerNormBackward {
 };
 hipError_t launchLayerNormBackward(const LayerNormBackward &a, hipStream_t stream);
 
+// The scale of a difference of scores, as (x part - m part) rest: by halves below
+// 1, where a difference past binary32 may have a product that is not.
+struct DifferenceScale {
+    float part, rest;
+};
+inline DifferenceScale differenceScale(float scale) {
+    return scale < 1.0f ? DifferenceScale{0.5f, 2.0f * scale} : DifferenceScale{1.0f, scale};
+}
+
 // The forward pass over the scores: token log probabilities (count == 0) and
 // distillation (count > 0; top == 0).
 struct LogitsForward {
@@ -63,6 +72,7 @@ struct LogitsForward {
     uint64_t rows;
     uint32_t vocab;
     float scale;
+    DifferenceScale difference;
     const int32_t *targets;
     float *logprob, *stats, *entropy;
     uint32_t top;
@@ -84,6 +94,7 @@ struct LogitsBackward {
     uint64_t rows;
     uint32_t vocab, width;
     float scale;
+    DifferenceScale difference;
     const int32_t *targets;
     const float *stats, *entropy, *dlogprob, *dentropy;
     const int32_t *teacherIndex;
