@@ -649,14 +649,13 @@ def checkpoint_load(directory, step, table, m, v, master=None, params=None):
 _DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _u32(n):
-    """A size for a 32-bit argument; ctypes would pass a larger one's low word,
-    so those become the largest, which is out of every range."""
-    return n if 0 <= n <= 0xFFFFFFFF else 0xFFFFFFFF
+# Of a size past an argument's type, ctypes would pass the low word: those
+# become the type's largest, which is out of every range.
+_U32, _U64 = 0xFFFFFFFF, 0xFFFFFFFFFFFFFFFF
 
 
-def _u64(n):
-    return n if 0 <= n <= 0xFFFFFFFFFFFFFFFF else 0xFFFFFFFFFFFFFFFF
+def _sized(n, most):
+    return n if 0 <= n <= most else most
 
 
 def _matrix(t, name):
@@ -750,7 +749,7 @@ def layernorm_workspace_bytes(rows, cols):
     """Device bytes layernorm_backward of these sizes, or of smaller ones, needs as workspace."""
     out = ctypes.c_uint64(0)
     _check("bfo_layernorm_workspace_bytes",
-           _lib().bfo_layernorm_workspace_bytes(_u64(rows), _u32(cols), ctypes.byref(out)))
+           _lib().bfo_layernorm_workspace_bytes(_sized(rows, _U64), _sized(cols, _U32), ctypes.byref(out)))
     return out.value
 
 
@@ -768,8 +767,8 @@ def layernorm_forward(x, weight, bias, out, mean=None, rstd=None, eps=1e-5):
     pt = _param_type(weight)
     _launch("layernorm_forward", dev, xp, xs, _vector(weight, pt, cols, "weight", dev),
             _vector(bias, pt, cols, "bias", dev), op, os_, _vector(mean, torch.float32, rows, "mean", dev),
-            _vector(rstd, torch.float32, rows, "rstd", dev), rows, _u32(cols), eps, _DTYPE_CODES[x.dtype],
-            _DTYPE_CODES[pt])
+            _vector(rstd, torch.float32, rows, "rstd", dev), rows, cols if cols < _U32 else _U32, eps,
+            _DTYPE_CODES[x.dtype], _DTYPE_CODES[pt])
 
 
 def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, workspace=None, accumulate_dx=False,
@@ -787,8 +786,8 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, wor
     db = _vector(dbias, pt, cols, "dbias", dev)
     ws = _workspace_ptr(workspace, layernorm_workspace_bytes(rows, cols), dev, "new_layernorm_workspace")
     _launch("layernorm_backward", dev, gp, gs, xp, xs, w, _vector(mean, torch.float32, rows, "mean", dev),
-            _vector(rstd, torch.float32, rows, "rstd", dev), dp, ds, dw, db, rows, _u32(cols), _DTYPE_CODES[x.dtype],
-            _DTYPE_CODES[pt],
+            _vector(rstd, torch.float32, rows, "rstd", dev), dp, ds, dw, db, rows, cols if cols < _U32 else _U32,
+            _DTYPE_CODES[x.dtype], _DTYPE_CODES[pt],
             (ACCUMULATE_DX if accumulate_dx else 0) | (ACCUMULATE_PARAMS if accumulate_params else 0), ws)
 
 
@@ -798,7 +797,8 @@ def logits_workspace_bytes(rows, vocab, top=0):
     sizes, or of smaller ones, need."""
     out = ctypes.c_uint64(0)
     _check("bfo_logits_workspace_bytes",
-           _lib().bfo_logits_workspace_bytes(_u64(rows), _u32(vocab), _u32(top), ctypes.byref(out)))
+           _lib().bfo_logits_workspace_bytes(_sized(rows, _U64), _sized(vocab, _U32), _sized(top, _U32),
+                                             ctypes.byref(out)))
     return out.value
 
 
@@ -807,17 +807,12 @@ def new_logits_workspace(rows, vocab, top, device):
     return torch.empty(max(16, logits_workspace_bytes(rows, vocab, top)), dtype=torch.uint8, device=device)
 
 
-def _logits_workspace(workspace, rows, vocab, top, dev):
-    need = logits_workspace_bytes(rows, vocab, top) if rows <= SPLIT_ROWS else 0
-    return _workspace_ptr(workspace, need, dev, "new_logits_workspace")
-
-
 def _vocab(vocab, cols):
     if vocab is None:
-        return _u32(cols)
-    if not 0 < vocab <= cols:
+        vocab = cols
+    elif not 0 < vocab <= cols:
         raise ValueError(f"vocab is {vocab}, the rows have {cols} columns")
-    return _u32(vocab)
+    return vocab if vocab < _U32 else _U32
 
 
 def _columns(t, name, rows):
@@ -842,11 +837,12 @@ def token_logprobs_forward(logits, targets=None, logprob=None, stats=None, entro
     top = 0
     if top_index is not None:
         top = _columns(top_index, "top_index", rows)
-    ws = _logits_workspace(workspace, rows, v, top, dev)
+    ws = _workspace_ptr(workspace, logits_workspace_bytes(rows, v, top) if rows <= SPLIT_ROWS else 0, dev,
+                        "new_logits_workspace")
     _launch("token_logprobs_forward", dev, lp, ls, rows, v, _DTYPE_CODES[logits.dtype], scale,
             _vector(targets, torch.int32, rows, "targets", dev), _vector(logprob, torch.float32, rows, "logprob", dev),
             _vector(stats, torch.float32, 2 * rows, "stats", dev),
-            _vector(entropy, torch.float32, rows, "entropy", dev), _u32(top),
+            _vector(entropy, torch.float32, rows, "entropy", dev), top if top < _U32 else _U32,
             _vector(top_index, torch.int32, rows * top, "top_index", dev),
             _vector(top_logprob, torch.float32, rows * top, "top_logprob", dev), ws)
 
@@ -859,7 +855,7 @@ def token_logprobs_backward(logits, targets, stats, dlogprob, dlogits, entropy=N
     lp, ls, rows, cols = _matrix(logits, "logits")
     dev = logits.device
     dp, ds = _matrix_like(dlogits, "dlogits", logits.dtype, dev, rows, cols)
-    _launch("token_logprobs_backward", dev, lp, ls, rows, _vocab(vocab, cols), _u32(cols),
+    _launch("token_logprobs_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols if cols < _U32 else _U32,
             _DTYPE_CODES[logits.dtype], scale, _vector(targets, torch.int32, rows, "targets", dev),
             _vector(stats, torch.float32, 2 * rows, "stats", dev),
             _vector(entropy, torch.float32, rows, "entropy", dev),
@@ -870,7 +866,8 @@ def token_logprobs_backward(logits, targets, stats, dlogprob, dlogits, entropy=N
 def _teacher(teacher_index, teacher_logits, rows, dev):
     count = _columns(teacher_index, "teacher_index", rows)
     return (_vector(teacher_index, torch.int32, rows * count, "teacher_index", dev),
-            _vector(teacher_logits, torch.float32, rows * count, "teacher_logits", dev), _u32(count))
+            _vector(teacher_logits, torch.float32, rows * count, "teacher_logits", dev),
+            count if count < _U32 else _U32)
 
 
 def distill_forward(logits, teacher_index, teacher_logits, kl, stats=None, targets=None, logprob=None, vocab=None,
@@ -884,7 +881,8 @@ def distill_forward(logits, teacher_index, teacher_logits, kl, stats=None, targe
     dev = logits.device
     v = _vocab(vocab, cols)
     ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
-    ws = _logits_workspace(workspace, rows, v, 0, dev)
+    ws = _workspace_ptr(workspace, logits_workspace_bytes(rows, v, 0) if rows <= SPLIT_ROWS else 0, dev,
+                        "new_logits_workspace")
     _launch("distill_forward", dev, lp, ls, rows, v, _DTYPE_CODES[logits.dtype], scale, ti, tl, count,
             _vector(targets, torch.int32, rows, "targets", dev), _vector(kl, torch.float32, rows, "kl", dev),
             _vector(logprob, torch.float32, rows, "logprob", dev),
@@ -899,8 +897,8 @@ def distill_backward(logits, teacher_index, teacher_logits, stats, dkl, dlogits,
     dev = logits.device
     dp, ds = _matrix_like(dlogits, "dlogits", logits.dtype, dev, rows, cols)
     ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
-    _launch("distill_backward", dev, lp, ls, rows, _vocab(vocab, cols), _u32(cols), _DTYPE_CODES[logits.dtype], scale,
-            ti, tl, count, _vector(targets, torch.int32, rows, "targets", dev),
+    _launch("distill_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols if cols < _U32 else _U32,
+            _DTYPE_CODES[logits.dtype], scale, ti, tl, count, _vector(targets, torch.int32, rows, "targets", dev),
             _vector(stats, torch.float32, 2 * rows, "stats", dev),
             _vector(dkl, torch.float32, rows, "dkl", dev),
             _vector(dlogprob, torch.float32, rows, "dlogprob", dev), dp, ds)

@@ -825,8 +825,8 @@ def special_rows(logits, V):
     return logits
 
 
-# (rows, vocabulary, type): a kept maximum covers two or three chunks of a lane's columns, with 512 lanes, with 256, with
-# 256 and nontemporal loads, and in segments; then one chunk with nontemporal loads in binary32.
+# (rows, vocabulary, type): a kept maximum covers two or three chunks of a lane's columns, with 512 lanes, with 256,
+# with 256 and nontemporal loads, and in segments; then one chunk with nontemporal loads in binary32.
 LONG = [(130, 131072, "bf16"), (200, 131071, "f32"), (520, 60001, "bf16"), (520, 30001, "f32"), (600, 65537, "bf16"),
         (600, 50257, "f32"), (9, 1 << 20, "bf16"), (9, (1 << 20) + 77, "f32"), (3001, 20011, "f32")]
 
