@@ -364,11 +364,14 @@ struct BackwardShape {
     static constexpr int kRows = kBlock / kLanes;
 };
 
-// Up to here one launch for all gradients is faster than rows and partials: 2,048
-// rows of 1,600 bf16 9.3 us against 11.3 (fp32 12.3 against 12.8; of 801 11.5
-// against 10.4), 1,024 of 4,096 9.3 against 16.1 (fp32 14.0 and 16.3), 512 of 8,192
-// 10.1 against 12, one row of 1,600 2.9 against 5.0.  Twice as many are slower: a
-// column workgroup walks all rows by itself.
+// Up to here one launch for all gradients takes no longer than rows and partials,
+// as called from Python on inputs that no cache holds: 2,048 rows of 1,600 bf16
+// 12.4 us against 13.9 for 2,049 (fp32 15.2 and 15.7), of 801 11.3 and 13.9 (fp32
+// 13.4 and 13.7, where the kernels alone take 11.5 and 10.4); kernels alone, 1,024
+// of 4,096 9.3 against 16.1 (fp32 14.0 and 16.3), 512 of 8,192 10.1 against 12, one
+// row of 1,600 2.9 against 5.0.  Twice as many are slower: a column workgroup walks
+// all rows by itself.  The limit goes by columns, as the workspace's size does,
+// which knows no type.
 uint64_t fewRows(uint32_t cols) { return cols <= 2048 ? 2048 : cols <= 4096 ? 1024 : 512; }
 // Workgroups of narrow slabs walk more rows at a time, and are more: 1,024 rows of 1,600 bf16 6.3 us with 16 columns,
 // 5.7 with 8, but 256 rows 3.2 and 3.6; 512 rows of 4,096 6.4 with 32, 5.4 with 16;

@@ -11,7 +11,7 @@
 // and log sum.
 //
 // On an MI355X, bf16: 8192 x 50257 scores forward in 124 us (6.6 TB/s, bound by
-// memory), in 142 with entropy and 20 alternatives (bound by the vector ALUs, 85%
+// memory), in 142 with entropy and 20 alternatives (bound by the vector ALUs, 83-88%
 // busy), gradient of 8192 x 50304 in 262 us (6.0 TB/s read and written).
 #include <type_traits>
 
@@ -91,8 +91,9 @@ constexpr uint32_t chunkElems() {
 }
 
 // Chunks are cut on 128-byte lines of memory, not from the row's first column
-// (odd rows 145 us for 167-172): the columns of a row's first line that come
-// before the row.  Which lane sums which column thus depends on the row's start.
+// (8192 x 50257 bf16 of odd rows 129 us for 171): the columns of a row's first line
+// that come before the row.  Which lane sums which column thus depends on the row's
+// start.
 template <typename T>
 __device__ __forceinline__ int leadOf(const T *row) {
     return int((reinterpret_cast<uintptr_t>(row) & 127u) / sizeof(T));
@@ -102,7 +103,13 @@ constexpr uint32_t kMaxLead = 128 / sizeof(T) - 1;
 
 constexpr uint32_t kNoScores = 0xFFFF;  // upper half of a NaN, which reaches no bound
 constexpr int kGroups = 256;           // groups of lanes whose maxima bound the top
-constexpr int kSlots = 28;             // stretches of a lane's chunks whose maxima are kept
+// Stretches of a lane's chunks whose maxima are kept.  Stretches of one chunk are
+// the best (8192 x 50257 bf16, 20 best, at an earlier step: 157 us, of several 162).
+// 28 are seven steps of four chunks, the most steps that leave LDS for the seven
+// workgroups a CU has registers for (22 of 160 KB each): one chunk each up to 57,344
+// bf16 or 28,672 fp32 scores with 256 lanes.  Longer rows keep a maximum of several:
+// 4096 x 128256 bf16 with 20 best 174 us, 6.0 TB/s.
+constexpr int kSlots = 28;
 constexpr uint32_t kCandidates = 512;  // scores the top is picked from
 
 template <int kBlock>
@@ -139,7 +146,10 @@ __device__ __forceinline__ float boundOf(const uint32_t *keys, uint32_t top) {
 
 // The row's exact top, whatever it holds: the top-th key by four rounds of
 // 256 bins, then the keys above it and the first equal ones in index order.
-// For rows that the bound does not thin out (many equal scores, NaN).
+// For rows that the bound does not thin out (many equal scores, NaN, fewer
+// finite scores than asked for).  Five passes of one score a lane: 8192 x 50257
+// bf16 of nothing but such rows 5.8 ms against 145 us, one row of 32,000 184 us
+// against 9.
 template <typename T, int kBlock>
 __device__ __noinline__ void exactTop(const T *row, uint32_t V, uint32_t top, TopShared<kBlock> &sh) {
     uint32_t prefix = 0, need = top;
