@@ -209,8 +209,8 @@ int token_logprobs_forward(const void *logits, uint64_t stride, uint64_t rows, u
     if (rows && ((targets != nullptr) != (logprob != nullptr) || (top != 0) != (top_index != nullptr) ||
                  (top != 0) != (top_logprob != nullptr)))
         return BFO_EINVAL;
-    const bfo::LogitsForward a{{logits, stride}, rows, vocab, scale, bfo::differenceScale(scale), targets, logprob, stats, entropy, top, top_index,
-                               top_logprob, nullptr, nullptr, 0, nullptr, workspace};
+    const bfo::LogitsForward a{{logits, stride}, rows, vocab, scale, bfo::differenceScale(scale), targets, logprob,
+                               stats, entropy, top, top_index, top_logprob, nullptr, nullptr, 0, nullptr, workspace};
     return forwardPass(a, dtype, stream);
 }
 
@@ -223,8 +223,8 @@ int token_logprobs_backward(const void *logits, uint64_t stride, uint64_t rows, 
     if (rows && ((targets != nullptr) != (dlogprob != nullptr) || (entropy != nullptr) != (dentropy != nullptr) ||
                  (!targets && !entropy) || !stats))
         return BFO_EINVAL;
-    const bfo::LogitsBackward a{{logits, stride}, {dlogits, dlogits_stride}, rows, vocab, width, scale, bfo::differenceScale(scale), targets, stats,
-                                entropy, dlogprob, dentropy, nullptr, nullptr, 0, nullptr};
+    const bfo::LogitsBackward a{{logits, stride}, {dlogits, dlogits_stride}, rows, vocab, width, scale,
+                                bfo::differenceScale(scale), targets, stats, entropy, dlogprob, dentropy, nullptr, nullptr, 0, nullptr};
     return backwardPass(a, dtype, stream);
 }
 
@@ -238,8 +238,8 @@ int distill_forward(const void *logits, uint64_t stride, uint64_t rows, uint32_t
     if (count > BFO_TOP_MAX) return BFO_ERANGE;
     if (rows && (!teacher_index || !teacher_logits || !kl || (targets != nullptr) != (logprob != nullptr)))
         return BFO_EINVAL;
-    const bfo::LogitsForward a{{logits, stride}, rows, vocab, scale, bfo::differenceScale(scale), targets, logprob, stats, nullptr, 0, nullptr,
-                               nullptr, teacher_index, teacher_logits, count, kl, workspace};
+    const bfo::LogitsForward a{{logits, stride}, rows, vocab, scale, bfo::differenceScale(scale), targets, logprob,
+                               stats, nullptr, 0, nullptr, nullptr, teacher_index, teacher_logits, count, kl, workspace};
     return forwardPass(a, dtype, stream);
 }
 
@@ -253,8 +253,8 @@ int distill_backward(const void *logits, uint64_t stride, uint64_t rows, uint32_
     if (count > BFO_TOP_MAX) return BFO_ERANGE;
     if (rows && (!teacher_index || !teacher_logits || !dkl || !stats || (targets != nullptr) != (dlogprob != nullptr)))
         return BFO_EINVAL;
-    const bfo::LogitsBackward a{{logits, stride}, {dlogits, dlogits_stride}, rows, vocab, width, scale, bfo::differenceScale(scale), targets, stats,
-                                nullptr, dlogprob, nullptr, teacher_index, teacher_logits, count, dkl};
+    const bfo::LogitsBackward a{{logits, stride}, {dlogits, dlogits_stride}, rows, vocab, width, scale,
+                                bfo::differenceScale(scale), targets, stats, nullptr, dlogprob, nullptr, teacher_index, teacher_logits, count, dkl};
     return backwardPass(a, dtype, stream);
 }
 
