@@ -224,7 +224,8 @@ int token_logprobs_backward(const void *logits, uint64_t stride, uint64_t rows, 
                  (!targets && !entropy) || !stats))
         return BFO_EINVAL;
     const bfo::LogitsBackward a{{logits, stride}, {dlogits, dlogits_stride}, rows, vocab, width, scale,
-                                bfo::differenceScale(scale), targets, stats, entropy, dlogprob, dentropy, nullptr, nullptr, 0, nullptr};
+                                bfo::differenceScale(scale), targets, stats, entropy, dlogprob, dentropy, nullptr,
+                                nullptr, 0, nullptr};
     return backwardPass(a, dtype, stream);
 }
 
@@ -239,7 +240,8 @@ int distill_forward(const void *logits, uint64_t stride, uint64_t rows, uint32_t
     if (rows && (!teacher_index || !teacher_logits || !kl || (targets != nullptr) != (logprob != nullptr)))
         return BFO_EINVAL;
     const bfo::LogitsForward a{{logits, stride}, rows, vocab, scale, bfo::differenceScale(scale), targets, logprob,
-                               stats, nullptr, 0, nullptr, nullptr, teacher_index, teacher_logits, count, kl, workspace};
+                               stats, nullptr, 0, nullptr, nullptr, teacher_index, teacher_logits, count, kl,
+                               workspace};
     return forwardPass(a, dtype, stream);
 }
 
@@ -254,7 +256,8 @@ int distill_backward(const void *logits, uint64_t stride, uint64_t rows, uint32_
     if (rows && (!teacher_index || !teacher_logits || !dkl || !stats || (targets != nullptr) != (dlogprob != nullptr)))
         return BFO_EINVAL;
     const bfo::LogitsBackward a{{logits, stride}, {dlogits, dlogits_stride}, rows, vocab, width, scale,
-                                bfo::differenceScale(scale), targets, stats, nullptr, dlogprob, nullptr, teacher_index, teacher_logits, count, dkl};
+                                bfo::differenceScale(scale), targets, stats, nullptr, dlogprob, nullptr,
+                                teacher_index, teacher_logits, count, dkl};
     return backwardPass(a, dtype, stream);
 }
 
