@@ -43,7 +43,10 @@ EXPORTS = ("shard_range", "bfo_table_create", "bfo_table_create_layout", "bfo_ta
            "bfo_checksum64", "adamw_sr_step_with_norm",
            "layernorm_forward", "bfo_layernorm_workspace_bytes", "layernorm_backward",
            "bfo_logits_workspace_bytes", "token_logprobs_forward", "token_logprobs_backward",
-           "distill_forward", "distill_backward")
+           "distill_forward", "distill_backward",
+           "rmsnorm_forward", "bfo_rmsnorm_workspace_bytes", "rmsnorm_backward",
+           "activation_forward", "activation_backward", "activation_pack", "activation_unpack",
+           "bfo_rotary_frequencies", "rotary_apply")
 
 LR_CONSTANT, LR_LINEAR, LR_COSINE, LR_WSD = 0, 1, 2, 3
 
@@ -52,6 +55,15 @@ ACCUMULATE_DX, ACCUMULATE_PARAMS = 1, 2
 LAYERNORM_MAX_COLS = 16384
 TOP_MAX = 128
 VOCAB_MAX = 1 << 28
+I8, E4M3 = 0, 1
+GROUP = 128
+CODES_OF_OUT, CODES_OF_NORMALISED = 0, 1
+RMSNORM_MAX_COLS = 16384
+SILU, GELU = 0, 1
+ACTIVATION_MAX_COLS = 1 << 28
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+ROTARY_UNSCALED, ROTARY_LINEAR, ROTARY_BASE, ROTARY_BY_TURNS, ROTARY_BY_PAIR = 0, 1, 2, 3, 4
+ROTARY_MAX_DIM, ROTARY_MAX_HEADS = 1024, 65535
 SPLIT_ROWS = 128  # forward passes over the vocabulary use a workspace up to here only
 
 
@@ -80,6 +92,12 @@ class LrSchedule(ctypes.Structure):
 class StepScalars(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("bc1", ctypes.c_float), ("bc2", ctypes.c_float),
                 ("reserved", ctypes.c_uint32), ("t", ctypes.c_uint64), ("seed", ctypes.c_uint64)]
+
+
+class RotaryScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_uint32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("length", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
 
 
 NORM_RESULT_BYTES = 16  # bfo_norm_result: double sumsq; float norm; float scale
@@ -152,6 +170,18 @@ def _lib():
         "token_logprobs_backward": (i32, [vp, u64, u64, u32, u32, i32, f32, vp, vp, vp, vp, vp, vp, u64, vp]),
         "distill_forward": (i32, [vp, u64, u64, u32, i32, f32, vp, vp, u32, vp, vp, vp, vp, vp, vp]),
         "distill_backward": (i32, [vp, u64, u64, u32, u32, i32, f32, vp, vp, u32, vp, vp, vp, vp, vp, u64, vp]),
+        "rmsnorm_forward": (i32, [vp, u64, vp, u64, vp, vp, u64, vp, u64, vp, vp, u64, vp, i32, i32, u32, u64, u32, f32,
+                                  i32, i32, vp]),
+        "bfo_rmsnorm_workspace_bytes": (i32, [u64, u32, pu64]),
+        "rmsnorm_backward": (i32, [vp, u64, vp, u64, vp, u64, vp, i32, u32, vp, vp, vp, u64, vp, vp, u64, u64, u32, i32,
+                                   i32, i32, vp, vp]),
+        "activation_forward": (i32, [vp, u64, vp, u64, vp, u64, vp, u64, vp, vp, u64, vp, i32, u64, u32, i32, i32, vp]),
+        "activation_backward": (i32, [vp, u64, vp, u64, vp, u64, vp, u64, vp, vp, u64, vp, i32, vp, u64, vp, u64, vp, u64,
+                                      u64, u32, i32, i32, vp]),
+        "activation_pack": (i32, [vp, u64, vp, u64, vp, i32, u64, u32, i32, vp]),
+        "activation_unpack": (i32, [vp, u64, vp, i32, u32, vp, u64, u64, u32, i32, vp]),
+        "bfo_rotary_frequencies": (i32, [ctypes.POINTER(RotaryScaling), u32, ctypes.POINTER(ctypes.c_double)]),
+        "rotary_apply": (i32, [vp, u64, u64, vp, u64, u64, u64, u32, u32, u32, i32, vp, vp, u64, f32, i32, i32, vp]),
         "bfo_status_string": (ctypes.c_char_p, [i32]),
         "bfo_last_hip_error": (i32, []),
     }
@@ -902,3 +932,202 @@ def distill_backward(logits, teacher_index, teacher_logits, stats, dkl, dlogits,
             _vector(stats, torch.float32, 2 * rows, "stats", dev),
             _vector(dkl, torch.float32, rows, "dkl", dev),
             _vector(dlogprob, torch.float32, rows, "dlogprob", dev), dp, ds)
+
+
+# --------------------------------------------------------------------------
+# Operators between a transformer block's matrix products (RMS norm, the
+# feed-forward's activation, rotary positions).  Codes are a matrix of
+# torch.int8 or torch.float8_e4m3fn, their scales a float32 tensor of one
+# column for every GROUP columns of the codes, or of one column for whole rows.
+# --------------------------------------------------------------------------
+
+_CODE_TYPES = {torch.int8: I8, torch.float8_e4m3fn: E4M3}
+_NO_MATRIX = (None, 0)
+_NO_CODES = (None, 0, None, I8, GROUP)
+
+
+def _optional_matrix(t, name, dtype, dev, rows, cols):
+    return _NO_MATRIX if t is None else _matrix_like(t, name, dtype, dev, rows, cols)
+
+
+def _codes(codes, scales, name, dev, rows, cols, whole_row=False):
+    """(device pointer, row stride, scales' pointer, code type, columns of a
+    group) of codes of a rows x cols matrix, or of none."""
+    if codes is None and scales is None:
+        return _NO_CODES
+    if not isinstance(codes, torch.Tensor) or codes.dtype not in _CODE_TYPES:
+        raise TypeError(f"{name} must be a torch.int8 or torch.float8_e4m3fn tensor")
+    p, stride = _matrix_like(codes, name, codes.dtype, dev, rows, cols)
+    groups = (cols + GROUP - 1) // GROUP
+    per_row = whole_row and isinstance(scales, torch.Tensor) and scales.dim() == 2 and scales.shape[1] == 1
+    if per_row:
+        groups = 1
+    sp = _vector(scales, torch.float32, rows * groups, f"the scales of {name}", dev)
+    if sp is None or scales.shape != (rows, groups):
+        raise ValueError(f"the scales of {name} must be a {(rows, groups)} tensor")
+    return p, stride, sp, _CODE_TYPES[codes.dtype], 0 if per_row else GROUP
+
+
+def new_codes(rows, cols, device, dtype=torch.int8, per_row=False):
+    """(codes, scales) for a rows x cols matrix; per_row: one scale a row instead
+    of one for every GROUP columns."""
+    if dtype not in _CODE_TYPES:
+        raise TypeError("dtype must be torch.int8 or torch.float8_e4m3fn")
+    groups = 1 if per_row else (cols + GROUP - 1) // GROUP
+    return (torch.empty(rows, cols, dtype=dtype, device=device),
+            torch.empty(rows, groups, dtype=torch.float32, device=device))
+
+
+def rmsnorm_forward(x, weight, out=None, residual=None, total=None, rstd=None, codes=None, scales=None,
+                    codes_of=CODES_OF_NORMALISED, eps=1e-5):
+    """total = x + residual, rstd = 1 / sqrt(mean(total^2) + eps) and out =
+    total * rstd * weight per row; codes and scales keep out (CODES_OF_OUT) or
+    total * rstd (CODES_OF_NORMALISED) in 8 bits.  Every output but the ones
+    wanted may be None; total may be x or residual."""
+    xp, xs, rows, cols = _matrix(x, "x")
+    dev, dt = x.device, x.dtype
+    pt = _param_type(weight)
+    cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
+    _launch("rmsnorm_forward", dev, xp, xs, *_optional_matrix(residual, "residual", dt, dev, rows, cols),
+            _vector(weight, pt, cols, "weight", dev), *_optional_matrix(total, "total", dt, dev, rows, cols),
+            *_optional_matrix(out, "out", dt, dev, rows, cols), _vector(rstd, torch.float32, rows, "rstd", dev),
+            cp, cs, sp, ct, codes_of, group, rows, cols if cols < _U32 else _U32, eps, _DTYPE_CODES[dt],
+            _DTYPE_CODES[pt])
+
+
+@functools.lru_cache(maxsize=4096)
+def rmsnorm_workspace_bytes(rows, cols):
+    """Device bytes rmsnorm_backward of these sizes, or of smaller ones, needs as workspace."""
+    out = ctypes.c_uint64(0)
+    _check("bfo_rmsnorm_workspace_bytes",
+           _lib().bfo_rmsnorm_workspace_bytes(_sized(rows, _U64), _sized(cols, _U32), ctypes.byref(out)))
+    return out.value
+
+
+def new_rmsnorm_workspace(rows, cols, device):
+    """A device buffer for rmsnorm_backward of up to rows x cols matrices (at least 16 bytes)."""
+    return torch.empty(max(16, rmsnorm_workspace_bytes(rows, cols)), dtype=torch.uint8, device=device)
+
+
+def rmsnorm_backward(dout, x, weight, rstd, dx, dweight, codes=None, scales=None, out=None, workspace=None,
+                     accumulate_dx=False, accumulate_params=False):
+    """Gradients of rmsnorm_forward into dx and dweight, from the normalised row
+    x (the forward pass's total), or from its codes (CODES_OF_NORMALISED; x
+    None).  out, unless None, gets the forward pass's out again.  accumulate_*:
+    add to what they hold.  workspace: new_rmsnorm_workspace(rows, cols, device)."""
+    gp, gs, rows, cols = _matrix(dout, "dout")
+    dev, dt = dout.device, dout.dtype
+    if (x is None) == (codes is None):
+        raise ValueError("either x or codes must be given")
+    pt = _param_type(weight)
+    cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
+    ws = _workspace_ptr(workspace, rmsnorm_workspace_bytes(rows, cols), dev, "new_rmsnorm_workspace")
+    _launch("rmsnorm_backward", dev, gp, gs, *_optional_matrix(x, "x", dt, dev, rows, cols), cp, cs, sp, ct, group,
+            _vector(weight, pt, cols, "weight", dev), _vector(rstd, torch.float32, rows, "rstd", dev),
+            *_matrix_like(dx, "dx", dt, dev, rows, cols), _vector(dweight, pt, cols, "dweight", dev),
+            *_optional_matrix(out, "out", dt, dev, rows, cols), rows, cols if cols < _U32 else _U32,
+            _DTYPE_CODES[dt], _DTYPE_CODES[pt],
+            (ACCUMULATE_DX if accumulate_dx else 0) | (ACCUMULATE_PARAMS if accumulate_params else 0), ws)
+
+
+def _code_type(first, second):
+    """The one code type of two matrices, of which the second may be none."""
+    if second[0] is not None and first[3] != second[3]:
+        raise TypeError("gate_codes and up_codes must have the same type")
+    return first[3]
+
+
+def activation_forward(gate, up, out, kind=SILU, gate_codes=None, gate_scales=None, up_codes=None, up_scales=None):
+    """out = act(gate) * up (act(gate) if up is None), act SILU or GELU; the codes
+    and scales keep both inputs in 8 bits for the backward pass.  out may be
+    gate or up."""
+    gp, gs, rows, cols = _matrix(gate, "gate")
+    dev, dt = gate.device, gate.dtype
+    gc = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
+    uc = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
+    _launch("activation_forward", dev, gp, gs, *_optional_matrix(up, "up", dt, dev, rows, cols),
+            *_matrix_like(out, "out", dt, dev, rows, cols), *gc[:3], *uc[:3], _code_type(gc, uc), rows,
+            cols if cols < _U32 else _U32, kind, _DTYPE_CODES[dt])
+
+
+def activation_backward(dout, gate, up, dgate, dup, kind=SILU, gate_codes=None, gate_scales=None, up_codes=None,
+                        up_scales=None, out=None):
+    """Gradients of activation_forward into dgate and dup (None without up), from
+    gate and up or, where those are None, from their codes; out, unless None,
+    gets act(gate) * up again.  Outputs may be dout, gate or up."""
+    op, os_, rows, cols = _matrix(dout, "dout")
+    dev, dt = dout.device, dout.dtype
+    gc = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
+    uc = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
+    _launch("activation_backward", dev, op, os_, *_optional_matrix(gate, "gate", dt, dev, rows, cols),
+            *_optional_matrix(up, "up", dt, dev, rows, cols), *gc[:3], *uc[:3], _code_type(gc, uc),
+            *_matrix_like(dgate, "dgate", dt, dev, rows, cols), *_optional_matrix(dup, "dup", dt, dev, rows, cols),
+            *_optional_matrix(out, "out", dt, dev, rows, cols), rows, cols if cols < _U32 else _U32, kind,
+            _DTYPE_CODES[dt])
+
+
+def activation_pack(x, codes, scales):
+    """x in 8 bits: codes, and a scale for every GROUP columns."""
+    xp, xs, rows, cols = _matrix(x, "x")
+    _launch("activation_pack", x.device, xp, xs, *_codes(codes, scales, "codes", x.device, rows, cols)[:4], rows,
+            cols if cols < _U32 else _U32, _DTYPE_CODES[x.dtype])
+
+
+def activation_unpack(codes, scales, out):
+    """The values that codes stand for, rounded to out's type."""
+    op, os_, rows, cols = _matrix(out, "out")
+    cp, cs, sp, ct, group = _codes(codes, scales, "codes", out.device, rows, cols, whole_row=True)
+    _launch("activation_unpack", out.device, cp, cs, sp, ct, group, op, os_, rows, cols if cols < _U32 else _U32,
+            _DTYPE_CODES[out.dtype])
+
+
+def rotary_frequencies(rotated, base=10000.0, scaling=ROTARY_UNSCALED, factor=1.0, length=0.0, low=0.0, high=0.0,
+                       device=None):
+    """The angle per position of each pair of `rotated` columns (float64), scaled
+    for contexts `factor` times as long as `length` (bfo_rotary_frequencies)."""
+    out = (ctypes.c_double * max(1, min(rotated, ROTARY_MAX_DIM) // 2))()
+    s = RotaryScaling(scaling, 0, base, factor, length, low, high)
+    _check("bfo_rotary_frequencies",
+           _lib().bfo_rotary_frequencies(ctypes.byref(s), _sized(rotated, _U32), out))
+    return torch.tensor(out[:], dtype=torch.float64, device=device)
+
+
+def _heads(t, name):
+    """(device pointer, token stride, head stride) of a tokens x heads x columns tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPE_CODES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D (tokens, heads, columns), got {t.dim()} dimensions")
+    tokens, heads, step = t.stride()
+    if step != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected a GPU")
+    return t.data_ptr(), tokens, heads
+
+
+def rotary_apply(x, frequencies, out, positions=None, period=0, layout=ROTARY_HALF, amplitude=1.0, backward=False):
+    """out = x (tokens x heads x columns) with the pairs of each head's first
+    2 * len(frequencies) columns turned by position * frequency; backward: turned
+    back, which takes the gradient of out to that of x.  frequencies: float64, on
+    the GPU.  positions: int32 per token, or None for the token's index (modulo
+    period if that is not 0).  out may be x."""
+    xp, xt, xh = _heads(x, "x")
+    op, ot, oh = _heads(out, "out")
+    dev = x.device
+    if out.dtype != x.dtype:
+        raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
+    if out.device != dev:
+        raise ValueError(f"out is on {out.device}, expected {dev}")
+    if out.shape != x.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
+    if not isinstance(frequencies, torch.Tensor):
+        raise TypeError("frequencies must be a torch.Tensor")
+    tokens, heads, dim = x.shape
+    pairs = frequencies.numel()
+    _launch("rotary_apply", dev, xp, xt, xh, op, ot, oh, tokens, _sized(heads, _U32), _sized(dim, _U32),
+            _sized(2 * pairs, _U32), layout, _vector(frequencies, torch.float64, pairs, "frequencies", dev),
+            _vector(positions, torch.int32, tokens, "positions", dev), period, amplitude, int(backward),
+            _DTYPE_CODES[x.dtype])

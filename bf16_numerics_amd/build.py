@@ -14,7 +14,9 @@ LIB = os.path.join(HERE, "libbf16opt.so")
 SOURCES = [os.path.join(CSRC, "bfo_kernels.hip"), os.path.join(CSRC, "bfo_abi.cpp"),
            os.path.join(CSRC, "bfo_control.cpp"), os.path.join(CSRC, "bfo_checkpoint.cpp"),
            os.path.join(CSRC, "bfo_layernorm.hip"), os.path.join(CSRC, "bfo_logits.hip"),
-           os.path.join(CSRC, "bfo_ops.cpp")]
+           os.path.join(CSRC, "bfo_ops.cpp"), os.path.join(CSRC, "bfo_rmsnorm.hip"),
+           os.path.join(CSRC, "bfo_activation.hip"), os.path.join(CSRC, "bfo_rotary.hip"),
+           os.path.join(CSRC, "bfo_block.cpp")]
 ARCH = os.environ.get("BFO_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

@@ -1,0 +1,134 @@
+// bfo_codes.hpp -- 8-bit codes with scales: values of a row in groups of
+// kGroup columns (or the whole row), each code an 8-bit integer or an e4m3
+// float, each value code * scale.
+//
+// scale = max(amax / top, 2^-126), amax the group's largest absolute value and
+// top what the code type holds at most (127, 448), so that the largest value
+// takes the whole range and a group of zeros has a scale to divide by; the
+// code is value / scale rounded to nearest even.  A value is off by at most
+// half a step: scale / 2 for integers, 2^-4 of itself for e4m3 (or
+// scale * 2^-10 below scale * 2^-6).  For normally distributed values integers
+// of a group of 128 are about four times as exact; e4m3 keeps small values
+// beside large ones.  Absolute values are compared as bit patterns, in which a
+// NaN is above infinity: a group that holds either gets a scale that is not
+// finite and all its values read back as NaN.
+#pragma once
+
+#include "bfo_device.hpp"
+#include "bfo_ops.hpp"
+
+namespace bfo {
+namespace {
+
+constexpr int kGroup = int(BFO_GROUP);
+
+// Words that may start at any byte.
+typedef uint32_t Bytes4 __attribute__((aligned(1)));
+typedef uint32_t Bytes8 __attribute__((ext_vector_type(2), aligned(1)));
+
+__device__ __forceinline__ uint32_t absBits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The largest of the values of the kLanes lanes (16 or 32 from a multiple of it
+// on, or the wavefront), in all of them.
+template <int kLanes>
+__device__ __forceinline__ uint32_t laneMax(uint32_t v) {
+    static_assert(kLanes == 16 || kLanes == 32 || kLanes == 64, "one DPP row, two or the wavefront");
+    if constexpr (kLanes == 64) {
+        return waveExtreme<true>(v);
+    } else {
+        v = max(v, uint32_t(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 8, 0xF, 0xF, false)));
+        v = max(v, uint32_t(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 4, 0xF, 0xF, false)));
+        v = max(v, uint32_t(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 2, 0xF, 0xF, false)));
+        v = max(v, uint32_t(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 1, 0xF, 0xF, false)));
+        if constexpr (kLanes == 32) {
+            const auto both = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+            v = max(uint32_t(both[0]), uint32_t(both[1]));
+        }
+        return v;
+    }
+}
+
+// The scale of values up to `amax` (its bits) and its reciprocal.
+struct CodeScale {
+    float scale, inverse;
+};
+template <int kType>
+__device__ __forceinline__ CodeScale codeScale(uint32_t amax) {
+    constexpr float kTopInverse = kType == BFO_I8 ? 1.0f / 127.0f : 1.0f / 448.0f, kSmallest = 0x1p-126f;
+    float s = __uint_as_float(amax) * kTopInverse;
+    s = s < kSmallest ? kSmallest : s;  // a NaN stays
+    return {s, 1.0f / s};
+}
+
+// The codes of N values, four to a word.
+template <int kType, int N>
+__device__ __forceinline__ void encode(const float (&v)[N], float inverse, uint32_t (&w)[N / 4]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        if constexpr (kType == BFO_I8) {
+            // Added to 1.5 * 2^23, a number is rounded to an integer in the sum's low bits.
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(v[i + e] * inverse + 12582912.0f);
+            const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
+            w[i / 4] = lo | hi;
+        } else {
+            int r = __builtin_amdgcn_cvt_pk_fp8_f32(v[i] * inverse, v[i + 1] * inverse, 0, false);
+            r = __builtin_amdgcn_cvt_pk_fp8_f32(v[i + 2] * inverse, v[i + 3] * inverse, r, true);
+            w[i / 4] = uint32_t(r);
+        }
+    }
+}
+
+// The values that N codes stand for.
+template <int kType, int N>
+__device__ __forceinline__ void decode(const uint32_t (&w)[N / 4], float scale, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        if constexpr (kType == BFO_I8) {
+            const uint32_t u = w[i / 4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i + e] = float(int8_t(u >> (8 * e))) * scale;
+        } else {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[i / 4]), false);
+            const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(w[i / 4]), true);
+            v[i] = lo[0] * scale, v[i + 1] = lo[1] * scale;
+            v[i + 2] = hi[0] * scale, v[i + 3] = hi[1] * scale;
+        }
+    }
+}
+
+// Codes of the columns [c, c + N) of those from `base` on, of which [0, cols)
+// are there; 0 for the others, and for all if not `live`.
+template <int N>
+__device__ __forceinline__ void loadCodes(const uint8_t *base, int c, int cols, bool live, uint32_t (&w)[N / 4]) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = 0u;
+    if (live && c + N <= cols) {
+        if constexpr (N == 8) {
+            const Bytes8 q = *reinterpret_cast<const Bytes8 *>(base + c);
+            w[0] = q.x, w[1] = q.y;
+        } else {
+            w[0] = *reinterpret_cast<const Bytes4 *>(base + c);
+        }
+    } else if (live && c < cols) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c + i < cols) w[i / 4] |= uint32_t(base[c + i]) << (8 * (i % 4));
+    }
+}
+template <int N>
+__device__ __forceinline__ void storeCodes(uint8_t *base, int c, int cols, const uint32_t (&w)[N / 4]) {
+    if (c + N <= cols) {
+        if constexpr (N == 8) *reinterpret_cast<Bytes8 *>(base + c) = Bytes8{w[0], w[1]};
+        else *reinterpret_cast<Bytes4 *>(base + c) = w[0];
+    } else if (c < cols) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c + i < cols) base[c + i] = uint8_t(w[i / 4] >> (8 * (i % 4)));
+    }
+}
+
+}  // namespace
+}  // namespace bfo

@@ -65,6 +65,26 @@ struct Chunk {
             }
         }
     }
+    // Adds the other chunk's values, rounding to T.
+    __device__ __forceinline__ void add(const Chunk &o) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint((*this)[i] + o[i]);
+            else w[i] = packBf16((*this)[2 * i] + o[2 * i], (*this)[2 * i + 1] + o[2 * i + 1]);
+        }
+    }
+    // Stores the columns [c, c + N) of those from `base` on that lie in [0, cols).
+    __device__ __forceinline__ void storeRow(T *base, int c, int cols) const {
+        if (c + N <= cols) {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4)
+                *(reinterpret_cast<Words4 *>(base + c) + i / 4) = Words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+        } else if (c < cols) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (c + i < cols) storeOne(base + c + i, (*this)[i]);
+        }
+    }
     // Columns [c, c + N) of those from `base` on, of which [0, cols) are there;
     // 0 for the others, and for all if not `live`.  The zeros come first, so that
     // no load waits for another one's lanes.  Here and below a `base` that is the
@@ -132,11 +152,15 @@ __device__ __forceinline__ float lastLane(float v) {
 }
 template <int kLanes>
 __device__ __forceinline__ float laneSum(float v) {
-    static_assert(kLanes == 16 || kLanes == 64, "one DPP row or the wavefront");
+    static_assert(kLanes == 16 || kLanes == 32 || kLanes == 64, "one DPP row, two or the wavefront");
     v += dpp<kRowRotate + 8>(0.0f, v);
     v += dpp<kRowRotate + 4>(0.0f, v);
     v += dpp<kRowRotate + 2>(0.0f, v);
     v += dpp<kRowRotate + 1>(0.0f, v);
+    if constexpr (kLanes == 32) {
+        const auto both = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(both[0]) + __uint_as_float(both[1]);
+    }
     if constexpr (kLanes == 64) {
         v += dpp<kRowBroadcast15, 0xA>(0.0f, v);
         v += dpp<kRowBroadcast31, 0xC>(0.0f, v);

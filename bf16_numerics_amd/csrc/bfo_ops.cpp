@@ -1,73 +1,14 @@
 // bfo_ops.cpp -- host side of the training-loop operators declared in
 // include/bf16opt.h: argument checks and the kernel launches on the caller's
 // stream.
-#include <hip/hip_runtime_api.h>
-
 #include <cmath>
-#include <cstdint>
 
-#include "bfo_checks.hpp"
-#include "bfo_internal.hpp"
+#include "bfo_args.hpp"
 #include "bfo_ops.hpp"
 
 namespace {
 
-using bfo::alignedTo;
-using bfo::overlap;
-using bfo::Rows;
-using bfo::Span;
-using bfo::span;
-
-constexpr uint64_t kMaxRows = uint64_t(1) << 31;
-constexpr uint64_t kMaxBytes = uint64_t(1) << 62;  // of one matrix
-
-bool knownType(int dtype) { return dtype == BFO_BF16 || dtype == BFO_F32; }
-uint64_t sizeOf(int dtype) { return dtype == BFO_BF16 ? 2 : 4; }
-
-int done(hipError_t e) { return e == hipSuccess ? BFO_OK : bfo::recordHipFailure(e); }
-
-// A matrix of `cols` used columns; the status its sizes and pointer earn.
-int matrix(const void *p, uint64_t stride, uint64_t rows, uint64_t cols, int dtype, Rows &out) {
-    const uint64_t size = sizeOf(dtype);
-    out = Rows{p, rows, cols * size, stride * size};
-    if (rows > kMaxRows || stride > kMaxBytes / size) return BFO_ERANGE;
-    if (rows && !p) return BFO_EINVAL;
-    if (rows > 1) {
-        if (stride < cols) return BFO_EINVAL;
-        if (stride * size > kMaxBytes / rows) return BFO_ERANGE;
-    }
-    return alignedTo(p, size) ? BFO_OK : BFO_EMISALIGNED;
-}
-
-// One array argument with the way it is used.
-struct Use {
-    Span at;
-    bool written;
-};
-Use reads(const void *p, uint64_t bytes) { return {span(p, bytes), false}; }
-Use writes(const void *p, uint64_t bytes) { return {span(p, bytes), true}; }
-
-// True when a written array shares a byte with another array of the call.
-template <int N>
-bool conflict(const Use (&use)[N]) {
-    for (int i = 0; i < N; ++i)
-        for (int j = i + 1; j < N; ++j)
-            if ((use[i].written || use[j].written) && overlap(use[i].at, use[j].at)) return true;
-    return false;
-}
-// The same between matrices and plain arrays.
-template <int N>
-bool conflict(const Rows &m, bool written, const Use (&use)[N]) {
-    for (int i = 0; i < N; ++i)
-        if ((written || use[i].written) && overlap(m.whole(), use[i].at)) return true;
-    return false;
-}
-
-bool allAligned(std::initializer_list<const void *> ps, uintptr_t a) {
-    for (const void *p : ps)
-        if (!alignedTo(p, a)) return false;
-    return true;
-}
+using namespace bfo;
 
 int checkLayerNorm(uint32_t cols, int dtype, int paramDtype) {
     if (!knownType(dtype) || !knownType(paramDtype) || cols == 0) return BFO_EINVAL;

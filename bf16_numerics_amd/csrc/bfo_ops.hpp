@@ -1,9 +1,10 @@
 // bfo_ops.hpp -- limits, partitions and kernel launchers of the training-loop
-// operators, shared by their host ABI (bfo_ops.cpp) and their gfx950 kernels
-// (bfo_layernorm.hip, bfo_logits.hip).
+// operators, shared by their host ABI (bfo_ops.cpp, bfo_block.cpp) and their
+// gfx950 kernels (bfo_layernorm.hip, bfo_logits.hip, bfo_rmsnorm.hip,
+// bfo_activation.hip, bfo_rotary.hip).
 #pragma once
 
-#include <hip/hip_runtime_api.h>
+#include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "../../include/bf16opt.h"
@@ -55,6 +56,118 @@ struct LayerNormBackward {
     float *partials;
 };
 hipError_t launchLayerNormBackward(const LayerNormBackward &a, hipStream_t stream);
+
+// Codes of a matrix, `stride` bytes from row to row, and their scales.
+struct ConstCodes {
+    const void *p;
+    uint64_t stride;
+    const float *scales;
+    bool wholeRow;  // one scale a row instead of one a group
+};
+struct CodeMatrix {
+    void *p;
+    uint64_t stride;
+    float *scales;
+};
+
+// RMS norm backward: as layer norm's, with one sum a column.
+uint32_t rmsBackwardBlocks(uint64_t rows, uint32_t cols);
+inline uint64_t rmsWorkspaceBytes(uint64_t rows, uint32_t cols) {
+    return uint64_t(rmsBackwardBlocks(rows, cols)) * cols * sizeof(float);
+}
+uint64_t rmsWorkspaceBound(uint64_t rows, uint32_t cols);  // as lnWorkspaceBound
+
+struct RmsNormForward {
+    ConstMatrix x, residual;
+    const void *weight;
+    Matrix total, out;
+    float *rstd;
+    Matrix codes;
+    float *scales;
+    int codeType, codesOfOut;
+    uint32_t group;  // BFO_GROUP, or 0: the whole row
+    uint64_t rows;
+    uint32_t cols;
+    float eps;
+    int dtype, paramDtype;
+};
+hipError_t launchRmsNormForward(const RmsNormForward &a, hipStream_t stream);
+
+struct RmsNormBackward {
+    ConstMatrix dout, x, codes;
+    const float *scales;
+    int codeType;
+    uint32_t group;
+    const void *weight;
+    const float *rstd;
+    Matrix dx;
+    void *dweight;
+    Matrix out;
+    uint64_t rows;
+    uint32_t cols;
+    int dtype, paramDtype, accumulate;
+    float *partials;
+};
+hipError_t launchRmsNormBackward(const RmsNormBackward &a, hipStream_t stream);
+
+// Division of numbers below 2^31 by a constant from 1 to 2^31: with s the bits of
+// by - 1, (n * (floor(2^(31 + s) / by) + 1)) >> (31 + s) is the quotient, as the
+// factor is off by at most 2^s / 2^(31 + s) of itself.
+struct FastDivide {
+    uint32_t by, factor, shift;
+    FastDivide() = default;
+    explicit FastDivide(uint32_t d) : by(d), shift(31) {
+        while (shift < 62 && (uint64_t(1) << (shift - 31)) < d) ++shift;
+        factor = uint32_t((uint64_t(1) << shift) / d + 1);
+    }
+    __host__ __device__ uint32_t divide(uint32_t n) const { return uint32_t(uint64_t(n) * factor >> shift); }
+};
+
+// The rows' groups of columns, `count` in all (at most 2^31).
+struct GroupGrid {
+    uint32_t cols, count;
+    FastDivide perRow;
+};
+
+// Beside the kinds and code types of the ABI: codes by themselves, and none.
+constexpr int kIdentity = -1, kNoCodes = -1;
+
+struct ActivationForward {
+    ConstMatrix gate, up;
+    Matrix out;
+    CodeMatrix gateCodes, upCodes;
+    int codeType;
+    GroupGrid grid;
+    int kind, dtype;
+};
+hipError_t launchActivationForward(const ActivationForward &a, hipStream_t stream);
+
+struct ActivationBackward {
+    ConstMatrix dout, gate, up;
+    ConstCodes gateCodes, upCodes;
+    int codeType;
+    Matrix dgate, dup, out;
+    GroupGrid grid;
+    int kind, dtype;
+};
+hipError_t launchActivationBackward(const ActivationBackward &a, hipStream_t stream);
+
+struct Rotary {
+    const void *x;
+    uint64_t xToken, xHead;
+    void *out;
+    uint64_t outToken, outHead;
+    uint64_t tokens;
+    uint32_t heads, headDim, rotated;
+    const double *frequencies;
+    const int32_t *positions;
+    uint64_t period;
+    float amplitude;
+    int backward;
+    uint32_t headsAtOnce;     // of a wavefront; this and the next set by the launch
+    FastDivide itemsPerHead;  // 16-byte items of work
+};
+hipError_t launchRotary(const Rotary &a, int dtype, int layout, hipStream_t stream);
 
 // The scale of a difference of scores, as (x part - m part) rest: by halves below
 // 1, where a difference past binary32 may have a product that is not.

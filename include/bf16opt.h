@@ -638,6 +638,164 @@ int distill_backward(const void *logits, uint64_t stride, uint64_t rows, uint32_
                      uint32_t count, const int32_t *targets, const float *stats, const float *dkl,
                      const float *dlogprob, void *dlogits, uint64_t dlogits_stride, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators between a transformer block's matrix products: root-mean-square
+ * norm with the residual's addition, the feed-forward's activation, rotary
+ * positions, each with its gradient, and what a training step keeps between
+ * forward and backward in 8 bits.  Conventions as above.
+ *
+ * Codes.  rows x cols values are kept as one byte each (codes: a matrix of
+ * bytes, rows `codes_stride` bytes apart, starting anywhere) and a binary32
+ * scale for every group of BFO_GROUP columns of a row (scales: rows x
+ * ceil(cols / BFO_GROUP), contiguous; the last group of a row may be shorter),
+ * or, where a call takes group == 0, one scale for the whole row (scales: rows).
+ * With amax the group's largest absolute value and top = 127 (BFO_I8: signed
+ * integers) or 448 (BFO_E4M3: 8-bit floats of 4 exponent and 3 mantissa bits,
+ * no infinities), in binary32
+ *   scale = max(amax * (1 / top), 2^-126)
+ *   code  = value * (1 / scale), rounded to the nearest code, ties to even
+ * and a code stands for code * scale: at most scale / 2 off for integers, a
+ * 16th of itself (or scale * 2^-10, if more) for e4m3.  A group with a NaN or
+ * an infinity stands for NaN throughout.
+ * ------------------------------------------------------------------------- */
+enum { BFO_I8 = 0, BFO_E4M3 = 1 };
+#define BFO_GROUP 128u
+
+/* Root-mean-square norm of x + residual.  Per row:
+ *   total = x + residual, rounded to the type (x itself where residual is NULL)
+ *   rstd = 1 / sqrt(sum(total^2) / cols + eps)
+ *   normalised = total * rstd;  out = normalised * weight
+ * weight holds cols values of param_dtype.  total, out and rstd (rows floats,
+ * for the backward pass) may be NULL, total must be without a residual; total
+ * may be x or residual (same pointer and stride).  codes and scales, both or
+ * neither: codes_of BFO_CODES_OF_OUT keeps out (for a product in 8 bits; out
+ * before its rounding), BFO_CODES_OF_NORMALISED the normalised row (for the
+ * backward pass); group BFO_GROUP or 0.  At least one of out and codes must be
+ * given.  1 <= cols <= BFO_RMSNORM_MAX_COLS (0 -> BFO_EINVAL, above ->
+ * BFO_ERANGE); eps >= 0 and finite.  A row with a NaN gives NaN, one with an
+ * infinity rstd 0 and NaN in its place.  The sum of squares is binary32's, which
+ * holds it for |total| < 2^57 (beyond, it may overflow: rstd 0 and out 0); where
+ * eps = 0, a row of zeros has no finite result, and one below 2^-56 may lose its
+ * squares. */
+#define BFO_RMSNORM_MAX_COLS 16384u
+enum { BFO_CODES_OF_OUT = 0, BFO_CODES_OF_NORMALISED = 1 };
+int rmsnorm_forward(const void *x, uint64_t x_stride, const void *residual, uint64_t residual_stride,
+                    const void *weight, void *total, uint64_t total_stride, void *out, uint64_t out_stride,
+                    float *rstd, void *codes, uint64_t codes_stride, float *scales, int code_type, int codes_of,
+                    uint32_t group, uint64_t rows, uint32_t cols, float eps, int dtype, int param_dtype,
+                    void *stream);
+
+/* *bytes = the workspace rmsnorm_backward needs.  Host only. */
+int bfo_rmsnorm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t *bytes);
+
+/* Gradients of rmsnorm_forward, from its rstd and either the row that it
+ * normalised (x: the forward pass's total) or that row's codes of
+ * BFO_CODES_OF_NORMALISED (x NULL).  With xhat = x * rstd, or what the codes
+ * stand for, and h = weight * dout, per row:
+ *   dx = rstd * (h - xhat * sum(h * xhat) / cols)
+ * (the gradient of x, of the residual and of total alike), and over the rows
+ * dweight = sum(dout * xhat).  out, unless NULL, gets xhat * weight again, which
+ * the next product's weight gradient needs and a step that keeps codes has not
+ * kept.  accumulate, rows == 0 and the types as in layernorm_backward. */
+int rmsnorm_backward(const void *dout, uint64_t dout_stride, const void *x, uint64_t x_stride, const void *codes,
+                     uint64_t codes_stride, const float *scales, int code_type, uint32_t group, const void *weight,
+                     const float *rstd, void *dx, uint64_t dx_stride, void *dweight, void *out, uint64_t out_stride,
+                     uint64_t rows, uint32_t cols, int dtype, int param_dtype, int accumulate, void *workspace,
+                     void *stream);
+
+/* The feed-forward's activation: out = act(gate) * up, or act(gate) where up is
+ * NULL, with act(g) = g / (1 + exp(-z)) and
+ *   BFO_SILU  z = g
+ *   BFO_GELU  z = 2 sqrt(2 / pi) (g + 0.044715 g^3)   (GELU's tanh form)
+ * gate_codes with gate_scales, and up_codes with up_scales where up is given,
+ * keep both inputs in codes for the backward pass (all of them or none), in
+ * groups of BFO_GROUP columns.  out may be gate or up (same pointer and stride).
+ * Any infinity or NaN in gate gives what the formula gives, except that -inf
+ * gives NaN.  1 <= cols <= BFO_ACTIVATION_MAX_COLS; rows * ceil(cols /
+ * BFO_GROUP) <= 2^31 (above -> BFO_ERANGE). */
+enum { BFO_SILU = 0, BFO_GELU = 1 };
+#define BFO_ACTIVATION_MAX_COLS (1u << 28)
+int activation_forward(const void *gate, uint64_t gate_stride, const void *up, uint64_t up_stride, void *out,
+                       uint64_t out_stride, void *gate_codes, uint64_t gate_codes_stride, float *gate_scales,
+                       void *up_codes, uint64_t up_codes_stride, float *up_scales, int code_type, uint64_t rows,
+                       uint32_t cols, int kind, int dtype, void *stream);
+
+/* Gradients of activation_forward at its inputs (gate, and up if it was given)
+ * or at what their codes stand for (gate and up NULL):
+ *   dgate = dout * up * act'(gate);  dup = dout * act(gate)
+ * (without up: dgate = dout * act'(gate), and dup is NULL).  out, unless NULL,
+ * gets act(gate) * up again, for the next product's weight gradient.  Each
+ * output may be one of dout, gate and up (same pointer and stride). */
+int activation_backward(const void *dout, uint64_t dout_stride, const void *gate, uint64_t gate_stride,
+                        const void *up, uint64_t up_stride, const void *gate_codes, uint64_t gate_codes_stride,
+                        const float *gate_scales, const void *up_codes, uint64_t up_codes_stride,
+                        const float *up_scales, int code_type, void *dgate, uint64_t dgate_stride, void *dup,
+                        uint64_t dup_stride, void *out, uint64_t out_stride, uint64_t rows, uint32_t cols, int kind,
+                        int dtype, void *stream);
+
+/* Any other activation that a step keeps in 8 bits: its codes in groups of
+ * BFO_GROUP columns, and the values that codes (of either group) stand for, in
+ * binary32 or rounded to bf16.  Sizes as in activation_forward. */
+int activation_pack(const void *x, uint64_t x_stride, void *codes, uint64_t codes_stride, float *scales,
+                    int code_type, uint64_t rows, uint32_t cols, int dtype, void *stream);
+int activation_unpack(const void *codes, uint64_t codes_stride, const float *scales, int code_type, uint32_t group,
+                      void *out, uint64_t out_stride, uint64_t rows, uint32_t cols, int dtype, void *stream);
+
+/* The angle per position of each pair of a head's rotated columns, with base >
+ * 1: frequency[i] = base^(-2 i / rotated), i < rotated / 2, and for contexts
+ * `factor` >= 1 times as long as the `length` positions that a model was
+ * trained on:
+ *   BFO_ROTARY_UNSCALED  as it is
+ *   BFO_ROTARY_LINEAR    divided by factor
+ *   BFO_ROTARY_BASE      of the base * factor^(rotated / (rotated - 2)): the first
+ *                        as it is, the last divided by factor (rotated >= 4)
+ *   BFO_ROTARY_BY_TURNS  divided by factor below `low` turns in length positions,
+ *                        as it is above `high`, and between them mixed in proportion
+ *                        to the number of turns
+ *   BFO_ROTARY_BY_PAIR   the same, mixed in proportion to the pair's index
+ * (0 < low < high; length and these two are used by the last two kinds only).
+ * frequencies: rotated / 2 doubles of host memory, which a caller copies to the
+ * device once.  rotated: even, 2 ... BFO_ROTARY_MAX_DIM.  BFO_EINVAL for
+ * anything else.  Host only. */
+#define BFO_ROTARY_MAX_DIM 1024u
+#define BFO_ROTARY_MAX_HEADS 65535u
+enum { BFO_ROTARY_UNSCALED = 0, BFO_ROTARY_LINEAR = 1, BFO_ROTARY_BASE = 2, BFO_ROTARY_BY_TURNS = 3, BFO_ROTARY_BY_PAIR = 4 };
+typedef struct {
+    int32_t kind;
+    uint32_t reserved;
+    double base;
+    double factor;
+    double length;
+    double low;
+    double high;
+} bfo_rotary_scaling;
+int bfo_rotary_frequencies(const bfo_rotary_scaling *scaling, uint32_t rotated, double *frequencies);
+
+/* Rotary positions: out = x with the pairs of every head's first `rotated`
+ * columns turned by the token's position times the pair's frequency:
+ *   (a, b) -> amplitude * (a cos - b sin, a sin + b cos)
+ * Pair i is columns (i, i + rotated / 2) for BFO_ROTARY_HALF, (2 i, 2 i + 1) for
+ * BFO_ROTARY_INTERLEAVED.  Columns from rotated on are copied.  backward != 0
+ * turns back (b's signs change places): x is then the gradient of the turned
+ * heads and out that of the heads before.
+ * x, out: head h of token t starts at t * token_stride + h * head_stride and
+ * holds head_dim values with unit stride; either the tokens' rows or the heads'
+ * may be the outer ones, but they may not reach into one another (so queries and
+ * keys of one buffer take one call).  out may be x (same pointer and strides);
+ * the columns behind are then not touched.
+ * frequencies: device array of rotated / 2 doubles (8-byte aligned), in radians
+ * per position.  positions: device array of tokens int32 (any sign), or NULL:
+ * position t, or t % period where period is not 0 (sequences of that length, one
+ * after the other).  Angles are formed and reduced in binary64, the rest is
+ * binary32, rounded once.  amplitude (finite): 1, or what a long context's
+ * scaling asks for.  heads <= BFO_ROTARY_MAX_HEADS, head_dim <=
+ * BFO_ROTARY_MAX_DIM, rotated even, 2 ... head_dim. */
+enum { BFO_ROTARY_HALF = 0, BFO_ROTARY_INTERLEAVED = 1 };
+int rotary_apply(const void *x, uint64_t x_token_stride, uint64_t x_head_stride, void *out,
+                 uint64_t out_token_stride, uint64_t out_head_stride, uint64_t tokens, uint32_t heads,
+                 uint32_t head_dim, uint32_t rotated, int layout, const double *frequencies,
+                 const int32_t *positions, uint64_t period, float amplitude, int backward, int dtype, void *stream);
+
 /* Static string naming a status code. */
 const char *bfo_status_string(int status);
 
