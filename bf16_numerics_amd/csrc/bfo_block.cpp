@@ -284,7 +284,7 @@ int rotary_apply(const void *x, uint64_t x_token_stride, uint64_t x_head_stride,
     const Use use[] = {reads(frequencies, 4 * uint64_t(rotated)), reads(positions, 4 * tokens)};
     if (conflict(matrices) || conflict(matrices, use)) return BFO_EINVAL;
     const Rotary a{x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads, head_dim,
-                   rotated, frequencies, positions, period, amplitude, backward != 0, 0, FastDivide()};
+                   rotated, frequencies, positions, period, amplitude, backward != 0, 0, 0, {}, {}, {}, {}};
     return done(launchRotary(a, dtype, layout, static_cast<hipStream_t>(stream)));
 }
 

@@ -36,6 +36,12 @@ struct Chunk {
     static constexpr int kWords = N * int(sizeof(T)) / 4;
     uint32_t w[kWords];
 
+    Chunk() = default;
+    // N values, rounded to T.
+    __device__ __forceinline__ explicit Chunk(const float *v) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? __float_as_uint(v[i]) : packBf16(v[2 * i], v[2 * i + 1]);
+    }
     __device__ __forceinline__ float operator[](int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         else return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
@@ -73,12 +79,15 @@ struct Chunk {
             else w[i] = packBf16((*this)[2 * i] + o[2 * i], (*this)[2 * i + 1] + o[2 * i + 1]);
         }
     }
+    __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4)
+            *(reinterpret_cast<Words4 *>(p) + i / 4) = Words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+    }
     // Stores the columns [c, c + N) of those from `base` on that lie in [0, cols).
     __device__ __forceinline__ void storeRow(T *base, int c, int cols) const {
         if (c + N <= cols) {
-#pragma unroll
-            for (int i = 0; i < kWords; i += 4)
-                *(reinterpret_cast<Words4 *>(base + c) + i / 4) = Words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+            store(base + c);
         } else if (c < cols) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -118,7 +127,7 @@ struct Chunk {
 
 // Stores N values, rounded to T, at those of the columns [c, c + N) from
 // `base` on that lie in [lo, hi).
-template <typename T, int N>
+template <bool kNontemporal = false, typename T, int N>
 __device__ __forceinline__ void storeRow(T *base, int c, int lo, int hi, const float (&v)[N]) {
     if (c >= lo && c + N <= hi) {
         uint32_t w[N * sizeof(T) / 4];
@@ -128,8 +137,12 @@ __device__ __forceinline__ void storeRow(T *base, int c, int lo, int hi, const f
             else if (i % 2 == 0) w[i / 2] = packBf16(v[i], v[i + 1]);
         }
 #pragma unroll
-        for (int i = 0; i < int(N * sizeof(T) / 4); i += 4)
-            *(reinterpret_cast<Words4 *>(base + c) + i / 4) = Words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+        for (int i = 0; i < int(N * sizeof(T) / 4); i += 4) {
+            Words4 *p = reinterpret_cast<Words4 *>(base + c) + i / 4;
+            const Words4 q{w[i], w[i + 1], w[i + 2], w[i + 3]};
+            if constexpr (kNontemporal) __builtin_nontemporal_store(q, p);
+            else *p = q;
+        }
     } else if (c + N > lo && c < hi) {
 #pragma unroll
         for (int i = 0; i < N; ++i)

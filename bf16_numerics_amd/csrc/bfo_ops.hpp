@@ -164,8 +164,10 @@ struct Rotary {
     uint64_t period;
     float amplitude;
     int backward;
-    uint32_t headsAtOnce;     // of a wavefront; this and the next set by the launch
-    FastDivide itemsPerHead;  // 16-byte items of work
+    // Set by the launch: a workgroup's tokens and heads, the blocks of heads, the
+    // workgroups' work in all, and the items of work a head is cut into.
+    uint32_t tokensAtOnce, units;
+    FastDivide headsAtOnce, headBlocks, itemsPerHead, pairsPerToken;
 };
 hipError_t launchRotary(const Rotary &a, int dtype, int layout, hipStream_t stream);
 

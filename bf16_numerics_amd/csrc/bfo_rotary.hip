@@ -3,112 +3,176 @@
 // Pair i of a head at position p is turned by the angle p * frequency[i]:
 //   (a, b) -> amplitude * (a cos - b sin, a sin + b cos),
 // backward by the negative angle, which is the transpose.  Angles are formed
-// and reduced to a turn in 64 bits, so that far positions keep them.  A
-// wavefront takes a token and a range of its heads: each lane forms the sine
-// and cosine of one pair (and of pair + 64, ...) into LDS, then the wavefront
-// walks over the heads, 16-byte chunks of both members of the pairs a lane.
+// and reduced to a turn in 64 bits, so that far positions keep them; sines and
+// cosines are those of the turn's rest in 32 bits.
+//
+// Bound by memory: every column is read and written once, and the sines are
+// shared by a token's heads.  A workgroup takes a token's heads, up to two
+// 16-byte chunks a lane (or several tokens of few heads, or a part of a token
+// of many): its lanes first ask for the angles' parts, then for their chunks,
+// and form the sines into LDS while those are on their way.  8192 tokens of 64
+// heads of 128 bf16 columns: 46.0 us in halves and 47.2 interleaved, 5.8 and 5.7
+// TB/s, where a copy of the same bytes takes 50.2.  A wavefront a token, walking
+// over its heads with the sines in its own LDS: 62 and 67 us, with four chunks in
+// flight 54 and 56; one 16-byte chunk a lane 46 (halves need two) and 58;
+// workgroups of 256 lanes 47.4 and 46.8, of 1,024 49.9 and 50.0; chunks asked for
+// before the angles 49.8 and 55.6.
+#include <type_traits>
+
 #include "bfo_device.hpp"
 #include "bfo_ops.hpp"
 
 namespace bfo {
 namespace {
 
-constexpr int kBlock = 256, kWaves = kBlock / 64;
+constexpr int kBlock = 512;
+static_assert(kBlock >= 129, "a head's items fit a workgroup");
 constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
 
-// Rotated pairs that one item of work holds.
-template <typename T, bool kHalf>
-constexpr int pairsAtOnce() {
-    return (kHalf ? 16 : 8) / int(sizeof(T));
-}
+// Columns behind the rotated ones that a lane copies at a time.
+constexpr int kCopied = 8;
 
-template <typename T, bool kHalf>
+// What a lane takes at a time: P pairs from pair `first` on, in two 16-byte
+// chunks, or kCopied columns from column `first` on.  A head has at most 129 such
+// items, which fit a workgroup.  kWhole: the last item of a
+// head's pairs, or of its columns, starts so much earlier that it ends with them
+// (what two items share is the same in both, and read before either writes);
+// otherwise, for too few of them, they end inside one.
+template <typename T, bool kHalf, bool kWhole>
+struct Item {
+    static constexpr int E = 16 / int(sizeof(T)), P = E;
+    Chunk<T, E> u, v;
+
+    // A chunk at column c of a head, of which `there` columns are there.
+    __device__ __forceinline__ static void get(Chunk<T, E> &w, const T *head, int c, int there) {
+        if constexpr (kWhole) w.load(head + c);
+        else w.loadRow(head, c, there);
+    }
+    __device__ __forceinline__ static void put(const Chunk<T, E> &w, T *head, int c, int there) {
+        if constexpr (kWhole) w.store(head + c);
+        else w.storeRow(head, c, there);
+    }
+    __device__ __forceinline__ void loadPairs(const T *head, int first, int pairs) {
+        if constexpr (kHalf) {
+            get(u, head, first, pairs);
+            get(v, head + pairs, first, pairs);
+        } else {
+            get(u, head, 2 * first, 2 * pairs);
+            get(v, head + E, 2 * first, 2 * pairs - E);
+        }
+    }
+    __device__ __forceinline__ void loadBehind(const T *head, int first, int dim) {
+        get(u, head, first, dim);
+        if constexpr (kCopied > E) get(v, head + E, first, dim - E);
+    }
+    __device__ __forceinline__ void storeBehind(T *head, int first, int dim) const {
+        put(u, head, first, dim);
+        if constexpr (kCopied > E) put(v, head + E, first, dim - E);
+    }
+    // The pairs turned, stored.
+    __device__ __forceinline__ void turn(const float2 *turns, T *head, int first, int pairs) const {
+        float y[2 * E];
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            const int i = kHalf ? e : 2 * e, j = kHalf ? E + e : 2 * e + 1;
+            const float a = i < E ? u[i] : v[i - E], b = j < E ? u[j] : v[j - E];
+            const float2 t = turns[first + e];
+            y[i] = fmaf(a, t.x, -(b * t.y));
+            y[j] = fmaf(a, t.y, b * t.x);
+        }
+        const int c = kHalf ? first : 2 * first, there = kHalf ? pairs : 2 * pairs;
+        put(Chunk<T, E>(&y[0]), head, c, there);
+        put(Chunk<T, E>(&y[E]), kHalf ? head + pairs : head + E, c, kHalf ? there : there - E);
+    }
+};
+
+// Sines and cosines of a workgroup at most: 16 KB of LDS, as four workgroups fill a CU.
+constexpr uint32_t kTurns = 2048;
+
+// kBehind: columns behind the rotated ones are copied.
+template <typename T, bool kHalf, bool kWhole, bool kBehind>
 __global__ __launch_bounds__(kBlock) void rotaryKernel(Rotary a) {
-    constexpr int E = 16 / int(sizeof(T));
-    constexpr int P = pairsAtOnce<T, kHalf>();
-    extern __shared__ float turns[];  // a wavefront's cosines, then its sines
-    const int lane = int(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    const int pairs = int(a.rotated / 2), room = (pairs + 7) / 8 * 8;
-    float *cosine = turns + wave * 2 * room, *sine = cosine + room;
-    const uint32_t first = blockIdx.y * a.headsAtOnce;
-    const uint32_t heads = min(a.headsAtOnce, a.heads - first);
-    const uint32_t turning = uint32_t(pairs + P - 1) / P, items = heads * a.itemsPerHead.by;
-    for (uint64_t token = uint64_t(blockIdx.x) * kWaves + wave; token < a.tokens; token += uint64_t(gridDim.x) * kWaves) {
-        const int64_t position = a.positions ? int64_t(a.positions[token]) : int64_t(a.period ? token % a.period : token);
-        for (int i = lane; i < pairs; i += 64) {
-            double t = double(position) * a.frequencies[i] * kTurn;
-            t -= rint(t);
-            float s, c;
-            sincospif(2.0f * float(t), &s, &c);
-            cosine[i] = c * a.amplitude;
-            sine[i] = (a.backward ? -s : s) * a.amplitude;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const T *x = static_cast<const T *>(a.x) + token * a.xToken + first * a.xHead;
-        T *out = static_cast<T *>(a.out) + token * a.outToken + first * a.outHead;
-        for (uint32_t item = lane; item < items; item += 64) {
-            const uint32_t head = a.itemsPerHead.divide(item);
-            const uint32_t k = item - head * a.itemsPerHead.by;
-            const T *in = x + head * a.xHead;
-            T *to = out + head * a.outHead;
-            if (k >= turning) {  // columns behind the rotated ones
-                const int c = int(a.rotated) + int(k - turning) * E;
-                Chunk<T, E> v;
-                v.loadRow(in, c, int(a.headDim));
-                v.storeRow(to, c, int(a.headDim));
-                continue;
-            }
-            const int i = int(k) * P;
-            float c[P], s[P];
-#pragma unroll
-            for (int e = 0; e < P; ++e) c[e] = cosine[i + e], s[e] = sine[i + e];
-            if constexpr (kHalf) {
-                Chunk<T, E> u, v;
-                u.loadRow(in, i, pairs);
-                v.loadRow(in + pairs, i, pairs);
-                float y[E], z[E];
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    y[e] = fmaf(u[e], c[e], -(v[e] * s[e]));
-                    z[e] = fmaf(u[e], s[e], v[e] * c[e]);
-                }
-                storeRow(to, i, 0, pairs, y);
-                storeRow(to + pairs, i, 0, pairs, z);
-            } else {
-                Chunk<T, E> v;
-                v.loadRow(in, 2 * i, 2 * pairs);
-                float y[E];
-#pragma unroll
-                for (int e = 0; e < P; ++e) {
-                    y[2 * e] = fmaf(v[2 * e], c[e], -(v[2 * e + 1] * s[e]));
-                    y[2 * e + 1] = fmaf(v[2 * e], s[e], v[2 * e + 1] * c[e]);
-                }
-                storeRow(to, 2 * i, 0, 2 * pairs, y);
-            }
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+    constexpr uint32_t P = Item<T, kHalf, kWhole>::P;
+    extern __shared__ float2 table[];  // every token's cosines and sines
+    const uint32_t pairs = a.rotated / 2, room = (pairs + 7) / 8 * 8, turning = (pairs + P - 1) / P;
+    // What the angle of a workgroup's pair i is made of, and its cosine and sine.
+    struct Angle {
+        uint32_t token, pair;
+        int32_t position;
+        double frequency;
+    };
+    auto load = [&](uint64_t firstToken, uint32_t i) -> Angle {
+        const uint32_t t = a.pairsPerToken.divide(i), pair = i - t * pairs;
+        return {t, pair, a.positions ? a.positions[firstToken + t] : 0, a.frequencies[pair]};
+    };
+    auto put = [&](uint64_t firstToken, const Angle &angle) {
+        const uint64_t n = firstToken + angle.token;
+        const double position = a.positions ? double(angle.position) : double(a.period ? n % a.period : n);
+        double turn = position * angle.frequency * kTurn;
+        turn -= rint(turn);
+        float s, c;
+        sincospif(2.0f * float(turn), &s, &c);
+        table[angle.token * room + angle.pair] = {c * a.amplitude, (a.backward ? -s : s) * a.amplitude};
+    };
+    for (uint32_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+        const uint32_t block = a.headBlocks.divide(unit);
+        const uint32_t firstHead = (unit - block * a.headBlocks.by) * a.headsAtOnce.by;
+        const uint64_t firstToken = uint64_t(block) * a.tokensAtOnce;
+        const uint32_t tokens = uint32_t(min(uint64_t(a.tokensAtOnce), a.tokens - firstToken));
+        // The angle's parts first, so that no lane waits for its item before it forms the sine.
+        const uint32_t angles = tokens * pairs;
+        const Angle angle = load(firstToken, min(threadIdx.x, angles - 1));
+        const T *x = static_cast<const T *>(a.x) + firstToken * a.xToken + firstHead * a.xHead;
+        T *out = static_cast<T *>(a.out) + firstToken * a.outToken + firstHead * a.outHead;
+        const uint32_t row = a.itemsPerHead.divide(threadIdx.x), k = threadIdx.x - row * a.itemsPerHead.by;
+        const uint32_t token = a.headsAtOnce.divide(row), head = row - token * a.headsAtOnce.by;
+        const bool live = token < tokens && firstHead + head < a.heads;
+        const T *from = x + token * a.xToken + head * a.xHead;
+        Item<T, kHalf, kWhole> item;
+        // The item's first pair, or its first column behind them.
+        const bool turns = !kBehind || k < turning;
+        int at = turns ? int(k * P) : int(a.rotated) + int(k - turning) * kCopied;
+        if constexpr (kWhole) at = min(at, turns ? int(pairs - P) : int(a.headDim) - kCopied);
+        if (live && turns) item.loadPairs(from, at, int(pairs));
+        else if (kBehind && live) item.loadBehind(from, at, int(a.headDim));
+        if (threadIdx.x < angles) put(firstToken, angle);
+        for (uint32_t i = threadIdx.x + kBlock; i < angles; i += kBlock) put(firstToken, load(firstToken, i));
+        __syncthreads();
+        T *to = out + token * a.outToken + head * a.outHead;
+        if (live && turns) item.turn(table + token * room, to, at, int(pairs));
+        else if (kBehind && live) item.storeBehind(to, at, int(a.headDim));
+        if (unit + gridDim.x < a.units) __syncthreads();
     }
 }
 
 template <typename T, bool kHalf>
 void launch(Rotary a, hipStream_t stream) {
-    constexpr uint32_t P = pairsAtOnce<T, kHalf>(), E = 16 / sizeof(T);
-    const bool inPlace = a.x == a.out;
-    const uint32_t turning = (a.rotated / 2 + P - 1) / P;
-    const uint32_t per = turning + (inPlace ? 0 : (a.headDim - a.rotated + E - 1) / E);
+    constexpr uint32_t P = Item<T, kHalf, true>::P;
+    const uint32_t pairs = a.rotated / 2, turning = (pairs + P - 1) / P;
+    const uint32_t per = turning + (a.x == a.out ? 0 : (a.headDim - a.rotated + kCopied - 1) / kCopied);
+    // A workgroup's tokens and heads: as many as its lanes have items for, the heads of a
+    // token in blocks of like size.
+    const uint32_t fit = kBlock / per;
+    const uint32_t blocks = (a.heads + fit - 1) / fit, heads = (a.heads + blocks - 1) / blocks;
+    uint32_t tokens = fit / heads;
+    if (tokens > kTurns / pairs) tokens = kTurns / pairs;
+    if (tokens > a.tokens) tokens = uint32_t(a.tokens);
+    if (tokens < 1) tokens = 1;
     a.itemsPerHead = FastDivide(per);
-    // A wavefront takes all heads of a token where the tokens fill the chip by
-    // themselves, else as few as give each lane one item.
-    const uint64_t wanted = a.tokens * a.heads * per / 64 / 8192 + 1;  // items a lane
-    uint64_t heads = wanted * 64 / per;
-    heads = heads < 1 ? 1 : heads > a.heads ? a.heads : heads;
-    a.headsAtOnce = uint32_t(heads);
-    const uint64_t tokens = (a.tokens + kWaves - 1) / kWaves, most = 1u << 22;
-    const uint32_t room = (a.rotated / 2 + 7) / 8 * 8;
-    hipLaunchKernelGGL((rotaryKernel<T, kHalf>), dim3(uint32_t(tokens < most ? tokens : most), (a.heads + a.headsAtOnce - 1) / a.headsAtOnce),
-                       dim3(kBlock), kWaves * 2 * room * sizeof(float), stream, a);
+    a.headsAtOnce = FastDivide(heads);
+    a.headBlocks = FastDivide(blocks);
+    a.pairsPerToken = FastDivide(pairs);
+    a.tokensAtOnce = tokens;
+    a.units = uint32_t((a.tokens + tokens - 1) / tokens * blocks);
+    const uint32_t lds = tokens * ((pairs + 7) / 8 * 8) * sizeof(float2);
+    const dim3 grid(a.units < (1u << 22) ? a.units : 1u << 22);
+    auto with = [&](auto whole, auto behind) {
+        hipLaunchKernelGGL((rotaryKernel<T, kHalf, decltype(whole)::value, decltype(behind)::value>), grid, dim3(kBlock),
+                           lds, stream, a);
+    };
+    if (pairs >= P && per == turning) with(std::true_type{}, std::false_type{});
+    else if (pairs >= P && a.headDim - a.rotated >= uint32_t(kCopied)) with(std::true_type{}, std::true_type{});
+    else with(std::false_type{}, std::true_type{});
 }
 
 }  // namespace
