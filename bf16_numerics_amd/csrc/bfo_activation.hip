@@ -61,7 +61,7 @@ __device__ __forceinline__ void writeGroup(const CodeMatrix &m, const Place &p, 
     if (threadIdx.x % kLanes == 0) m.scales[p.row * g.perRow.by + p.group] = s.scale;
 }
 
-template <typename T, int kKind, bool kGated, int kType>
+template <typename T, int kKind, bool kGated, int kType, bool kStream>
 __global__ __launch_bounds__(kBlock) void actForwardKernel(ActivationForward a) {
     constexpr int E = 16 / int(sizeof(T));
     constexpr uint32_t kAt = kBlock / (kGroup / E);  // groups of a workgroup
@@ -69,8 +69,8 @@ __global__ __launch_bounds__(kBlock) void actForwardKernel(ActivationForward a) 
     for (uint32_t i = blockIdx.x * kAt + threadIdx.x / (kGroup / E); i < a.grid.count; i += gridDim.x * kAt) {
         const Place p = place<E>(a.grid, i);
         Chunk<T, E> gate, up;
-        gate.loadRow(static_cast<const T *>(a.gate.p) + p.row * a.gate.stride, p.c, C);
-        if constexpr (kGated) up.loadRow(static_cast<const T *>(a.up.p) + p.row * a.up.stride, p.c, C);
+        gate.template loadRow<kStream>(static_cast<const T *>(a.gate.p) + p.row * a.gate.stride, p.c, C);
+        if constexpr (kGated) up.template loadRow<kStream>(static_cast<const T *>(a.up.p) + p.row * a.up.stride, p.c, C);
         float g[E], u[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -88,19 +88,19 @@ __global__ __launch_bounds__(kBlock) void actForwardKernel(ActivationForward a) 
                 const Activation<kKind> f(g[e]);
                 y[e] = kGated ? f.act * u[e] : f.act;
             }
-            storeRow(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, 0, C, y);
+            storeRow<kStream>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, 0, C, y);
         }
     }
 }
 
 // A kept input: the matrix itself or its codes.
-template <typename T, int E, int kType>
+template <typename T, int E, int kType, bool kStream>
 __device__ __forceinline__ void readKept(const ConstMatrix &m, const ConstCodes &codes, const Place &p,
                                          const GroupGrid &g, float (&v)[E]) {
     const int C = int(g.cols);
     if constexpr (kType == kNoCodes) {
         Chunk<T, E> raw;
-        raw.loadRow(static_cast<const T *>(m.p) + p.row * m.stride, p.c, C);
+        raw.template loadRow<kStream>(static_cast<const T *>(m.p) + p.row * m.stride, p.c, C);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = raw[e];
     } else {
@@ -110,7 +110,7 @@ __device__ __forceinline__ void readKept(const ConstMatrix &m, const ConstCodes 
     }
 }
 
-template <typename T, int kKind, bool kGated, int kType>
+template <typename T, int kKind, bool kGated, int kType, bool kStream>
 __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a) {
     constexpr int E = 16 / int(sizeof(T));
     constexpr uint32_t kAt = kBlock / (kGroup / E);
@@ -118,14 +118,14 @@ __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a
     for (uint32_t i = blockIdx.x * kAt + threadIdx.x / (kGroup / E); i < a.grid.count; i += gridDim.x * kAt) {
         const Place p = place<E>(a.grid, i);
         float g[E], u[E], y[E];
-        readKept<T, E, kType>(a.gate, a.gateCodes, p, a.grid, g);
+        readKept<T, E, kType, kStream>(a.gate, a.gateCodes, p, a.grid, g);
         if constexpr (kKind == kIdentity) {
-            storeRow(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, 0, C, g);
+            storeRow<kStream>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, 0, C, g);
             continue;
         } else {
-            if constexpr (kGated) readKept<T, E, kType>(a.up, a.upCodes, p, a.grid, u);
+            if constexpr (kGated) readKept<T, E, kType, kStream>(a.up, a.upCodes, p, a.grid, u);
             Chunk<T, E> d;
-            d.loadRow(static_cast<const T *>(a.dout.p) + p.row * a.dout.stride, p.c, C);
+            d.template loadRow<kStream>(static_cast<const T *>(a.dout.p) + p.row * a.dout.stride, p.c, C);
             float act[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -133,16 +133,16 @@ __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a
                 act[e] = f.act;
                 y[e] = (kGated ? d[e] * u[e] : d[e]) * f.slope;
             }
-            storeRow(static_cast<T *>(a.dgate.p) + p.row * a.dgate.stride, p.c, 0, C, y);
+            storeRow<kStream>(static_cast<T *>(a.dgate.p) + p.row * a.dgate.stride, p.c, 0, C, y);
             if constexpr (kGated) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] = d[e] * act[e];
-                storeRow(static_cast<T *>(a.dup.p) + p.row * a.dup.stride, p.c, 0, C, y);
+                storeRow<kStream>(static_cast<T *>(a.dup.p) + p.row * a.dup.stride, p.c, 0, C, y);
             }
             if (a.out.p) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] = kGated ? act[e] * u[e] : act[e];
-                storeRow(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, 0, C, y);
+                storeRow<kStream>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, 0, C, y);
             }
         }
     }
@@ -151,21 +151,26 @@ __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a
 template <int kValue>
 using Const = std::integral_constant<int, kValue>;
 
-// f(type, kind, gated, code type) with the call's values as constants.
+// f(type, kind, gated, code type, streamed) with the call's values as constants.
 template <typename F>
-hipError_t byKind(int dtype, int kind, bool gated, int codeType, F f) {
-    auto coded = [&](auto t, auto k, auto g) {
-        if (codeType == BFO_I8) f(t, k, g, Const<BFO_I8>{});
-        else if (codeType == BFO_E4M3) f(t, k, g, Const<BFO_E4M3>{});
-        else if constexpr (decltype(k)::value != kIdentity) f(t, k, g, Const<kNoCodes>{});
+hipError_t byKind(int dtype, int kind, bool gated, int codeType, bool streamed, F f) {
+    auto coded = [&](auto t, auto k, auto g, auto s) {
+        if (codeType == BFO_I8) f(t, k, g, Const<BFO_I8>{}, s);
+        else if (codeType == BFO_E4M3) f(t, k, g, Const<BFO_E4M3>{}, s);
+        else if constexpr (decltype(k)::value != kIdentity) f(t, k, g, Const<kNoCodes>{}, s);
     };
-    auto kinds = [&](auto t) {
-        if (kind == kIdentity) coded(t, Const<kIdentity>{}, std::false_type{});
-        else if (kind == BFO_SILU) gated ? coded(t, Const<BFO_SILU>{}, std::true_type{}) : coded(t, Const<BFO_SILU>{}, std::false_type{});
-        else gated ? coded(t, Const<BFO_GELU>{}, std::true_type{}) : coded(t, Const<BFO_GELU>{}, std::false_type{});
+    auto gates = [&](auto t, auto k, auto s) {
+        if constexpr (decltype(k)::value == kIdentity) coded(t, k, std::false_type{}, s);
+        else gated ? coded(t, k, std::true_type{}, s) : coded(t, k, std::false_type{}, s);
     };
-    if (dtype == BFO_BF16) kinds(bf16_t(0));
-    else kinds(float(0));
+    auto kinds = [&](auto t, auto s) {
+        if (kind == kIdentity) gates(t, Const<kIdentity>{}, s);
+        else if (kind == BFO_SILU) gates(t, Const<BFO_SILU>{}, s);
+        else gates(t, Const<BFO_GELU>{}, s);
+    };
+    auto streams = [&](auto t) { streamed ? kinds(t, std::true_type{}) : kinds(t, std::false_type{}); };
+    if (dtype == BFO_BF16) streams(bf16_t(0));
+    else streams(float(0));
     return hipGetLastError();
 }
 
@@ -177,24 +182,37 @@ dim3 workgroups(const GroupGrid &g) {
     return dim3(n < most ? n : most);
 }
 
+// Bytes of `matrices` matrices and `codes` matrices in codes.
+uint64_t bytes(const GroupGrid &g, int dtype, int matrices, int codes) {
+    return uint64_t(g.count / g.perRow.by) * g.cols * (matrices * (dtype == BFO_BF16 ? 2 : 4) + codes);
+}
+
 }  // namespace
 
 hipError_t launchActivationForward(const ActivationForward &a, hipStream_t stream) {
     if (!a.grid.count) return hipSuccess;
-    return byKind(a.dtype, a.kind, a.up.p != nullptr, a.codeType, [&](auto t, auto kind, auto gated, auto type) {
-        using T = decltype(t);
-        hipLaunchKernelGGL((actForwardKernel<T, decltype(kind)::value, decltype(gated)::value, decltype(type)::value>),
-                           workgroups<T>(a.grid), dim3(kBlock), 0, stream, a);
-    });
+    const int inputs = a.up.p ? 2 : 1;
+    const bool streamed = streams(bytes(a.grid, a.dtype, inputs + 1, a.codeType == kNoCodes ? 0 : inputs));
+    return byKind(a.dtype, a.kind, a.up.p != nullptr, a.codeType, streamed,
+                  [&](auto t, auto kind, auto gated, auto type, auto nt) {
+                      using T = decltype(t);
+                      hipLaunchKernelGGL((actForwardKernel<T, decltype(kind)::value, decltype(gated)::value,
+                                                           decltype(type)::value, decltype(nt)::value>),
+                                         workgroups<T>(a.grid), dim3(kBlock), 0, stream, a);
+                  });
 }
 
 hipError_t launchActivationBackward(const ActivationBackward &a, hipStream_t stream) {
     if (!a.grid.count) return hipSuccess;
-    return byKind(a.dtype, a.kind, a.dup.p != nullptr, a.codeType, [&](auto t, auto kind, auto gated, auto type) {
-        using T = decltype(t);
-        hipLaunchKernelGGL((actBackwardKernel<T, decltype(kind)::value, decltype(gated)::value, decltype(type)::value>),
-                           workgroups<T>(a.grid), dim3(kBlock), 0, stream, a);
-    });
+    const int inputs = a.dup.p ? 2 : 1, coded = a.codeType == kNoCodes ? 0 : inputs;
+    const bool streamed = streams(bytes(a.grid, a.dtype, 1 + inputs - coded + inputs + (a.out.p ? 1 : 0), coded));
+    return byKind(a.dtype, a.kind, a.dup.p != nullptr, a.codeType, streamed,
+                  [&](auto t, auto kind, auto gated, auto type, auto nt) {
+                      using T = decltype(t);
+                      hipLaunchKernelGGL((actBackwardKernel<T, decltype(kind)::value, decltype(gated)::value,
+                                                            decltype(type)::value, decltype(nt)::value>),
+                                         workgroups<T>(a.grid), dim3(kBlock), 0, stream, a);
+                  });
 }
 
 }  // namespace bfo

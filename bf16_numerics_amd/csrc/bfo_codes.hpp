@@ -99,6 +99,15 @@ __device__ __forceinline__ void decode(const uint32_t (&w)[N / 4], float scale, 
     }
 }
 
+template <int N>
+__device__ __forceinline__ void getCodes(const uint8_t *p, uint32_t (&w)[N / 4]) {
+    if constexpr (N == 8) {
+        const Bytes8 q = *reinterpret_cast<const Bytes8 *>(p);
+        w[0] = q.x, w[1] = q.y;
+    } else {
+        w[0] = *reinterpret_cast<const Bytes4 *>(p);
+    }
+}
 // Codes of the columns [c, c + N) of those from `base` on, of which [0, cols)
 // are there; 0 for the others, and for all if not `live`.
 template <int N>
@@ -106,12 +115,7 @@ __device__ __forceinline__ void loadCodes(const uint8_t *base, int c, int cols, 
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) w[i] = 0u;
     if (live && c + N <= cols) {
-        if constexpr (N == 8) {
-            const Bytes8 q = *reinterpret_cast<const Bytes8 *>(base + c);
-            w[0] = q.x, w[1] = q.y;
-        } else {
-            w[0] = *reinterpret_cast<const Bytes4 *>(base + c);
-        }
+        getCodes<N>(base + c, w);
     } else if (live && c < cols) {
 #pragma unroll
         for (int i = 0; i < N; ++i)

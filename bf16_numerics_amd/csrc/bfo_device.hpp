@@ -79,15 +79,20 @@ struct Chunk {
             else w[i] = packBf16((*this)[2 * i] + o[2 * i], (*this)[2 * i + 1] + o[2 * i + 1]);
         }
     }
+    template <bool kNontemporal = false>
     __device__ __forceinline__ void store(T *p) const {
 #pragma unroll
-        for (int i = 0; i < kWords; i += 4)
-            *(reinterpret_cast<Words4 *>(p) + i / 4) = Words4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+        for (int i = 0; i < kWords; i += 4) {
+            const Words4 v{w[i], w[i + 1], w[i + 2], w[i + 3]};
+            if constexpr (kNontemporal) __builtin_nontemporal_store(v, reinterpret_cast<Words4 *>(p) + i / 4);
+            else *(reinterpret_cast<Words4 *>(p) + i / 4) = v;
+        }
     }
     // Stores the columns [c, c + N) of those from `base` on that lie in [0, cols).
+    template <bool kNontemporal = false>
     __device__ __forceinline__ void storeRow(T *base, int c, int cols) const {
         if (c + N <= cols) {
-            store(base + c);
+            store<kNontemporal>(base + c);
         } else if (c < cols) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -98,9 +103,10 @@ struct Chunk {
     // 0 for the others, and for all if not `live`.  The zeros come first, so that
     // no load waits for another one's lanes.  Here and below a `base` that is the
     // same in all lanes keeps the addresses at one scalar and one lane offset.
+    template <bool kNontemporal = false>
     __device__ __forceinline__ void loadRow(const T *base, int c, int cols, bool live = true) {
         zero();
-        if (live && c + N <= cols) load(base + c);
+        if (live && c + N <= cols) load<kNontemporal>(base + c);
         else if (live && c < cols) loadPart(base, c, 0, cols);
     }
     // The same with [lo, hi) there and -inf elsewhere.
@@ -130,19 +136,10 @@ struct Chunk {
 template <bool kNontemporal = false, typename T, int N>
 __device__ __forceinline__ void storeRow(T *base, int c, int lo, int hi, const float (&v)[N]) {
     if (c >= lo && c + N <= hi) {
-        uint32_t w[N * sizeof(T) / 4];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
-            else if (i % 2 == 0) w[i / 2] = packBf16(v[i], v[i + 1]);
-        }
-#pragma unroll
-        for (int i = 0; i < int(N * sizeof(T) / 4); i += 4) {
-            Words4 *p = reinterpret_cast<Words4 *>(base + c) + i / 4;
-            const Words4 q{w[i], w[i + 1], w[i + 2], w[i + 3]};
-            if constexpr (kNontemporal) __builtin_nontemporal_store(q, p);
-            else *p = q;
-        }
+        Chunk<T, N> q(v);
+        // The compiler stores values that it has just rounded to bf16 without the hint.
+        if constexpr (kNontemporal) q.forget();
+        q.template store<kNontemporal>(base + c);
     } else if (c + N > lo && c < hi) {
 #pragma unroll
         for (int i = 0; i < N; ++i)

@@ -68,45 +68,91 @@ __device__ __forceinline__ void writeCodes(const RmsNormForward &a, uint64_t row
     }
 }
 
+// E weights from column c on, 0 behind the last.
+template <int E>
+__device__ __forceinline__ void loadWeights(const void *weight, int type, int c, int C, float (&w)[E]) {
+    if (type == BFO_BF16) {
+        Chunk<bf16_t, E> q;
+        q.loadRow(static_cast<const bf16_t *>(weight), c, C);
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] = q[e];
+    } else {
+        Chunk<float, E> q;
+        q.loadRow(static_cast<const float *>(weight), c, C);
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] = q[e];
+    }
+}
+
+// How a row's chunks are loaded.  kEven, for widths of whole chunks: without a
+// branch, from the row's last chunk where there is none, whose values the caller
+// drops (an earlier row's loads need not be waited for at the branch's end).
+enum Loads { kAny, kEven, kEvenStream };
+template <Loads kLoads, typename T, int E>
+__device__ __forceinline__ void loadChunk(Chunk<T, E> &w, const T *row, int c, int C, bool live) {
+    if constexpr (kLoads == kAny) w.loadRow(row, c, C, live);
+    else w.template load<kLoads == kEvenStream>(row + min(c, C - E));
+}
+template <Loads kLoads, typename T, int E>
+__device__ __forceinline__ void storeChunk(T *row, int c, int C, const float (&v)[E]) {
+    if constexpr (kLoads == kAny) {
+        storeRow(row, c, 0, C, v);
+    } else if (c < C) {
+        Chunk<T, E> q(v);
+        // The compiler stores values that it has just rounded to bf16 without the hint.
+        if constexpr (kLoads == kEvenStream) q.forget();
+        q.template store<kLoads == kEvenStream>(row + c);
+    }
+}
+// The row to load from.
+template <Loads kLoads>
+__device__ __forceinline__ uint64_t loadedRow(uint64_t row, uint64_t rows) {
+    return kLoads == kAny ? row : min(row, rows - 1);
+}
+
 // kLanes lanes own a row, kChunks 16-byte chunks each; kBlock / kLanes rows
 // per workgroup at a time.
-template <typename T, typename W, int kLanes, int kChunks, int kBlock>
+template <typename T, Loads kLoads, int kLanes, int kChunks, int kBlock>
 __global__ __launch_bounds__(kBlock) void rmsForwardKernel(RmsNormForward a) {
     constexpr int E = 16 / int(sizeof(T));
     constexpr int kRows = kBlock / kLanes;
     constexpr int kWidth = kLanes * E;  // columns from chunk to chunk
+    constexpr bool kStream = kLoads == kEvenStream;
     __shared__ float red[2][kBlock / 64][1];
     __shared__ uint32_t most[2][kBlock / 64];
     const int lane = int(threadIdx.x % kLanes), c = lane * E, C = int(a.cols);
     const float inv = 1.0f / float(C);
-    Chunk<W, E> w[kChunks];
+    float w[kChunks][E];
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) w[k].loadRow(static_cast<const W *>(a.weight) + kWidth * k, c, C - kWidth * k);
+    for (int k = 0; k < kChunks; ++k) loadWeights(a.weight, a.paramDtype, kWidth * k + c, C, w[k]);
     int turn = 0;
     for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < a.rows; base += uint64_t(gridDim.x) * kRows) {
-        const uint64_t row = base + rowGroup<kLanes>();
+        const uint64_t row = base + rowGroup<kLanes>(), from = loadedRow<kLoads>(row, a.rows);
         const bool live = row < a.rows;
-        const T *x = static_cast<const T *>(a.x.p) + row * a.x.stride;
-        Chunk<T, E> raw[kChunks], more[kChunks];
+        Chunk<T, E> raw[kChunks];
+        const T *x = static_cast<const T *>(a.x.p) + from * a.x.stride;
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) raw[k].loadRow(x + kWidth * k, c, C - kWidth * k, live);
+        for (int k = 0; k < kChunks; ++k) loadChunk<kLoads>(raw[k], x, kWidth * k + c, C, live);
         if (a.residual.p) {
-            const T *r = static_cast<const T *>(a.residual.p) + row * a.residual.stride;
+            Chunk<T, E> more[kChunks];
+            const T *r = static_cast<const T *>(a.residual.p) + from * a.residual.stride;
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k) more[k].loadRow(r + kWidth * k, c, C - kWidth * k, live);
+            for (int k = 0; k < kChunks; ++k) loadChunk<kLoads>(more[k], r, kWidth * k + c, C, live);
 #pragma unroll
             for (int k = 0; k < kChunks; ++k) raw[k].add(more[k]);
             if (a.total.p && live) {
                 T *t = static_cast<T *>(a.total.p) + row * a.total.stride;
 #pragma unroll
-                for (int k = 0; k < kChunks; ++k) raw[k].storeRow(t + kWidth * k, c, C - kWidth * k);
+                for (int k = 0; k < kChunks; ++k) raw[k].template storeRow<kStream>(t, kWidth * k + c, C);
             }
         }
         float s[1] = {0.0f};
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k)
+        for (int k = 0; k < kChunks; ++k) {
+            if (kLoads != kAny && kWidth * k + c >= C) raw[k].zero();
 #pragma unroll
             for (int e = 0; e < E; ++e) s[0] = fmaf(raw[k][e], raw[k][e], s[0]);
+        }
         rowSums<kLanes, kBlock>(s, red[turn]);
         const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
         float v[kChunks][E];
@@ -120,11 +166,9 @@ __global__ __launch_bounds__(kBlock) void rmsForwardKernel(RmsNormForward a) {
             else writeCodes<BFO_E4M3, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
         }
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-            w[k].forget();
+        for (int k = 0; k < kChunks; ++k)
 #pragma unroll
             for (int e = 0; e < E; ++e) v[k][e] *= w[k][e];
-        }
         if (a.codes.p && a.codesOfOut) {
             if (a.codeType == BFO_I8) writeCodes<BFO_I8, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
             else writeCodes<BFO_E4M3, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
@@ -133,46 +177,120 @@ __global__ __launch_bounds__(kBlock) void rmsForwardKernel(RmsNormForward a) {
         if (a.out.p && live) {
             T *out = static_cast<T *>(a.out.p) + row * a.out.stride;
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k) storeRow(out + kWidth * k, c, 0, C - kWidth * k, v[k]);
+            for (int k = 0; k < kChunks; ++k) storeChunk<kLoads>(out, kWidth * k + c, C, v[k]);
         }
     }
 }
 
-// The normalised values of a row: kept as the row itself, or as codes.
-template <typename T, int E, bool kCoded>
+// The normalised values of N columns: kept as the row itself, or as codes.
+template <typename T, int N, bool kCoded, Loads kLoads>
 struct Normalised;
-template <typename T, int E>
-struct Normalised<T, E, false> {
-    Chunk<T, E> raw;
-    __device__ __forceinline__ void load(const RmsNormBackward &a, uint64_t row, int first, int c, bool live) {
-        raw.loadRow(static_cast<const T *>(a.x.p) + row * a.x.stride + first, c, int(a.cols) - first, live);
+template <typename T, int N, Loads kLoads>
+struct Normalised<T, N, false, kLoads> {
+    Chunk<T, N> raw;
+    __device__ __forceinline__ void load(const RmsNormBackward &a, uint64_t row, int c, bool live) {
+        loadChunk<kLoads>(raw, static_cast<const T *>(a.x.p) + row * a.x.stride, c, int(a.cols), live);
     }
-    __device__ __forceinline__ void values(const RmsNormBackward &, float rstd, float (&v)[E]) const {
+    __device__ __forceinline__ void values(const RmsNormBackward &, float rstd, float (&v)[N]) const {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = raw[e] * rstd;
+        for (int e = 0; e < N; ++e) v[e] = raw[e] * rstd;
     }
 };
-template <typename T, int E>
-struct Normalised<T, E, true> {
-    uint32_t w[E / 4];
+template <typename T, int N, Loads kLoads>
+struct Normalised<T, N, true, kLoads> {
+    uint32_t w[N / 4];
     float scale;
-    __device__ __forceinline__ void load(const RmsNormBackward &a, uint64_t row, int first, int c, bool live) {
+    __device__ __forceinline__ void load(const RmsNormBackward &a, uint64_t row, int c, bool live) {
         const int C = int(a.cols);
-        loadCodes<E>(static_cast<const uint8_t *>(a.codes.p) + row * a.codes.stride + first, c, C - first, live, w);
-        const uint32_t groups = a.group ? (a.cols + kGroup - 1) / kGroup : 1;
-        const uint32_t group = a.group ? uint32_t(first + c) / kGroup : 0;
-        scale = live && first + c < C ? a.scales[row * groups + group] : 0.0f;
+        const uint8_t *codes = static_cast<const uint8_t *>(a.codes.p) + row * a.codes.stride;
+        if constexpr (kLoads == kAny) {
+            loadCodes<N>(codes, c, C, live, w);
+        } else {
+            c = min(c, C - N);
+            getCodes<N>(codes + c, w);
+        }
+        const uint32_t groups = a.group ? (a.cols + kGroup - 1) / kGroup : 1, group = a.group ? uint32_t(c) / kGroup : 0;
+        scale = kLoads != kAny || (live && c < C) ? a.scales[row * groups + group] : 0.0f;
     }
-    __device__ __forceinline__ void values(const RmsNormBackward &a, float, float (&v)[E]) const {
-        if (a.codeType == BFO_I8) decode<BFO_I8, E>(w, scale, v);
-        else decode<BFO_E4M3, E>(w, scale, v);
+    __device__ __forceinline__ void values(const RmsNormBackward &a, float, float (&v)[N]) const {
+        if (a.codeType == BFO_I8) decode<BFO_I8, N>(w, scale, v);
+        else decode<BFO_E4M3, N>(w, scale, v);
     }
 };
+
+// dx of the rows first, first + step, ... of a workgroup's kBlock / kLanes row
+// groups; with kSums, each lane's sums of dout * xhat per column.
+template <typename T, bool kCoded, Loads kLoads, int kLanes, int kChunks, int kBlock, bool kSums, int kSlots, int E>
+__device__ __forceinline__ void rowGradients(const RmsNormBackward &a, uint64_t first, uint64_t step,
+                                             float (&red)[2][kBlock / 64][1], float (&dw)[kSlots][E]) {
+    constexpr int kWidth = kLanes * E;
+    const int c = int(threadIdx.x % kLanes) * E, C = int(a.cols);
+    const uint32_t sub = rowGroup<kLanes>();
+    const float inv = 1.0f / float(C);
+    const bool addDx = (a.accumulate & BFO_ACCUMULATE_DX) != 0;
+    float w[kChunks][E];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) loadWeights(a.weight, a.paramDtype, kWidth * k + c, C, w[k]);
+    int turn = 0;
+    for (uint64_t base = first; base < a.rows; base += step) {
+        const uint64_t row = base + sub, from = loadedRow<kLoads>(row, a.rows);
+        const bool live = row < a.rows;
+        const float rstd = kLoads != kAny || live ? a.rstd[from] : 0.0f;
+        const T *g = static_cast<const T *>(a.dout.p) + from * a.dout.stride;
+        Normalised<T, E, kCoded, kLoads> kept[kChunks];
+        Chunk<T, E> gr[kChunks];
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+            kept[k].load(a, from, kWidth * k + c, live);
+            loadChunk<kLoads>(gr[k], g, kWidth * k + c, C, live);
+        }
+        float xhat[kChunks][E], h[kChunks][E], s[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+            kept[k].values(a, rstd, xhat[k]);
+            if (kLoads != kAny && (!live || kWidth * k + c >= C)) {
+                gr[k].zero();
+#pragma unroll
+                for (int e = 0; e < E; ++e) xhat[k][e] = 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                h[k][e] = gr[k][e] * w[k][e];
+                s[0] = fmaf(h[k][e], xhat[k][e], s[0]);
+                if constexpr (kSums) dw[k][e] = fmaf(gr[k][e], xhat[k][e], dw[k][e]);
+            }
+        }
+        rowSums<kLanes, kBlock>(s, red[turn]);
+        turn ^= 1;
+        if (!live) continue;
+        const float mean = s[0] * inv;
+        T *dx = static_cast<T *>(a.dx.p) + row * a.dx.stride;
+        T *out = static_cast<T *>(a.out.p) + row * a.out.stride;
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+            float y[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] = fmaf(-xhat[k][e], mean, h[k][e]) * rstd;
+            if (addDx) {
+                Chunk<T, E> old;
+                old.loadRow(dx, kWidth * k + c, C);
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] += old[e];
+            }
+            storeChunk<kLoads>(dx, kWidth * k + c, C, y);
+            if (a.out.p) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = xhat[k][e] * w[k][e];
+                storeChunk<kLoads>(out, kWidth * k + c, C, y);
+            }
+        }
+    }
+}
 
 // Stage 1: dx of the workgroup's rows, and its sums of dout * xhat per column,
 // which stay in registers over the rows, are added over the row groups through
 // LDS and end as one row of the partials.
-template <typename T, typename W, bool kCoded, int kLanes, int kChunks, int kBlock>
+template <typename T, bool kCoded, Loads kLoads, int kLanes, int kChunks, int kBlock>
 __global__ __launch_bounds__(kBlock) void rmsBackwardKernel(RmsNormBackward a) {
     constexpr int E = 16 / int(sizeof(T));
     constexpr int kRows = kBlock / kLanes;
@@ -181,65 +299,11 @@ __global__ __launch_bounds__(kBlock) void rmsBackwardKernel(RmsNormBackward a) {
     __shared__ float sums[kRows > 1 ? kChunks * E * kLanes : 1];
     const int lane = int(threadIdx.x % kLanes), c = lane * E, C = int(a.cols);
     const uint32_t sub = rowGroup<kLanes>();
-    const float inv = 1.0f / float(C);
-    const bool addDx = (a.accumulate & BFO_ACCUMULATE_DX) != 0;
-    Chunk<W, E> w[kChunks];
     float dw[kChunks][E];
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) {
-        w[k].loadRow(static_cast<const W *>(a.weight) + kWidth * k, c, C - kWidth * k);
-#pragma unroll
-        for (int e = 0; e < E; ++e) dw[k][e] = 0.0f;
-    }
-    int turn = 0;
-    for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < a.rows; base += uint64_t(gridDim.x) * kRows) {
-        const uint64_t row = base + sub;
-        const bool live = row < a.rows;
-        const T *g = static_cast<const T *>(a.dout.p) + row * a.dout.stride;
-        const float rstd = live ? a.rstd[row] : 0.0f;
-        Normalised<T, E, kCoded> kept[kChunks];
-        Chunk<T, E> gr[kChunks];
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-            kept[k].load(a, row, kWidth * k, c, live);
-            gr[k].loadRow(g + kWidth * k, c, C - kWidth * k, live);
-        }
-        float xhat[kChunks][E], s[1] = {0.0f};
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-            w[k].forget();
-            kept[k].values(a, rstd, xhat[k]);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                s[0] = fmaf(gr[k][e] * w[k][e], xhat[k][e], s[0]);
-                dw[k][e] = fmaf(gr[k][e], xhat[k][e], dw[k][e]);
-            }
-        }
-        rowSums<kLanes, kBlock>(s, red[turn]);
-        turn ^= 1;
-        if (!live) continue;
-        const float mean = s[0] * inv;
-        T *dx = static_cast<T *>(a.dx.p) + row * a.dx.stride;
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-            w[k].forget();
-            float y[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) y[e] = fmaf(-xhat[k][e], mean, gr[k][e] * w[k][e]) * rstd;
-            if (addDx) {
-                Chunk<T, E> old;
-                old.loadRow(dx + kWidth * k, c, C - kWidth * k);
-#pragma unroll
-                for (int e = 0; e < E; ++e) y[e] += old[e];
-            }
-            storeRow(dx + kWidth * k, c, 0, C - kWidth * k, y);
-            if (a.out.p) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = xhat[k][e] * w[k][e];
-                storeRow(static_cast<T *>(a.out.p) + row * a.out.stride + kWidth * k, c, 0, C - kWidth * k, y);
-            }
-        }
-    }
+    for (int i = 0; i < kChunks * E; ++i) dw[i / E][i % E] = 0.0f;
+    rowGradients<T, kCoded, kLoads, kLanes, kChunks, kBlock, true>(a, uint64_t(blockIdx.x) * kRows,
+                                                                   uint64_t(gridDim.x) * kRows, red, dw);
     if constexpr (kRows > 1) {
         // The groups add in turn: group 0 first, then 1, ...
         __syncthreads();
@@ -258,11 +322,70 @@ __global__ __launch_bounds__(kBlock) void rmsBackwardKernel(RmsNormBackward a) {
     }
     float *part = a.partials + uint64_t(blockIdx.x) * C;
 #pragma unroll
-    for (int k = 0; k < kChunks; ++k) storeRow(part + kWidth * k, c, 0, C - kWidth * k, dw[k]);
+    for (int k = 0; k < kChunks; ++k) storeRow(part, kWidth * k + c, 0, C, dw[k]);
 }
 
-// How a row of up to kCols columns is spread, as layer norm's rows are: kLanes
-// lanes hold it in kChunks 16-byte chunks each, in workgroups of kBlock lanes.
+// Few rows, in one launch and without partials: rstd is given, so dweight needs
+// nothing of dx.  The first workgroups sum kSlabCols columns each over all rows (4
+// columns a lane), the others form dx; both read dout and the kept rows, which the
+// caches hold.
+template <typename T, bool kCoded, int kLanes, int kChunks, int kBlock, int kSlabCols>
+__global__ __launch_bounds__(kBlock) void rmsBackwardFewKernel(RmsNormBackward a, uint32_t slabs) {
+    constexpr int E = 16 / int(sizeof(T));
+    constexpr int kRows = kBlock / kLanes;
+    constexpr int N = 4, kRowLanes = kSlabCols / N, kGroups = kBlock / kRowLanes, kAtOnce = 4;
+    constexpr int kParts = kBlock / kSlabCols;  // lanes that add one column's sums
+    __shared__ float red[2][kBlock / 64][1];
+    __shared__ float sums[kGroups][kSlabCols + 1];
+    if (blockIdx.x >= slabs) {
+        float none[1][E];
+        rowGradients<T, kCoded, kAny, kLanes, kChunks, kBlock, false>(a, uint64_t(blockIdx.x - slabs) * kRows,
+                                                                      uint64_t(gridDim.x - slabs) * kRows, red, none);
+        return;
+    }
+    const int c0 = int(Slabs<T, kSlabCols>::firstColumn(blockIdx.x)), C = int(a.cols);
+    if (c0 >= C) return;
+    const int c = c0 + int(threadIdx.x % kRowLanes) * N;
+    const uint32_t group = threadIdx.x / kRowLanes;
+    float dw[N] = {};
+    for (uint64_t base = group; base < a.rows; base += kGroups * kAtOnce) {
+        Normalised<T, N, kCoded, kAny> kept[kAtOnce];
+        Chunk<T, N> gr[kAtOnce];
+        float rstd[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const uint64_t row = base + kGroups * i;
+            const bool live = row < a.rows;
+            kept[i].load(a, row, c, live);
+            gr[i].loadRow(static_cast<const T *>(a.dout.p) + row * a.dout.stride, c, C, live);
+            rstd[i] = live ? a.rstd[row] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            float xhat[N];
+            kept[i].values(a, rstd[i], xhat);
+#pragma unroll
+            for (int e = 0; e < N; ++e) dw[e] = fmaf(gr[i][e], xhat[e], dw[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) sums[group][c - c0 + e] = dw[e];
+    __syncthreads();
+    const int column = int(threadIdx.x) / kParts, part = int(threadIdx.x) % kParts;
+    float t = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kGroups / kParts; ++g) t += sums[part * (kGroups / kParts) + g][column];
+#pragma unroll
+    for (int d = 1; d < kParts; d *= 2) t += __shfl_xor(t, d, 64);
+    if (part == 0 && c0 + column < C) {
+        const bool add = (a.accumulate & BFO_ACCUMULATE_PARAMS) != 0;
+        if (a.paramDtype == BFO_BF16) storeParam(static_cast<bf16_t *>(a.dweight) + c0 + column, t, add);
+        else storeParam(static_cast<float *>(a.dweight) + c0 + column, t, add);
+    }
+}
+
+// How a row of up to kCols columns is spread: kLanes lanes hold it in kChunks
+// 16-byte chunks each, in workgroups of kBlock lanes.
 template <int kWidth, typename T>
 struct ForwardShape {
     static constexpr int kCols = kWidth == 0 ? 128 : 256 << kWidth;
@@ -273,56 +396,110 @@ struct ForwardShape {
 template <int kWidth, typename T>
 struct BackwardShape {
     static constexpr int kCols = kWidth == 0 ? 128 : 256 << kWidth;
-    static constexpr int kLanes = kWidth == 0 ? 8 * int(sizeof(T)) : kWidth < 6 ? 32 << kWidth : 1024;
+    static constexpr int kWide = 8 * int(sizeof(T)) << kWidth;  // two chunks a lane
+    static constexpr int kLanes = kWidth == 0 ? 8 * int(sizeof(T)) : kWide < 64 ? 64 : kWide > 1024 ? 1024 : kWide;
     static constexpr int kChunks = kCols / kLanes / (16 / int(sizeof(T)));
     static constexpr int kBlock = kWidth == 0 ? 256 : kLanes < 512 ? 512 : kLanes;
     static constexpr int kRows = kBlock / kLanes;
 };
 
+// Up to here one launch for all gradients takes no longer than rows and partials.
+uint64_t fewRows(uint32_t cols) { return cols <= 2048 ? 2048 : cols <= 4096 ? 1024 : 512; }
+template <int kCols, typename F>
+void bySlab(uint64_t rows, F f) {
+    if constexpr (kCols > 4096) f(std::integral_constant<int, 32>{});
+    else if constexpr (kCols > 2048) f(std::integral_constant<int, 16>{});
+    else if (rows <= 512) f(std::integral_constant<int, 16>{});
+    else f(std::integral_constant<int, 8>{});
+}
+
+template <Loads kValue>
+using Constant = std::integral_constant<Loads, kValue>;
+
+// f with the way to load rows of a call that moves `bytes`.
+template <typename T, typename F>
+void byLoads(uint32_t cols, uint64_t bytes, F f) {
+    if (cols % (16 / sizeof(T))) f(Constant<kAny>{});
+    else if (streams(bytes)) f(Constant<kEvenStream>{});
+    else f(Constant<kEven>{});
+}
+
+template <typename F>
+void byType(int dtype, F f) {
+    dtype == BFO_BF16 ? f(bf16_t(0)) : f(float(0));
+}
+
 }  // namespace
 
 uint32_t rmsBackwardBlocks(uint64_t rows, uint32_t cols) {
+    if (rows <= fewRows(cols)) return 0;
     const int perBlock = byWidth(cols, [](auto width) { return BackwardShape<decltype(width)::value, bf16_t>::kRows; });
-    return gridFor(rows, perBlock, cols <= 4096 ? 512 : 256);
+    return gridFor(rows, perBlock, cols <= 8192 ? 512 : 256);
 }
 
+// Up to 8,192 columns the size grows with both: more columns mean no fewer
+// workgroups, from no more rows on.  Above, there are half as many workgroups.
 uint64_t rmsWorkspaceBound(uint64_t rows, uint32_t cols) {
-    const uint64_t own = rmsWorkspaceBytes(rows, cols), narrower = cols > 4096 ? rmsWorkspaceBytes(rows, 4096) : 0;
+    const uint64_t own = rmsWorkspaceBytes(rows, cols), narrower = cols > 8192 ? rmsWorkspaceBytes(rows, 8192) : 0;
     return own > narrower ? own : narrower;
 }
 
 hipError_t launchRmsNormForward(const RmsNormForward &a, hipStream_t stream) {
     if (!a.rows) return hipSuccess;
-    return byTypes(a.dtype, a.paramDtype, [&](auto t, auto w) {
-        byWidth(a.cols, [&](auto width) {
-            using S = ForwardShape<decltype(width)::value, decltype(t)>;
-            const uint32_t most = 256 * 16 * 256 / S::kBlock;
-            hipLaunchKernelGGL((rmsForwardKernel<decltype(t), decltype(w), S::kLanes, S::kChunks, S::kBlock>),
-                               dim3(gridFor(a.rows, S::kBlock / S::kLanes, most)), dim3(S::kBlock), 0, stream, a);
+    byType(a.dtype, [&](auto t) {
+        using T = decltype(t);
+        const int matrices = 1 + (a.residual.p ? 1 : 0) + (a.total.p ? 1 : 0) + (a.out.p ? 1 : 0);
+        byLoads<T>(a.cols, a.rows * a.cols * (matrices * sizeof(T) + (a.codes.p ? 1 : 0)), [&](auto loads) {
+            byWidth(a.cols, [&](auto width) {
+                using S = ForwardShape<decltype(width)::value, T>;
+                // At most 16 workgroups of 256 lanes a CU, which keep their weights over
+                // their rows.
+                const uint32_t most = 256 * 16 * 256 / S::kBlock;
+                hipLaunchKernelGGL((rmsForwardKernel<T, decltype(loads)::value, S::kLanes, S::kChunks, S::kBlock>),
+                                   dim3(gridFor(a.rows, S::kBlock / S::kLanes, most)), dim3(S::kBlock), 0, stream, a);
+            });
         });
     });
+    return hipGetLastError();
 }
 
 hipError_t launchRmsNormBackward(const RmsNormBackward &a, hipStream_t stream) {
     const uint32_t blocks = rmsBackwardBlocks(a.rows, a.cols);
-    return byTypes(a.dtype, a.paramDtype, [&](auto t, auto w) {
-        using T = decltype(t);
+    if (a.rows)
+        byType(a.dtype, [&](auto t) {
+            using T = decltype(t);
+            auto wide = [&](auto coded) {
+                byWidth(a.cols, [&](auto width) {
+                    using S = BackwardShape<decltype(width)::value, T>;
+                    if (blocks) {
+                        const int matrices = 2 + (a.x.p ? 1 : 0) + (a.out.p ? 1 : 0);
+                        byLoads<T>(a.cols, a.rows * a.cols * (matrices * sizeof(T) + (a.x.p ? 0 : 1)), [&](auto loads) {
+                            hipLaunchKernelGGL((rmsBackwardKernel<T, decltype(coded)::value, decltype(loads)::value,
+                                                                  S::kLanes, S::kChunks, S::kBlock>),
+                                               dim3(blocks), dim3(S::kBlock), 0, stream, a);
+                        });
+                    } else {
+                        bySlab<S::kCols>(a.rows, [&](auto columns) {
+                            constexpr int kSlabCols = decltype(columns)::value;
+                            const uint32_t slabs = Slabs<T, kSlabCols>::workgroups(a.cols);
+                            hipLaunchKernelGGL((rmsBackwardFewKernel<T, decltype(coded)::value, S::kLanes, S::kChunks,
+                                                                     S::kBlock, kSlabCols>),
+                                               dim3(slabs + gridFor(a.rows, S::kRows, 1024)), dim3(S::kBlock), 0,
+                                               stream, a, slabs);
+                        });
+                    }
+                });
+            };
+            a.codes.p ? wide(std::true_type{}) : wide(std::false_type{});
+        });
+    if (blocks || !a.rows) byType(a.paramDtype, [&](auto w) {
         using W = decltype(w);
-        if (blocks)
-            byWidth(a.cols, [&](auto width) {
-                using S = BackwardShape<decltype(width)::value, T>;
-                if (a.codes.p)
-                    hipLaunchKernelGGL((rmsBackwardKernel<T, W, true, S::kLanes, S::kChunks, S::kBlock>), dim3(blocks),
-                                       dim3(S::kBlock), 0, stream, a);
-                else
-                    hipLaunchKernelGGL((rmsBackwardKernel<T, W, false, S::kLanes, S::kChunks, S::kBlock>),
-                                       dim3(blocks), dim3(S::kBlock), 0, stream, a);
-            });
         hipLaunchKernelGGL((paramSumKernel<W>), dim3((a.cols + kParamCols - 1) / kParamCols),
                            dim3(kParamCols * kParamGroups), 0, stream, a.partials, blocks, a.cols, a.cols,
                            static_cast<W *>(a.dweight), static_cast<W *>(nullptr),
                            a.accumulate & BFO_ACCUMULATE_PARAMS);
     });
+    return hipGetLastError();
 }
 
 }  // namespace bfo

@@ -32,34 +32,34 @@ constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
 // Columns behind the rotated ones that a lane copies at a time.
 constexpr int kCopied = 8;
 
-// What a lane takes at a time: P pairs from pair `first` on, in two 16-byte
-// chunks, or kCopied columns from column `first` on.  A head has at most 129 such
-// items, which fit a workgroup.  kWhole: the last item of a
-// head's pairs, or of its columns, starts so much earlier that it ends with them
-// (what two items share is the same in both, and read before either writes);
-// otherwise, for too few of them, they end inside one.
-template <typename T, bool kHalf, bool kWhole>
+// What a lane takes at a time: two 16-byte chunks of a head, at column `first` of
+// the first half of its rotated columns and at the same of the second one, or
+// kCopied columns from column `first` on.  In halves the two hold the members of
+// the same pairs; interleaved, each holds pairs of its own, and where their number
+// is odd the halves share the middle one.  (Interleaved, two neighbouring chunks a
+// lane leave every store instruction half of each line: 47.2 us, 53.9 nontemporal.)
+// A head has at most 129 such items, which fit a workgroup.  kWhole: the last item
+// of a half, or of the columns, starts so much earlier that it ends with it;
+// otherwise, for too few of them, it ends inside.  What two items share is the same
+// in both, and read before either writes.
+template <typename T, bool kHalf, bool kWhole, bool kStream>
 struct Item {
-    static constexpr int E = 16 / int(sizeof(T)), P = E;
+    static constexpr int E = 16 / int(sizeof(T));
     Chunk<T, E> u, v;
 
     // A chunk at column c of a head, of which `there` columns are there.
     __device__ __forceinline__ static void get(Chunk<T, E> &w, const T *head, int c, int there) {
-        if constexpr (kWhole) w.load(head + c);
-        else w.loadRow(head, c, there);
+        if constexpr (kWhole) w.template load<kStream>(head + c);
+        else w.template loadRow<kStream>(head, c, there);
     }
-    __device__ __forceinline__ static void put(const Chunk<T, E> &w, T *head, int c, int there) {
-        if constexpr (kWhole) w.store(head + c);
-        else w.storeRow(head, c, there);
+    __device__ __forceinline__ static void put(Chunk<T, E> w, T *head, int c, int there) {
+        if constexpr (kStream) w.forget();
+        if constexpr (kWhole) w.template store<kStream>(head + c);
+        else w.template storeRow<kStream>(head, c, there);
     }
-    __device__ __forceinline__ void loadPairs(const T *head, int first, int pairs) {
-        if constexpr (kHalf) {
-            get(u, head, first, pairs);
-            get(v, head + pairs, first, pairs);
-        } else {
-            get(u, head, 2 * first, 2 * pairs);
-            get(v, head + E, 2 * first, 2 * pairs - E);
-        }
+    __device__ __forceinline__ void loadPairs(const T *head, int first, int half, int second) {
+        get(u, head, first, half);
+        get(v, head + second, first, half);
     }
     __device__ __forceinline__ void loadBehind(const T *head, int first, int dim) {
         get(u, head, first, dim);
@@ -70,31 +70,43 @@ struct Item {
         if constexpr (kCopied > E) put(v, head + E, first, dim - E);
     }
     // The pairs turned, stored.
-    __device__ __forceinline__ void turn(const float2 *turns, T *head, int first, int pairs) const {
-        float y[2 * E];
+    __device__ __forceinline__ void turn(const float2 *turns, T *head, int first, int half, int second) const {
+        float y[E], z[E];
+        if constexpr (kHalf) {
 #pragma unroll
-        for (int e = 0; e < P; ++e) {
-            const int i = kHalf ? e : 2 * e, j = kHalf ? E + e : 2 * e + 1;
-            const float a = i < E ? u[i] : v[i - E], b = j < E ? u[j] : v[j - E];
-            const float2 t = turns[first + e];
-            y[i] = fmaf(a, t.x, -(b * t.y));
-            y[j] = fmaf(a, t.y, b * t.x);
+            for (int e = 0; e < E; ++e) turnPair(u[e], v[e], turns[first + e], y[e], z[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                turnPair(u[e], u[e + 1], turns[(first + e) / 2], y[e], y[e + 1]);
+                turnPair(v[e], v[e + 1], turns[(second + first + e) / 2], z[e], z[e + 1]);
+            }
         }
-        const int c = kHalf ? first : 2 * first, there = kHalf ? pairs : 2 * pairs;
-        put(Chunk<T, E>(&y[0]), head, c, there);
-        put(Chunk<T, E>(&y[E]), kHalf ? head + pairs : head + E, c, kHalf ? there : there - E);
+        put(Chunk<T, E>(y), head, first, half);
+        put(Chunk<T, E>(z), head + second, first, half);
+    }
+    __device__ __forceinline__ static void turnPair(float a, float b, float2 t, float &x, float &y) {
+        x = fmaf(a, t.x, -(b * t.y));
+        y = fmaf(a, t.y, b * t.x);
     }
 };
+
+// The columns of each half (even where pairs lie side by side).
+template <bool kHalf>
+__host__ __device__ uint32_t halfColumns(uint32_t rotated) {
+    return kHalf ? rotated / 2 : (rotated / 2 + 1) / 2 * 2;
+}
 
 // Sines and cosines of a workgroup at most: 16 KB of LDS, as four workgroups fill a CU.
 constexpr uint32_t kTurns = 2048;
 
 // kBehind: columns behind the rotated ones are copied.
-template <typename T, bool kHalf, bool kWhole, bool kBehind>
+template <typename T, bool kHalf, bool kWhole, bool kBehind, bool kStream>
 __global__ __launch_bounds__(kBlock) void rotaryKernel(Rotary a) {
-    constexpr uint32_t P = Item<T, kHalf, kWhole>::P;
+    constexpr uint32_t E = 16 / sizeof(T);
     extern __shared__ float2 table[];  // every token's cosines and sines
-    const uint32_t pairs = a.rotated / 2, room = (pairs + 7) / 8 * 8, turning = (pairs + P - 1) / P;
+    const uint32_t pairs = a.rotated / 2, room = (pairs + 7) / 8 * 8;
+    const uint32_t half = halfColumns<kHalf>(a.rotated), second = a.rotated - half, turning = (half + E - 1) / E;
     // What the angle of a workgroup's pair i is made of, and its cosine and sine.
     struct Angle {
         uint32_t token, pair;
@@ -128,18 +140,18 @@ __global__ __launch_bounds__(kBlock) void rotaryKernel(Rotary a) {
         const uint32_t token = a.headsAtOnce.divide(row), head = row - token * a.headsAtOnce.by;
         const bool live = token < tokens && firstHead + head < a.heads;
         const T *from = x + token * a.xToken + head * a.xHead;
-        Item<T, kHalf, kWhole> item;
-        // The item's first pair, or its first column behind them.
+        Item<T, kHalf, kWhole, kStream> item;
+        // The item's first column, in a half or behind them.
         const bool turns = !kBehind || k < turning;
-        int at = turns ? int(k * P) : int(a.rotated) + int(k - turning) * kCopied;
-        if constexpr (kWhole) at = min(at, turns ? int(pairs - P) : int(a.headDim) - kCopied);
-        if (live && turns) item.loadPairs(from, at, int(pairs));
+        int at = turns ? int(k * E) : int(a.rotated) + int(k - turning) * kCopied;
+        if constexpr (kWhole) at = min(at, turns ? int(half - E) : int(a.headDim) - kCopied);
+        if (live && turns) item.loadPairs(from, at, int(half), int(second));
         else if (kBehind && live) item.loadBehind(from, at, int(a.headDim));
         if (threadIdx.x < angles) put(firstToken, angle);
         for (uint32_t i = threadIdx.x + kBlock; i < angles; i += kBlock) put(firstToken, load(firstToken, i));
         __syncthreads();
         T *to = out + token * a.outToken + head * a.outHead;
-        if (live && turns) item.turn(table + token * room, to, at, int(pairs));
+        if (live && turns) item.turn(table + token * room, to, at, int(half), int(second));
         else if (kBehind && live) item.storeBehind(to, at, int(a.headDim));
         if (unit + gridDim.x < a.units) __syncthreads();
     }
@@ -147,8 +159,8 @@ __global__ __launch_bounds__(kBlock) void rotaryKernel(Rotary a) {
 
 template <typename T, bool kHalf>
 void launch(Rotary a, hipStream_t stream) {
-    constexpr uint32_t P = Item<T, kHalf, true>::P;
-    const uint32_t pairs = a.rotated / 2, turning = (pairs + P - 1) / P;
+    constexpr uint32_t E = 16 / sizeof(T);
+    const uint32_t pairs = a.rotated / 2, half = halfColumns<kHalf>(a.rotated), turning = (half + E - 1) / E;
     const uint32_t per = turning + (a.x == a.out ? 0 : (a.headDim - a.rotated + kCopied - 1) / kCopied);
     // A workgroup's tokens and heads: as many as its lanes have items for, the heads of a
     // token in blocks of like size.
@@ -166,13 +178,17 @@ void launch(Rotary a, hipStream_t stream) {
     a.units = uint32_t((a.tokens + tokens - 1) / tokens * blocks);
     const uint32_t lds = tokens * ((pairs + 7) / 8 * 8) * sizeof(float2);
     const dim3 grid(a.units < (1u << 22) ? a.units : 1u << 22);
-    auto with = [&](auto whole, auto behind) {
-        hipLaunchKernelGGL((rotaryKernel<T, kHalf, decltype(whole)::value, decltype(behind)::value>), grid, dim3(kBlock),
-                           lds, stream, a);
+    auto with = [&](auto whole, auto behind, auto streamed) {
+        hipLaunchKernelGGL((rotaryKernel<T, kHalf, decltype(whole)::value, decltype(behind)::value,
+                                         decltype(streamed)::value>),
+                           grid, dim3(kBlock), lds, stream, a);
     };
-    if (pairs >= P && per == turning) with(std::true_type{}, std::false_type{});
-    else if (pairs >= P && a.headDim - a.rotated >= uint32_t(kCopied)) with(std::true_type{}, std::true_type{});
-    else with(std::false_type{}, std::true_type{});
+    const bool streamed = streams(2 * sizeof(T) * a.tokens * a.heads * a.headDim);
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    if (half < E || (per > turning && a.headDim - a.rotated < uint32_t(kCopied))) with(no, yes, no);
+    else if (per > turning) streamed ? with(yes, yes, yes) : with(yes, yes, no);
+    else streamed ? with(yes, no, yes) : with(yes, no, no);
 }
 
 }  // namespace
