@@ -688,6 +688,11 @@ def _sized(n, most):
     return n if 0 <= n <= most else most
 
 
+def _device(index):
+    """The device of that index, as in get_device(), which asks for less than .device."""
+    return torch.device("cuda", index) if index >= 0 else torch.device("cpu")
+
+
 def _matrix(t, name):
     """(device pointer, row stride, rows, columns) of a bf16 or fp32 matrix on a GPU."""
     if not isinstance(t, torch.Tensor):
@@ -711,8 +716,8 @@ def _matrix_like(t, name, dtype, dev, rows, cols):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {_device(dev)}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
     stride, step = t.stride()
@@ -729,8 +734,8 @@ def _vector(t, dtype, count, name, dev):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {_device(dev)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if t.numel() != count:
@@ -749,7 +754,7 @@ def _workspace_ptr(workspace, need, dev, maker):
         if need:
             raise ValueError(f"workspace must be {maker}(...)")
         return None
-    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous() or \
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be {maker}(...) for these sizes")
     return workspace.data_ptr()
@@ -761,15 +766,17 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _launch(name, dev, *args):
-    """Call entry point `name` with `dev` current, on dev's current stream."""
+    """Call entry point `name` with device `dev` current, on its current stream."""
     fn = getattr(_L, name)
-    index = dev.index
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, _current_raw_stream(index))
+    if _current_device() == dev:
+        rc = fn(*args, _current_raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _current_raw_stream(index))
+            rc = fn(*args, _current_raw_stream(dev))
     if rc != OK:
         raise BfoError(name, rc)
 
@@ -792,7 +799,7 @@ def layernorm_forward(x, weight, bias, out, mean=None, rstd=None, eps=1e-5):
     """out = (x - mean) * rstd * weight + bias per row of x (bias may be None).
     mean, rstd: float32 tensors of x's rows for the backward pass, or None."""
     xp, xs, rows, cols = _matrix(x, "x")
-    dev = x.device
+    dev = x.get_device()
     op, os_ = _matrix_like(out, "out", x.dtype, dev, rows, cols)
     pt = _param_type(weight)
     _launch("layernorm_forward", dev, xp, xs, _vector(weight, pt, cols, "weight", dev),
@@ -807,7 +814,7 @@ def layernorm_backward(dout, x, weight, mean, rstd, dx, dweight, dbias=None, wor
     wanted).  accumulate_*: add to what they hold.  workspace:
     new_layernorm_workspace(rows, cols, device)."""
     xp, xs, rows, cols = _matrix(x, "x")
-    dev = x.device
+    dev = x.get_device()
     gp, gs = _matrix_like(dout, "dout", x.dtype, dev, rows, cols)
     dp, ds = _matrix_like(dx, "dx", x.dtype, dev, rows, cols)
     pt = _param_type(weight)
@@ -862,7 +869,7 @@ def token_logprobs_forward(logits, targets=None, logprob=None, stats=None, entro
     entropy, and the top_index.shape[1] best tokens.  Every output but the ones
     wanted may be None."""
     lp, ls, rows, cols = _matrix(logits, "logits")
-    dev = logits.device
+    dev = logits.get_device()
     v = _vocab(vocab, cols)
     top = 0
     if top_index is not None:
@@ -883,7 +890,7 @@ def token_logprobs_backward(logits, targets, stats, dlogprob, dlogits, entropy=N
     (the logits' shape; may be the logits), from the forward pass's stats and
     entropy; columns from vocab on get 0.  targets and dlogprob may both be None."""
     lp, ls, rows, cols = _matrix(logits, "logits")
-    dev = logits.device
+    dev = logits.get_device()
     dp, ds = _matrix_like(dlogits, "dlogits", logits.dtype, dev, rows, cols)
     _launch("token_logprobs_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols if cols < _U32 else _U32,
             _DTYPE_CODES[logits.dtype], scale, _vector(targets, torch.int32, rows, "targets", dev),
@@ -908,7 +915,7 @@ def distill_forward(logits, teacher_index, teacher_logits, kl, stats=None, targe
     as in token_logprobs_forward.  teacher_logits are scaled here too, so they
     are unscaled scores, or top_logprob of a pass at scale 1."""
     lp, ls, rows, cols = _matrix(logits, "logits")
-    dev = logits.device
+    dev = logits.get_device()
     v = _vocab(vocab, cols)
     ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
     ws = _workspace_ptr(workspace, logits_workspace_bytes(rows, v, 0) if rows <= SPLIT_ROWS else 0, dev,
@@ -924,7 +931,7 @@ def distill_backward(logits, teacher_index, teacher_logits, stats, dkl, dlogits,
     """Gradient of sum(dkl * kl + dlogprob * logprob) into dlogits (the logits'
     shape; may be the logits); columns from vocab on get 0."""
     lp, ls, rows, cols = _matrix(logits, "logits")
-    dev = logits.device
+    dev = logits.get_device()
     dp, ds = _matrix_like(dlogits, "dlogits", logits.dtype, dev, rows, cols)
     ti, tl, count = _teacher(teacher_index, teacher_logits, rows, dev)
     _launch("distill_backward", dev, lp, ls, rows, _vocab(vocab, cols), cols if cols < _U32 else _U32,
@@ -955,17 +962,19 @@ def _codes(codes, scales, name, dev, rows, cols, whole_row=False):
     group) of codes of a rows x cols matrix, or of none."""
     if codes is None and scales is None:
         return _NO_CODES
-    if not isinstance(codes, torch.Tensor) or codes.dtype not in _CODE_TYPES:
+    ct = _CODE_TYPES.get(codes.dtype) if isinstance(codes, torch.Tensor) else None
+    if ct is None:
         raise TypeError(f"{name} must be a torch.int8 or torch.float8_e4m3fn tensor")
     p, stride = _matrix_like(codes, name, codes.dtype, dev, rows, cols)
-    groups = (cols + GROUP - 1) // GROUP
-    per_row = whole_row and isinstance(scales, torch.Tensor) and scales.dim() == 2 and scales.shape[1] == 1
-    if per_row:
-        groups = 1
-    sp = _vector(scales, torch.float32, rows * groups, f"the scales of {name}", dev)
-    if sp is None or scales.shape != (rows, groups):
-        raise ValueError(f"the scales of {name} must be a {(rows, groups)} tensor")
-    return p, stride, sp, _CODE_TYPES[codes.dtype], 0 if per_row else GROUP
+    groups = scales.shape[1] if isinstance(scales, torch.Tensor) and scales.dim() == 2 else 0
+    if groups == 1 and whole_row:
+        group = 0
+    elif groups and groups == (cols + GROUP - 1) // GROUP:
+        group = GROUP
+    else:
+        raise ValueError(f"the scales of {name} must be a {(rows, (cols + GROUP - 1) // GROUP)} tensor" +
+                         (f" or a {(rows, 1)} one" if whole_row else ""))
+    return p, stride, _vector(scales, torch.float32, rows * groups, "scales", dev), ct, group
 
 
 def new_codes(rows, cols, device, dtype=torch.int8, per_row=False):
@@ -985,7 +994,7 @@ def rmsnorm_forward(x, weight, out=None, residual=None, total=None, rstd=None, c
     total * rstd (CODES_OF_NORMALISED) in 8 bits.  Every output but the ones
     wanted may be None; total may be x or residual."""
     xp, xs, rows, cols = _matrix(x, "x")
-    dev, dt = x.device, x.dtype
+    dev, dt = x.get_device(), x.dtype
     pt = _param_type(weight)
     cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
     _launch("rmsnorm_forward", dev, xp, xs, *_optional_matrix(residual, "residual", dt, dev, rows, cols),
@@ -1016,7 +1025,7 @@ def rmsnorm_backward(dout, x, weight, rstd, dx, dweight, codes=None, scales=None
     None).  out, unless None, gets the forward pass's out again.  accumulate_*:
     add to what they hold.  workspace: new_rmsnorm_workspace(rows, cols, device)."""
     gp, gs, rows, cols = _matrix(dout, "dout")
-    dev, dt = dout.device, dout.dtype
+    dev, dt = dout.get_device(), dout.dtype
     if (x is None) == (codes is None):
         raise ValueError("either x or codes must be given")
     pt = _param_type(weight)
@@ -1042,7 +1051,7 @@ def activation_forward(gate, up, out, kind=SILU, gate_codes=None, gate_scales=No
     and scales keep both inputs in 8 bits for the backward pass.  out may be
     gate or up."""
     gp, gs, rows, cols = _matrix(gate, "gate")
-    dev, dt = gate.device, gate.dtype
+    dev, dt = gate.get_device(), gate.dtype
     gc = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
     uc = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
     _launch("activation_forward", dev, gp, gs, *_optional_matrix(up, "up", dt, dev, rows, cols),
@@ -1056,7 +1065,7 @@ def activation_backward(dout, gate, up, dgate, dup, kind=SILU, gate_codes=None, 
     gate and up or, where those are None, from their codes; out, unless None,
     gets act(gate) * up again.  Outputs may be dout, gate or up."""
     op, os_, rows, cols = _matrix(dout, "dout")
-    dev, dt = dout.device, dout.dtype
+    dev, dt = dout.get_device(), dout.dtype
     gc = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
     uc = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
     _launch("activation_backward", dev, op, os_, *_optional_matrix(gate, "gate", dt, dev, rows, cols),
@@ -1069,15 +1078,17 @@ def activation_backward(dout, gate, up, dgate, dup, kind=SILU, gate_codes=None, 
 def activation_pack(x, codes, scales):
     """x in 8 bits: codes, and a scale for every GROUP columns."""
     xp, xs, rows, cols = _matrix(x, "x")
-    _launch("activation_pack", x.device, xp, xs, *_codes(codes, scales, "codes", x.device, rows, cols)[:4], rows,
+    dev = x.get_device()
+    _launch("activation_pack", dev, xp, xs, *_codes(codes, scales, "codes", dev, rows, cols)[:4], rows,
             cols if cols < _U32 else _U32, _DTYPE_CODES[x.dtype])
 
 
 def activation_unpack(codes, scales, out):
     """The values that codes stand for, rounded to out's type."""
     op, os_, rows, cols = _matrix(out, "out")
-    cp, cs, sp, ct, group = _codes(codes, scales, "codes", out.device, rows, cols, whole_row=True)
-    _launch("activation_unpack", out.device, cp, cs, sp, ct, group, op, os_, rows, cols if cols < _U32 else _U32,
+    dev = out.get_device()
+    cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
+    _launch("activation_unpack", dev, cp, cs, sp, ct, group, op, os_, rows, cols if cols < _U32 else _U32,
             _DTYPE_CODES[out.dtype])
 
 
@@ -1116,11 +1127,11 @@ def rotary_apply(x, frequencies, out, positions=None, period=0, layout=ROTARY_HA
     period if that is not 0).  out may be x."""
     xp, xt, xh = _heads(x, "x")
     op, ot, oh = _heads(out, "out")
-    dev = x.device
+    dev = x.get_device()
     if out.dtype != x.dtype:
         raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
-    if out.device != dev:
-        raise ValueError(f"out is on {out.device}, expected {dev}")
+    if out.get_device() != dev:
+        raise ValueError(f"out is on {out.device}, expected {_device(dev)}")
     if out.shape != x.shape:
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
     if not isinstance(frequencies, torch.Tensor):

@@ -403,8 +403,13 @@ struct BackwardShape {
     static constexpr int kRows = kBlock / kLanes;
 };
 
-// Up to here one launch for all gradients takes no longer than rows and partials.
-uint64_t fewRows(uint32_t cols) { return cols <= 2048 ? 2048 : cols <= 4096 ? 1024 : 512; }
+// Up to here one launch for all gradients takes no longer than rows and partials, as
+// called from Python on inputs that no cache holds, from bf16 codes: 2,048 rows of
+// 2,048 columns 11.5 us against 13.0 (4,096 rows 19.1 and 13.1), 1,024 of 4,096 10.6
+// and 13.1 (2,048: 16.0 and 13.5), 512 of 8,192 10.6 and 13.6 (1,024: 16.2 and 15.8), 256
+// of 16,384 12.4 and 14.2 (512: 18.3 and 16.9); fp32 rows 2,048 of 1,600 12.0 and 12.8,
+// of 2,048 14.0 and 13.0.  A column workgroup walks all rows by itself.
+uint64_t fewRows(uint32_t cols) { return cols <= 2048 ? 2048 : cols <= 4096 ? 1024 : cols <= 8192 ? 512 : 256; }
 template <int kCols, typename F>
 void bySlab(uint64_t rows, F f) {
     if constexpr (kCols > 4096) f(std::integral_constant<int, 32>{});

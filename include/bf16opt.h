@@ -685,7 +685,9 @@ int rmsnorm_forward(const void *x, uint64_t x_stride, const void *residual, uint
                     uint32_t group, uint64_t rows, uint32_t cols, float eps, int dtype, int param_dtype,
                     void *stream);
 
-/* *bytes = the workspace rmsnorm_backward needs.  Host only. */
+/* *bytes = the workspace rmsnorm_backward needs; 0 for few rows (up to 2,048 of
+ * at most 2,048 columns, 1,024 of at most 4,096, 512 of at most 8,192, 256 of
+ * more), and workspace may then be NULL.  Host only. */
 int bfo_rmsnorm_workspace_bytes(uint64_t rows, uint32_t cols, uint64_t *bytes);
 
 /* Gradients of rmsnorm_forward, from its rstd and either the row that it

@@ -280,11 +280,11 @@ def test_binding_names_what_is_wrong(bfo):
         bfo.new_codes(4, 8, "cpu", torch.uint8)
     codes, scales = bfo.new_codes(4, 300, "cpu")
     assert codes.shape == (4, 300) and scales.shape == (4, 3) and bfo.new_codes(4, 300, "cpu", per_row=True)[1].shape == (4, 1)
-    dev = torch.device("cpu")
+    dev = -1                      # of the CPU
     assert bfo._codes(codes, scales, "codes", dev, 4, 300)[3:] == (bfo.I8, bfo.GROUP)
     assert bfo._codes(codes, scales[:, :1].contiguous(), "codes", dev, 4, 300, whole_row=True)[4] == 0
     for bad, err, match in (((codes, None), ValueError, "scales of codes"), ((None, scales), TypeError, "codes must be"),
-                            ((codes, scales.double()), TypeError, "scales of codes"),
+                            ((codes, scales.double()), TypeError, "scales must be torch.float32"),
                             ((codes, scales[:, :2].contiguous()), ValueError, "scales of codes"),
                             ((codes, scales[:, :1].contiguous()), ValueError, "scales of codes"),
                             ((codes.float(), scales), TypeError, "codes must be"),
