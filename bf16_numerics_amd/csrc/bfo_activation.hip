@@ -48,7 +48,7 @@ __device__ __forceinline__ Place place(const GroupGrid &g, uint32_t index) {
 }
 
 // v's codes and their group's scale.
-template <int kType, int E>
+template <int kType, Loads kLoads, bool kNontemporal, int E>
 __device__ __forceinline__ void writeGroup(const CodeMatrix &m, const Place &p, const GroupGrid &g, const float (&v)[E]) {
     constexpr int kLanes = kGroup / E;
     uint32_t amax = 0;
@@ -57,20 +57,27 @@ __device__ __forceinline__ void writeGroup(const CodeMatrix &m, const Place &p, 
     const CodeScale s = codeScale<kType>(laneMax<kLanes>(amax));
     uint32_t w[E / 4];
     encode<kType, E>(v, s.inverse, w);
-    storeCodes<E>(static_cast<uint8_t *>(m.p) + p.row * m.stride, p.c, int(g.cols), w);
+    storeCodes<kLoads, kNontemporal, E>(static_cast<uint8_t *>(m.p) + p.row * m.stride, p.c, int(g.cols), w);
     if (threadIdx.x % kLanes == 0) m.scales[p.row * g.perRow.by + p.group] = s.scale;
 }
 
-template <typename T, int kKind, bool kGated, int kType, bool kStream>
+template <typename T, int kKind, bool kGated, int kType, Loads kLoads>
 __global__ __launch_bounds__(kBlock) void actForwardKernel(ActivationForward a) {
     constexpr int E = 16 / int(sizeof(T));
     constexpr uint32_t kAt = kBlock / (kGroup / E);  // groups of a workgroup
+    // Of large calls, 8192 x 11008 bf16: two matrices of codes 121 us with plain stores,
+    // 115 with nontemporal ones, but one 69.6 and 72.1.
+    constexpr bool kStreamCodes = kLoads == kEvenStream && kGated;
     const int C = int(a.grid.cols);
     for (uint32_t i = blockIdx.x * kAt + threadIdx.x / (kGroup / E); i < a.grid.count; i += gridDim.x * kAt) {
         const Place p = place<E>(a.grid, i);
         Chunk<T, E> gate, up;
-        gate.template loadRow<kStream>(static_cast<const T *>(a.gate.p) + p.row * a.gate.stride, p.c, C);
-        if constexpr (kGated) up.template loadRow<kStream>(static_cast<const T *>(a.up.p) + p.row * a.up.stride, p.c, C);
+        loadChunk<kLoads>(gate, static_cast<const T *>(a.gate.p) + p.row * a.gate.stride, p.c, C, true);
+        if constexpr (kGated) loadChunk<kLoads>(up, static_cast<const T *>(a.up.p) + p.row * a.up.stride, p.c, C, true);
+        if (kLoads != kAny && p.c >= C) {
+            gate.zero();
+            if constexpr (kGated) up.zero();
+        }
         float g[E], u[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -78,8 +85,8 @@ __global__ __launch_bounds__(kBlock) void actForwardKernel(ActivationForward a) 
             u[e] = kGated ? up[e] : 1.0f;
         }
         if constexpr (kType != kNoCodes) {
-            writeGroup<kType, E>(a.gateCodes, p, a.grid, g);
-            if constexpr (kGated) writeGroup<kType, E>(a.upCodes, p, a.grid, u);
+            writeGroup<kType, kLoads, kStreamCodes, E>(a.gateCodes, p, a.grid, g);
+            if constexpr (kGated) writeGroup<kType, kLoads, kStreamCodes, E>(a.upCodes, p, a.grid, u);
         }
         if constexpr (kKind != kIdentity) {
             float y[E];
@@ -88,29 +95,29 @@ __global__ __launch_bounds__(kBlock) void actForwardKernel(ActivationForward a) 
                 const Activation<kKind> f(g[e]);
                 y[e] = kGated ? f.act * u[e] : f.act;
             }
-            storeRow<kStream>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, 0, C, y);
+            storeChunk<kLoads>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, C, y);
         }
     }
 }
 
 // A kept input: the matrix itself or its codes.
-template <typename T, int E, int kType, bool kStream>
+template <typename T, int E, int kType, Loads kLoads>
 __device__ __forceinline__ void readKept(const ConstMatrix &m, const ConstCodes &codes, const Place &p,
                                          const GroupGrid &g, float (&v)[E]) {
     const int C = int(g.cols);
     if constexpr (kType == kNoCodes) {
         Chunk<T, E> raw;
-        raw.template loadRow<kStream>(static_cast<const T *>(m.p) + p.row * m.stride, p.c, C);
+        loadChunk<kLoads>(raw, static_cast<const T *>(m.p) + p.row * m.stride, p.c, C, true);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = raw[e];
     } else {
         uint32_t w[E / 4];
-        loadCodes<E>(static_cast<const uint8_t *>(codes.p) + p.row * codes.stride, p.c, C, true, w);
+        loadCodeChunk<kLoads, E>(static_cast<const uint8_t *>(codes.p) + p.row * codes.stride, p.c, C, true, w);
         decode<kType, E>(w, codes.scales[codes.wholeRow ? p.row : p.row * g.perRow.by + p.group], v);
     }
 }
 
-template <typename T, int kKind, bool kGated, int kType, bool kStream>
+template <typename T, int kKind, bool kGated, int kType, Loads kLoads>
 __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a) {
     constexpr int E = 16 / int(sizeof(T));
     constexpr uint32_t kAt = kBlock / (kGroup / E);
@@ -118,14 +125,14 @@ __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a
     for (uint32_t i = blockIdx.x * kAt + threadIdx.x / (kGroup / E); i < a.grid.count; i += gridDim.x * kAt) {
         const Place p = place<E>(a.grid, i);
         float g[E], u[E], y[E];
-        readKept<T, E, kType, kStream>(a.gate, a.gateCodes, p, a.grid, g);
+        readKept<T, E, kType, kLoads>(a.gate, a.gateCodes, p, a.grid, g);
         if constexpr (kKind == kIdentity) {
-            storeRow<kStream>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, 0, C, g);
+            storeChunk<kLoads>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, C, g);
             continue;
         } else {
-            if constexpr (kGated) readKept<T, E, kType, kStream>(a.up, a.upCodes, p, a.grid, u);
+            if constexpr (kGated) readKept<T, E, kType, kLoads>(a.up, a.upCodes, p, a.grid, u);
             Chunk<T, E> d;
-            d.template loadRow<kStream>(static_cast<const T *>(a.dout.p) + p.row * a.dout.stride, p.c, C);
+            loadChunk<kLoads>(d, static_cast<const T *>(a.dout.p) + p.row * a.dout.stride, p.c, C, true);
             float act[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -133,16 +140,16 @@ __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a
                 act[e] = f.act;
                 y[e] = (kGated ? d[e] * u[e] : d[e]) * f.slope;
             }
-            storeRow<kStream>(static_cast<T *>(a.dgate.p) + p.row * a.dgate.stride, p.c, 0, C, y);
+            storeChunk<kLoads>(static_cast<T *>(a.dgate.p) + p.row * a.dgate.stride, p.c, C, y);
             if constexpr (kGated) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] = d[e] * act[e];
-                storeRow<kStream>(static_cast<T *>(a.dup.p) + p.row * a.dup.stride, p.c, 0, C, y);
+                storeChunk<kLoads>(static_cast<T *>(a.dup.p) + p.row * a.dup.stride, p.c, C, y);
             }
             if (a.out.p) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] = kGated ? act[e] * u[e] : act[e];
-                storeRow<kStream>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, 0, C, y);
+                storeChunk<kLoads>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, C, y);
             }
         }
     }
@@ -151,9 +158,9 @@ __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a
 template <int kValue>
 using Const = std::integral_constant<int, kValue>;
 
-// f(type, kind, gated, code type, streamed) with the call's values as constants.
+// f(type, kind, gated, code type, way to load) with the call's values as constants.
 template <typename F>
-hipError_t byKind(int dtype, int kind, bool gated, int codeType, bool streamed, F f) {
+hipError_t byKind(int dtype, int kind, bool gated, int codeType, uint32_t cols, uint64_t bytes, F f) {
     auto coded = [&](auto t, auto k, auto g, auto s) {
         if (codeType == BFO_I8) f(t, k, g, Const<BFO_I8>{}, s);
         else if (codeType == BFO_E4M3) f(t, k, g, Const<BFO_E4M3>{}, s);
@@ -168,9 +175,9 @@ hipError_t byKind(int dtype, int kind, bool gated, int codeType, bool streamed, 
         else if (kind == BFO_SILU) gates(t, Const<BFO_SILU>{}, s);
         else gates(t, Const<BFO_GELU>{}, s);
     };
-    auto streams = [&](auto t) { streamed ? kinds(t, std::true_type{}) : kinds(t, std::false_type{}); };
-    if (dtype == BFO_BF16) streams(bf16_t(0));
-    else streams(float(0));
+    auto types = [&](auto t) { byLoads<decltype(t)>(cols, bytes, [&](auto loads) { kinds(t, loads); }); };
+    if (dtype == BFO_BF16) types(bf16_t(0));
+    else types(float(0));
     return hipGetLastError();
 }
 
@@ -183,7 +190,7 @@ dim3 workgroups(const GroupGrid &g) {
 }
 
 // Bytes of `matrices` matrices and `codes` matrices in codes.
-uint64_t bytes(const GroupGrid &g, int dtype, int matrices, int codes) {
+uint64_t moved(const GroupGrid &g, int dtype, int matrices, int codes) {
     return uint64_t(g.count / g.perRow.by) * g.cols * (matrices * (dtype == BFO_BF16 ? 2 : 4) + codes);
 }
 
@@ -192,12 +199,12 @@ uint64_t bytes(const GroupGrid &g, int dtype, int matrices, int codes) {
 hipError_t launchActivationForward(const ActivationForward &a, hipStream_t stream) {
     if (!a.grid.count) return hipSuccess;
     const int inputs = a.up.p ? 2 : 1;
-    const bool streamed = streams(bytes(a.grid, a.dtype, inputs + 1, a.codeType == kNoCodes ? 0 : inputs));
-    return byKind(a.dtype, a.kind, a.up.p != nullptr, a.codeType, streamed,
-                  [&](auto t, auto kind, auto gated, auto type, auto nt) {
+    const uint64_t bytes = moved(a.grid, a.dtype, inputs + 1, a.codeType == kNoCodes ? 0 : inputs);
+    return byKind(a.dtype, a.kind, a.up.p != nullptr, a.codeType, a.grid.cols, bytes,
+                  [&](auto t, auto kind, auto gated, auto type, auto loads) {
                       using T = decltype(t);
                       hipLaunchKernelGGL((actForwardKernel<T, decltype(kind)::value, decltype(gated)::value,
-                                                           decltype(type)::value, decltype(nt)::value>),
+                                                           decltype(type)::value, decltype(loads)::value>),
                                          workgroups<T>(a.grid), dim3(kBlock), 0, stream, a);
                   });
 }
@@ -205,12 +212,12 @@ hipError_t launchActivationForward(const ActivationForward &a, hipStream_t strea
 hipError_t launchActivationBackward(const ActivationBackward &a, hipStream_t stream) {
     if (!a.grid.count) return hipSuccess;
     const int inputs = a.dup.p ? 2 : 1, coded = a.codeType == kNoCodes ? 0 : inputs;
-    const bool streamed = streams(bytes(a.grid, a.dtype, 1 + inputs - coded + inputs + (a.out.p ? 1 : 0), coded));
-    return byKind(a.dtype, a.kind, a.dup.p != nullptr, a.codeType, streamed,
-                  [&](auto t, auto kind, auto gated, auto type, auto nt) {
+    const uint64_t bytes = moved(a.grid, a.dtype, 1 + inputs - coded + inputs + (a.out.p ? 1 : 0), coded);
+    return byKind(a.dtype, a.kind, a.dup.p != nullptr, a.codeType, a.grid.cols, bytes,
+                  [&](auto t, auto kind, auto gated, auto type, auto loads) {
                       using T = decltype(t);
                       hipLaunchKernelGGL((actBackwardKernel<T, decltype(kind)::value, decltype(gated)::value,
-                                                            decltype(type)::value, decltype(nt)::value>),
+                                                            decltype(type)::value, decltype(loads)::value>),
                                          workgroups<T>(a.grid), dim3(kBlock), 0, stream, a);
                   });
 }

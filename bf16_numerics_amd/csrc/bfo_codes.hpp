@@ -1,4 +1,7 @@
-// bfo_codes.hpp -- 8-bit codes with scales: values of a row in groups of
+// bfo_codes.hpp -- what the operators between a block's matrix products share:
+// ways to load and store a row's chunks, and 8-bit codes with scales.
+//
+// Codes: values of a row in groups of
 // kGroup columns (or the whole row), each code an 8-bit integer or an e4m3
 // float, each value code * scale.
 //
@@ -14,11 +17,48 @@
 // finite and all its values read back as NaN.
 #pragma once
 
+#include <type_traits>
+
 #include "bfo_device.hpp"
 #include "bfo_ops.hpp"
 
 namespace bfo {
 namespace {
+
+// How a row's chunks are loaded.  kEven, for widths of whole chunks: without a
+// branch, from the row's last chunk where there is none, whose values the caller
+// drops (an earlier row's loads need not be waited for at the branch's end).
+enum Loads { kAny, kEven, kEvenStream };
+template <Loads kLoads, typename T, int E>
+__device__ __forceinline__ void loadChunk(Chunk<T, E> &w, const T *row, int c, int C, bool live) {
+    if constexpr (kLoads == kAny) w.loadRow(row, c, C, live);
+    else w.template load<kLoads == kEvenStream>(row + min(c, C - E));
+}
+template <Loads kLoads, typename T, int E>
+__device__ __forceinline__ void storeChunk(Chunk<T, E> w, T *row, int c, int C) {
+    if constexpr (kLoads == kAny) {
+        w.storeRow(row, c, C);
+    } else if (c < C) {
+        // The compiler stores values that it has just rounded to bf16 without the hint.
+        if constexpr (kLoads == kEvenStream) w.forget();
+        w.template store<kLoads == kEvenStream>(row + c);
+    }
+}
+template <Loads kLoads, typename T, int E>
+__device__ __forceinline__ void storeChunk(T *row, int c, int C, const float (&v)[E]) {
+    if constexpr (kLoads == kAny) storeRow(row, c, 0, C, v);
+    else storeChunk<kLoads>(Chunk<T, E>(v), row, c, C);
+}
+template <Loads kValue>
+using Constant = std::integral_constant<Loads, kValue>;
+
+// f with the way to load rows of a call that moves `bytes`.
+template <typename T, typename F>
+void byLoads(uint32_t cols, uint64_t bytes, F f) {
+    if (cols % (16 / sizeof(T))) f(Constant<kAny>{});
+    else if (streams(bytes)) f(Constant<kEvenStream>{});
+    else f(Constant<kEven>{});
+}
 
 constexpr int kGroup = int(BFO_GROUP);
 
@@ -122,12 +162,26 @@ __device__ __forceinline__ void loadCodes(const uint8_t *base, int c, int cols, 
             if (c + i < cols) w[i / 4] |= uint32_t(base[c + i]) << (8 * (i % 4));
     }
 }
-template <int N>
+// The same by the way to load rows.
+template <Loads kLoads, int N>
+__device__ __forceinline__ void loadCodeChunk(const uint8_t *row, int c, int C, bool live, uint32_t (&w)[N / 4]) {
+    if constexpr (kLoads == kAny) loadCodes<N>(row, c, C, live, w);
+    else getCodes<N>(row + min(c, C - N), w);
+}
+template <Loads kLoads, bool kNontemporal, int N>
 __device__ __forceinline__ void storeCodes(uint8_t *base, int c, int cols, const uint32_t (&w)[N / 4]) {
-    if (c + N <= cols) {
-        if constexpr (N == 8) *reinterpret_cast<Bytes8 *>(base + c) = Bytes8{w[0], w[1]};
-        else *reinterpret_cast<Bytes4 *>(base + c) = w[0];
-    } else if (c < cols) {
+    if (kLoads == kAny ? c + N <= cols : c < cols) {
+        if constexpr (N == 8) {
+            const Bytes8 q{w[0], w[1]};
+            Bytes8 *p = reinterpret_cast<Bytes8 *>(base + c);
+            if constexpr (kNontemporal) __builtin_nontemporal_store(q, p);
+            else *p = q;
+        } else {
+            Bytes4 *p = reinterpret_cast<Bytes4 *>(base + c);
+            if constexpr (kNontemporal) __builtin_nontemporal_store(Bytes4(w[0]), p);
+            else *p = w[0];
+        }
+    } else if (kLoads == kAny && c < cols) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (c + i < cols) base[c + i] = uint8_t(w[i / 4] >> (8 * (i % 4)));

@@ -28,7 +28,7 @@ __device__ __forceinline__ uint32_t rowMax(uint32_t v, uint32_t (&red)[kBlock / 
 }
 
 // Columns of a row in codes, with one scale for each group (or `whole` row).
-template <int kType, int kLanes, int kChunks, int kBlock, int E>
+template <int kType, Loads kLoads, int kLanes, int kChunks, int kBlock, int E>
 __device__ __forceinline__ void writeCodes(const RmsNormForward &a, uint64_t row, const float (&v)[kChunks][E],
                                            uint32_t (&red)[kBlock / 64]) {
     constexpr int kWidth = kLanes * E, kGroupLanes = kGroup / E;
@@ -47,7 +47,7 @@ __device__ __forceinline__ void writeCodes(const RmsNormForward &a, uint64_t row
         for (int k = 0; k < kChunks; ++k) {
             uint32_t w[E / 4];
             encode<kType, E>(v[k], s.inverse, w);
-            if (live) storeCodes<E>(codes + kWidth * k, c, C - kWidth * k, w);
+            if (live) storeCodes<kLoads, false, E>(codes + kWidth * k, c, C - kWidth * k, w);
         }
         return;
     }
@@ -62,7 +62,7 @@ __device__ __forceinline__ void writeCodes(const RmsNormForward &a, uint64_t row
         encode<kType, E>(v[k], s.inverse, w);
         const int left = C - kWidth * k - c;
         if (live && left > 0) {
-            storeCodes<E>(codes + kWidth * k, c, C - kWidth * k, w);
+            storeCodes<kLoads, false, E>(codes + kWidth * k, c, C - kWidth * k, w);
             if (lane % kGroupLanes == 0) a.scales[row * groups + uint32_t(kWidth * k + c) / kGroup] = s.scale;
         }
     }
@@ -84,26 +84,6 @@ __device__ __forceinline__ void loadWeights(const void *weight, int type, int c,
     }
 }
 
-// How a row's chunks are loaded.  kEven, for widths of whole chunks: without a
-// branch, from the row's last chunk where there is none, whose values the caller
-// drops (an earlier row's loads need not be waited for at the branch's end).
-enum Loads { kAny, kEven, kEvenStream };
-template <Loads kLoads, typename T, int E>
-__device__ __forceinline__ void loadChunk(Chunk<T, E> &w, const T *row, int c, int C, bool live) {
-    if constexpr (kLoads == kAny) w.loadRow(row, c, C, live);
-    else w.template load<kLoads == kEvenStream>(row + min(c, C - E));
-}
-template <Loads kLoads, typename T, int E>
-__device__ __forceinline__ void storeChunk(T *row, int c, int C, const float (&v)[E]) {
-    if constexpr (kLoads == kAny) {
-        storeRow(row, c, 0, C, v);
-    } else if (c < C) {
-        Chunk<T, E> q(v);
-        // The compiler stores values that it has just rounded to bf16 without the hint.
-        if constexpr (kLoads == kEvenStream) q.forget();
-        q.template store<kLoads == kEvenStream>(row + c);
-    }
-}
 // The row to load from.
 template <Loads kLoads>
 __device__ __forceinline__ uint64_t loadedRow(uint64_t row, uint64_t rows) {
@@ -117,7 +97,6 @@ __global__ __launch_bounds__(kBlock) void rmsForwardKernel(RmsNormForward a) {
     constexpr int E = 16 / int(sizeof(T));
     constexpr int kRows = kBlock / kLanes;
     constexpr int kWidth = kLanes * E;  // columns from chunk to chunk
-    constexpr bool kStream = kLoads == kEvenStream;
     __shared__ float red[2][kBlock / 64][1];
     __shared__ uint32_t most[2][kBlock / 64];
     const int lane = int(threadIdx.x % kLanes), c = lane * E, C = int(a.cols);
@@ -143,7 +122,7 @@ __global__ __launch_bounds__(kBlock) void rmsForwardKernel(RmsNormForward a) {
             if (a.total.p && live) {
                 T *t = static_cast<T *>(a.total.p) + row * a.total.stride;
 #pragma unroll
-                for (int k = 0; k < kChunks; ++k) raw[k].template storeRow<kStream>(t, kWidth * k + c, C);
+                for (int k = 0; k < kChunks; ++k) storeChunk<kLoads>(raw[k], t, kWidth * k + c, C);
             }
         }
         float s[1] = {0.0f};
@@ -162,16 +141,16 @@ __global__ __launch_bounds__(kBlock) void rmsForwardKernel(RmsNormForward a) {
             for (int e = 0; e < E; ++e) v[k][e] = raw[k][e] * rstd;
         if (lane == 0 && live && a.rstd) a.rstd[row] = rstd;
         if (a.codes.p && !a.codesOfOut) {
-            if (a.codeType == BFO_I8) writeCodes<BFO_I8, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
-            else writeCodes<BFO_E4M3, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
+            if (a.codeType == BFO_I8) writeCodes<BFO_I8, kLoads, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
+            else writeCodes<BFO_E4M3, kLoads, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
         }
 #pragma unroll
         for (int k = 0; k < kChunks; ++k)
 #pragma unroll
             for (int e = 0; e < E; ++e) v[k][e] *= w[k][e];
         if (a.codes.p && a.codesOfOut) {
-            if (a.codeType == BFO_I8) writeCodes<BFO_I8, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
-            else writeCodes<BFO_E4M3, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
+            if (a.codeType == BFO_I8) writeCodes<BFO_I8, kLoads, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
+            else writeCodes<BFO_E4M3, kLoads, kLanes, kChunks, kBlock>(a, row, v, most[turn]);
         }
         turn ^= 1;
         if (a.out.p && live) {
@@ -203,12 +182,8 @@ struct Normalised<T, N, true, kLoads> {
     __device__ __forceinline__ void load(const RmsNormBackward &a, uint64_t row, int c, bool live) {
         const int C = int(a.cols);
         const uint8_t *codes = static_cast<const uint8_t *>(a.codes.p) + row * a.codes.stride;
-        if constexpr (kLoads == kAny) {
-            loadCodes<N>(codes, c, C, live, w);
-        } else {
-            c = min(c, C - N);
-            getCodes<N>(codes + c, w);
-        }
+        loadCodeChunk<kLoads, N>(codes, c, C, live, w);
+        if constexpr (kLoads != kAny) c = min(c, C - N);
         const uint32_t groups = a.group ? (a.cols + kGroup - 1) / kGroup : 1, group = a.group ? uint32_t(c) / kGroup : 0;
         scale = kLoads != kAny || (live && c < C) ? a.scales[row * groups + group] : 0.0f;
     }
@@ -416,17 +391,6 @@ void bySlab(uint64_t rows, F f) {
     else if constexpr (kCols > 2048) f(std::integral_constant<int, 16>{});
     else if (rows <= 512) f(std::integral_constant<int, 16>{});
     else f(std::integral_constant<int, 8>{});
-}
-
-template <Loads kValue>
-using Constant = std::integral_constant<Loads, kValue>;
-
-// f with the way to load rows of a call that moves `bytes`.
-template <typename T, typename F>
-void byLoads(uint32_t cols, uint64_t bytes, F f) {
-    if (cols % (16 / sizeof(T))) f(Constant<kAny>{});
-    else if (streams(bytes)) f(Constant<kEvenStream>{});
-    else f(Constant<kEven>{});
 }
 
 template <typename F>
