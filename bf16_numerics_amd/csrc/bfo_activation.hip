@@ -74,10 +74,8 @@ __global__ __launch_bounds__(kBlock) void actForwardKernel(ActivationForward a) 
         Chunk<T, E> gate, up;
         loadChunk<kLoads>(gate, static_cast<const T *>(a.gate.p) + p.row * a.gate.stride, p.c, C, true);
         if constexpr (kGated) loadChunk<kLoads>(up, static_cast<const T *>(a.up.p) + p.row * a.up.stride, p.c, C, true);
-        if (kLoads != kAny && p.c >= C) {
-            gate.zero();
-            if constexpr (kGated) up.zero();
-        }
+        settle<kLoads>(gate, p.c, C, true);
+        if constexpr (kGated) settle<kLoads>(up, p.c, C, true);
         float g[E], u[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -101,21 +99,31 @@ __global__ __launch_bounds__(kBlock) void actForwardKernel(ActivationForward a) 
 }
 
 // A kept input: the matrix itself or its codes.
-template <typename T, int E, int kType, Loads kLoads>
-__device__ __forceinline__ void readKept(const ConstMatrix &m, const ConstCodes &codes, const Place &p,
-                                         const GroupGrid &g, float (&v)[E]) {
-    const int C = int(g.cols);
-    if constexpr (kType == kNoCodes) {
-        Chunk<T, E> raw;
-        loadChunk<kLoads>(raw, static_cast<const T *>(m.p) + p.row * m.stride, p.c, C, true);
+template <typename T, int E, Loads kLoads, int kType>
+struct Kept {
+    uint32_t w[E / 4];
+    float scale;
+    __device__ __forceinline__ void load(const ConstMatrix &, const ConstCodes &codes, const Place &p, const GroupGrid &g) {
+        loadCodes<kLoads, E>(static_cast<const uint8_t *>(codes.p) + p.row * codes.stride, p.c, int(g.cols), true, w);
+        scale = codes.scales[codes.wholeRow ? p.row : p.row * g.perRow.by + p.group];
+    }
+    __device__ __forceinline__ void values(const Place &p, const GroupGrid &g, float (&v)[E]) {
+        settleCodes<kLoads, E>(w, p.c, int(g.cols), true);
+        decode<kType, E>(w, scale, v);
+    }
+};
+template <typename T, int E, Loads kLoads>
+struct Kept<T, E, kLoads, kNoCodes> {
+    Chunk<T, E> raw;
+    __device__ __forceinline__ void load(const ConstMatrix &m, const ConstCodes &, const Place &p, const GroupGrid &g) {
+        loadChunk<kLoads>(raw, static_cast<const T *>(m.p) + p.row * m.stride, p.c, int(g.cols), true);
+    }
+    __device__ __forceinline__ void values(const Place &p, const GroupGrid &g, float (&v)[E]) {
+        settle<kLoads>(raw, p.c, int(g.cols), true);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = raw[e];
-    } else {
-        uint32_t w[E / 4];
-        loadCodeChunk<kLoads, E>(static_cast<const uint8_t *>(codes.p) + p.row * codes.stride, p.c, C, true, w);
-        decode<kType, E>(w, codes.scales[codes.wholeRow ? p.row : p.row * g.perRow.by + p.group], v);
     }
-}
+};
 
 template <typename T, int kKind, bool kGated, int kType, Loads kLoads>
 __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a) {
@@ -124,15 +132,20 @@ __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a
     const int C = int(a.grid.cols);
     for (uint32_t i = blockIdx.x * kAt + threadIdx.x / (kGroup / E); i < a.grid.count; i += gridDim.x * kAt) {
         const Place p = place<E>(a.grid, i);
+        Kept<T, E, kLoads, kType> gate, up;
         float g[E], u[E], y[E];
-        readKept<T, E, kType, kLoads>(a.gate, a.gateCodes, p, a.grid, g);
+        gate.load(a.gate, a.gateCodes, p, a.grid);
         if constexpr (kKind == kIdentity) {
+            gate.values(p, a.grid, g);
             storeChunk<kLoads>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, C, g);
             continue;
         } else {
-            if constexpr (kGated) readKept<T, E, kType, kLoads>(a.up, a.upCodes, p, a.grid, u);
+            if constexpr (kGated) up.load(a.up, a.upCodes, p, a.grid);
             Chunk<T, E> d;
             loadChunk<kLoads>(d, static_cast<const T *>(a.dout.p) + p.row * a.dout.stride, p.c, C, true);
+            gate.values(p, a.grid, g);
+            if constexpr (kGated) up.values(p, a.grid, u);
+            settle<kLoads>(d, p.c, C, true);
             float act[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {

@@ -84,12 +84,6 @@ __device__ __forceinline__ void loadWeights(const void *weight, int type, int c,
     }
 }
 
-// The row to load from.
-template <Loads kLoads>
-__device__ __forceinline__ uint64_t loadedRow(uint64_t row, uint64_t rows) {
-    return kLoads == kAny ? row : min(row, rows - 1);
-}
-
 // kLanes lanes own a row, kChunks 16-byte chunks each; kBlock / kLanes rows
 // per workgroup at a time.
 template <typename T, Loads kLoads, int kLanes, int kChunks, int kBlock>
@@ -106,7 +100,7 @@ __global__ __launch_bounds__(kBlock) void rmsForwardKernel(RmsNormForward a) {
     for (int k = 0; k < kChunks; ++k) loadWeights(a.weight, a.paramDtype, kWidth * k + c, C, w[k]);
     int turn = 0;
     for (uint64_t base = uint64_t(blockIdx.x) * kRows; base < a.rows; base += uint64_t(gridDim.x) * kRows) {
-        const uint64_t row = base + rowGroup<kLanes>(), from = loadedRow<kLoads>(row, a.rows);
+        const uint64_t row = base + rowGroup<kLanes>(), from = loadedRow(row, a.rows);
         const bool live = row < a.rows;
         Chunk<T, E> raw[kChunks];
         const T *x = static_cast<const T *>(a.x.p) + from * a.x.stride;
@@ -118,20 +112,24 @@ __global__ __launch_bounds__(kBlock) void rmsForwardKernel(RmsNormForward a) {
 #pragma unroll
             for (int k = 0; k < kChunks; ++k) loadChunk<kLoads>(more[k], r, kWidth * k + c, C, live);
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k) raw[k].add(more[k]);
+            for (int k = 0; k < kChunks; ++k) {
+                raw[k].add(more[k]);
+                settle<kLoads>(raw[k], kWidth * k + c, C, live);
+            }
             if (a.total.p && live) {
                 T *t = static_cast<T *>(a.total.p) + row * a.total.stride;
 #pragma unroll
                 for (int k = 0; k < kChunks; ++k) storeChunk<kLoads>(raw[k], t, kWidth * k + c, C);
             }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) settle<kLoads>(raw[k], kWidth * k + c, C, live);
         }
         float s[1] = {0.0f};
 #pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-            if (kLoads != kAny && kWidth * k + c >= C) raw[k].zero();
+        for (int k = 0; k < kChunks; ++k)
 #pragma unroll
             for (int e = 0; e < E; ++e) s[0] = fmaf(raw[k][e], raw[k][e], s[0]);
-        }
         rowSums<kLanes, kBlock>(s, red[turn]);
         const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
         float v[kChunks][E];
@@ -170,7 +168,8 @@ struct Normalised<T, N, false, kLoads> {
     __device__ __forceinline__ void load(const RmsNormBackward &a, uint64_t row, int c, bool live) {
         loadChunk<kLoads>(raw, static_cast<const T *>(a.x.p) + row * a.x.stride, c, int(a.cols), live);
     }
-    __device__ __forceinline__ void values(const RmsNormBackward &, float rstd, float (&v)[N]) const {
+    __device__ __forceinline__ void values(const RmsNormBackward &a, float rstd, int c, bool live, float (&v)[N]) {
+        settle<kLoads>(raw, c, int(a.cols), live);
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] = raw[e] * rstd;
     }
@@ -181,13 +180,14 @@ struct Normalised<T, N, true, kLoads> {
     float scale;
     __device__ __forceinline__ void load(const RmsNormBackward &a, uint64_t row, int c, bool live) {
         const int C = int(a.cols);
-        const uint8_t *codes = static_cast<const uint8_t *>(a.codes.p) + row * a.codes.stride;
-        loadCodeChunk<kLoads, N>(codes, c, C, live, w);
-        if constexpr (kLoads != kAny) c = min(c, C - N);
-        const uint32_t groups = a.group ? (a.cols + kGroup - 1) / kGroup : 1, group = a.group ? uint32_t(c) / kGroup : 0;
-        scale = kLoads != kAny || (live && c < C) ? a.scales[row * groups + group] : 0.0f;
+        loadCodes<kLoads, N>(static_cast<const uint8_t *>(a.codes.p) + row * a.codes.stride, c, C, live, w);
+        const uint32_t groups = a.group ? (a.cols + kGroup - 1) / kGroup : 1;
+        scale = a.scales[row * groups + (a.group ? uint32_t(min(c, C - 1)) / kGroup : 0)];
     }
-    __device__ __forceinline__ void values(const RmsNormBackward &a, float, float (&v)[N]) const {
+    __device__ __forceinline__ void values(const RmsNormBackward &a, float, int c, bool live, float (&v)[N]) {
+        const bool there = live && c < int(a.cols);
+        settleCodes<kLoads, N>(w, c, int(a.cols), live);
+        scale = there ? scale : 0.0f;  // of another row or group it may be no number
         if (a.codeType == BFO_I8) decode<BFO_I8, N>(w, scale, v);
         else decode<BFO_E4M3, N>(w, scale, v);
     }
@@ -208,9 +208,9 @@ __device__ __forceinline__ void rowGradients(const RmsNormBackward &a, uint64_t 
     for (int k = 0; k < kChunks; ++k) loadWeights(a.weight, a.paramDtype, kWidth * k + c, C, w[k]);
     int turn = 0;
     for (uint64_t base = first; base < a.rows; base += step) {
-        const uint64_t row = base + sub, from = loadedRow<kLoads>(row, a.rows);
+        const uint64_t row = base + sub, from = loadedRow(row, a.rows);
         const bool live = row < a.rows;
-        const float rstd = kLoads != kAny || live ? a.rstd[from] : 0.0f;
+        const float rstd = a.rstd[from];
         const T *g = static_cast<const T *>(a.dout.p) + from * a.dout.stride;
         Normalised<T, E, kCoded, kLoads> kept[kChunks];
         Chunk<T, E> gr[kChunks];
@@ -222,12 +222,8 @@ __device__ __forceinline__ void rowGradients(const RmsNormBackward &a, uint64_t 
         float xhat[kChunks][E], h[kChunks][E], s[1] = {0.0f};
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
-            kept[k].values(a, rstd, xhat[k]);
-            if (kLoads != kAny && (!live || kWidth * k + c >= C)) {
-                gr[k].zero();
-#pragma unroll
-                for (int e = 0; e < E; ++e) xhat[k][e] = 0.0f;
-            }
+            kept[k].values(a, live ? rstd : 0.0f, kWidth * k + c, live, xhat[k]);
+            settle<kLoads>(gr[k], kWidth * k + c, C, live);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 h[k][e] = gr[k][e] * w[k][e];
@@ -266,7 +262,7 @@ __device__ __forceinline__ void rowGradients(const RmsNormBackward &a, uint64_t 
 // which stay in registers over the rows, are added over the row groups through
 // LDS and end as one row of the partials.
 template <typename T, bool kCoded, Loads kLoads, int kLanes, int kChunks, int kBlock>
-__global__ __launch_bounds__(kBlock) void rmsBackwardKernel(RmsNormBackward a) {
+__global__ __launch_bounds__(kBlock, 4) void rmsBackwardKernel(RmsNormBackward a) {
     constexpr int E = 16 / int(sizeof(T));
     constexpr int kRows = kBlock / kLanes;
     constexpr int kWidth = kLanes * E;
@@ -304,7 +300,7 @@ __global__ __launch_bounds__(kBlock) void rmsBackwardKernel(RmsNormBackward a) {
 // nothing of dx.  The first workgroups sum kSlabCols columns each over all rows (4
 // columns a lane), the others form dx; both read dout and the kept rows, which the
 // caches hold.
-template <typename T, bool kCoded, int kLanes, int kChunks, int kBlock, int kSlabCols>
+template <typename T, bool kCoded, Loads kLoads, int kLanes, int kChunks, int kBlock, int kSlabCols>
 __global__ __launch_bounds__(kBlock) void rmsBackwardFewKernel(RmsNormBackward a, uint32_t slabs) {
     constexpr int E = 16 / int(sizeof(T));
     constexpr int kRows = kBlock / kLanes;
@@ -314,7 +310,7 @@ __global__ __launch_bounds__(kBlock) void rmsBackwardFewKernel(RmsNormBackward a
     __shared__ float sums[kGroups][kSlabCols + 1];
     if (blockIdx.x >= slabs) {
         float none[1][E];
-        rowGradients<T, kCoded, kAny, kLanes, kChunks, kBlock, false>(a, uint64_t(blockIdx.x - slabs) * kRows,
+        rowGradients<T, kCoded, kLoads, kLanes, kChunks, kBlock, false>(a, uint64_t(blockIdx.x - slabs) * kRows,
                                                                       uint64_t(gridDim.x - slabs) * kRows, red, none);
         return;
     }
@@ -324,21 +320,22 @@ __global__ __launch_bounds__(kBlock) void rmsBackwardFewKernel(RmsNormBackward a
     const uint32_t group = threadIdx.x / kRowLanes;
     float dw[N] = {};
     for (uint64_t base = group; base < a.rows; base += kGroups * kAtOnce) {
-        Normalised<T, N, kCoded, kAny> kept[kAtOnce];
+        Normalised<T, N, kCoded, kLoads> kept[kAtOnce];
         Chunk<T, N> gr[kAtOnce];
         float rstd[kAtOnce];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const uint64_t row = base + kGroups * i;
-            const bool live = row < a.rows;
-            kept[i].load(a, row, c, live);
-            gr[i].loadRow(static_cast<const T *>(a.dout.p) + row * a.dout.stride, c, C, live);
-            rstd[i] = live ? a.rstd[row] : 0.0f;
+            const uint64_t row = base + kGroups * i, from = loadedRow(row, a.rows);
+            kept[i].load(a, from, c, row < a.rows);
+            loadChunk<kLoads>(gr[i], static_cast<const T *>(a.dout.p) + from * a.dout.stride, c, C, row < a.rows);
+            rstd[i] = a.rstd[from];
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
+            const bool live = base + kGroups * i < a.rows;
             float xhat[N];
-            kept[i].values(a, rstd[i], xhat);
+            kept[i].values(a, live ? rstd[i] : 0.0f, c, live, xhat);
+            settle<kLoads>(gr[i], c, C, live);
 #pragma unroll
             for (int e = 0; e < N; ++e) dw[e] = fmaf(gr[i][e], xhat[e], dw[e]);
         }
@@ -424,8 +421,10 @@ hipError_t launchRmsNormForward(const RmsNormForward &a, hipStream_t stream) {
                 // At most 16 workgroups of 256 lanes a CU, which keep their weights over
                 // their rows.
                 const uint32_t most = 256 * 16 * 256 / S::kBlock;
-                hipLaunchKernelGGL((rmsForwardKernel<T, decltype(loads)::value, S::kLanes, S::kChunks, S::kBlock>),
-                                   dim3(gridFor(a.rows, S::kBlock / S::kLanes, most)), dim3(S::kBlock), 0, stream, a);
+                if constexpr (decltype(loads)::value != kNarrow || decltype(width)::value == 0)
+                    hipLaunchKernelGGL((rmsForwardKernel<T, decltype(loads)::value, S::kLanes, S::kChunks, S::kBlock>),
+                                       dim3(gridFor(a.rows, S::kBlock / S::kLanes, most)), dim3(S::kBlock), 0, stream,
+                                       a);
             });
         });
     });
@@ -443,18 +442,25 @@ hipError_t launchRmsNormBackward(const RmsNormBackward &a, hipStream_t stream) {
                     if (blocks) {
                         const int matrices = 2 + (a.x.p ? 1 : 0) + (a.out.p ? 1 : 0);
                         byLoads<T>(a.cols, a.rows * a.cols * (matrices * sizeof(T) + (a.x.p ? 0 : 1)), [&](auto loads) {
-                            hipLaunchKernelGGL((rmsBackwardKernel<T, decltype(coded)::value, decltype(loads)::value,
-                                                                  S::kLanes, S::kChunks, S::kBlock>),
-                                               dim3(blocks), dim3(S::kBlock), 0, stream, a);
+                            if constexpr (decltype(loads)::value != kNarrow || decltype(width)::value == 0)
+                                hipLaunchKernelGGL((rmsBackwardKernel<T, decltype(coded)::value, decltype(loads)::value,
+                                                                      S::kLanes, S::kChunks, S::kBlock>),
+                                                   dim3(blocks), dim3(S::kBlock), 0, stream, a);
                         });
                     } else {
                         bySlab<S::kCols>(a.rows, [&](auto columns) {
                             constexpr int kSlabCols = decltype(columns)::value;
                             const uint32_t slabs = Slabs<T, kSlabCols>::workgroups(a.cols);
-                            hipLaunchKernelGGL((rmsBackwardFewKernel<T, decltype(coded)::value, S::kLanes, S::kChunks,
-                                                                     S::kBlock, kSlabCols>),
-                                               dim3(slabs + gridFor(a.rows, S::kRows, 1024)), dim3(S::kBlock), 0,
-                                               stream, a, slabs);
+                            auto with = [&](auto loads) {
+                                hipLaunchKernelGGL((rmsBackwardFewKernel<T, decltype(coded)::value,
+                                                                         decltype(loads)::value, S::kLanes, S::kChunks,
+                                                                         S::kBlock, kSlabCols>),
+                                                   dim3(slabs + gridFor(a.rows, S::kRows, 1024)), dim3(S::kBlock), 0,
+                                                   stream, a, slabs);
+                            };
+                            if constexpr (decltype(width)::value == 0)
+                                if (a.cols < 16 / sizeof(T)) return with(Constant<kNarrow>{});
+                            with(Constant<kRagged>{});
                         });
                     }
                 });
