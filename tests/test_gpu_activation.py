@@ -233,3 +233,45 @@ def test_codes_kept_for_the_backward_pass_cost_what_their_step_is(bfo):
         exact = d.double() * activation(kind, gate.double())[1]
         half = scales.double().repeat_interleave(128, 1) / 2
         assert ((dg.double() - exact).abs() <= d.double().abs() * (1.2 * half * (1 + 1e-5) + 60 * U)).all()
+
+
+@pytest.mark.parametrize("cols", [1, 128])
+def test_more_groups_than_workgroups(bfo, cols):
+    """Above 2^26 groups the workgroups take several turns."""
+    rows = (1 << 26) + 40 if cols == 1 else 1 << 20
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[-64:] = matrix(generator(2), 64, cols, torch.bfloat16)
+    codes, scales = bfo.new_codes(rows, cols, DEV)
+    out = torch.empty_like(x)
+    bfo.activation_forward(x, None, out, gate_codes=codes, gate_scales=scales)
+    check_activation_forward(0, x[-64:], None, out[-64:])
+    check_codes(codes[-64:], scales[-64:], x[-64:].double(), 0, "gate")
+    assert not out[:-64].any() and not codes[:-64].any() and (scales[:-64] == SMALLEST).all()
+    del x, codes, scales, out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("gated", [True, False])
+def test_large_calls(bfo, dt, gated):
+    """Calls that pass through the caches are loaded and stored another way; widths of whole chunks and others."""
+    for cols in (4096, 4100, 4099):
+        rows = 6000 if dt == "bf16" else 3000
+        g, t = generator(cols), TYPES[dt]
+        gate, d = matrix(g, rows, cols, t, size=2.0), matrix(g, rows, cols, t, size=0.01)
+        up = matrix(g, rows, cols, t) if gated else None
+        out = torch.empty_like(gate)
+        kept = {}
+        kept["gate_codes"], kept["gate_scales"] = codes_for(bfo, rows, cols, "i8")
+        if gated:
+            kept["up_codes"], kept["up_scales"] = codes_for(bfo, rows, cols, "i8")
+        bfo.activation_forward(gate, up, out, **kept)
+        check_activation_forward(0, gate, up, out)
+        G = values(kept["gate_codes"], kept["gate_scales"])
+        H = values(kept["up_codes"], kept["up_scales"]) if gated else None
+        check_codes(kept["gate_codes"], kept["gate_scales"], gate.double(), 0, "gate")
+        dgate, dup, again = torch.empty_like(gate), torch.empty_like(gate) if gated else None, torch.empty_like(gate)
+        bfo.activation_backward(d, None, None, dgate, dup, out=again, **kept)
+        check_activation_backward(0, d, G, H, dgate, dup, again, 1)
+        bfo.activation_backward(d, gate, up, dgate, dup, out=again)
+        check_activation_backward(0, d, gate.double(), up.double() if gated else None, dgate, dup, again)

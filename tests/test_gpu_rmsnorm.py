@@ -259,3 +259,20 @@ def test_same_bits_on_other_streams_and_again(bfo):
             again = run_backward(bfo, d, x, w, rstd)
         s.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(again, (dx, dw, out)))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_large_calls(bfo, dt):
+    """Calls that pass through the caches are loaded and stored another way; widths of whole chunks and others."""
+    for cols in (4096, 5000, 5003):
+        rows = 6000 if dt == "bf16" else 3000
+        g, t = generator(cols), TYPES[dt]
+        x, r, d = (matrix(g, rows, cols, t) for _ in range(3))
+        w = weights(g, cols, t)
+        out, total, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device=DEV)
+        codes, scales = codes_for(bfo, rows, cols, "i8")
+        bfo.rmsnorm_forward(x, w, out, residual=r, total=total, rstd=rstd, codes=codes, scales=scales)
+        check_rms_forward(x, r, w, 1e-5, total, out, rstd, codes, scales)
+        check_rms_backward(d, values(codes, scales), w, rstd, *run_backward(bfo, d, None, w, rstd, codes=codes,
+                                                                            scales=scales))
+        check_rms_backward(d, total.double() * rstd.double()[:, None], w, rstd, *run_backward(bfo, d, total, w, rstd))

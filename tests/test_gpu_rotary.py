@@ -122,3 +122,30 @@ def test_turning_back_is_the_inverse_and_the_transpose(bfo):
         assert abs(a - b) <= 30 * 2.0 ** -24 * (turned.double() * y.double()).abs().sum()
         bfo.rotary_apply(turned, f, again, positions=positions, layout=layout, backward=True)
         assert (again - x).abs().max() <= 40 * 2.0 ** -24 * x.abs().max() * 2
+
+
+@pytest.mark.parametrize("half", [True, False])
+def test_large_calls(bfo, half):
+    """Calls that pass through the caches are loaded and stored another way."""
+    for t, dim, rotated in ((torch.bfloat16, 128, 128), (torch.float32, 80, 60), (torch.bfloat16, 100, 50)):
+        x, positions = inputs(dim, 5000, 80, dim, t)
+        f = bfo.rotary_frequencies(rotated, device=DEV)
+        out = torch.empty_like(x)
+        bfo.rotary_apply(x, f, out, positions=positions, layout=0 if half else 1)
+        check_rotary(out, x, positions, f, half)
+        bfo.rotary_apply(x, f, x, positions=positions, layout=0 if half else 1)
+        assert torch.equal(x, out)
+
+
+def test_more_work_than_workgroups(bfo):
+    """Above 2^22 pieces of work the workgroups take several turns."""
+    tokens = (1 << 26) + 50
+    x = torch.zeros(tokens, 1, 256, dtype=torch.bfloat16, device=DEV)
+    last, _ = inputs(11, 50, 1, 256, torch.bfloat16)
+    x[-50:] = last
+    f = bfo.rotary_frequencies(256, device=DEV)
+    bfo.rotary_apply(x, f, x, period=1 << 20)
+    check_rotary(x[-50:], last, torch.arange(tokens - 50, tokens, device=DEV) % (1 << 20), f, True)
+    assert not x[:-50].any()                      # zeros of either sign
+    del x
+    torch.cuda.empty_cache()
