@@ -699,9 +699,10 @@ def _matrix(t, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _DTYPE_CODES:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {t.dim()} dimensions")
-    rows, cols = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {len(shape)} dimensions")
+    rows, cols = shape
     stride, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
@@ -712,6 +713,13 @@ def _matrix(t, name):
 
 def _matrix_like(t, name, dtype, dev, rows, cols):
     """(device pointer, row stride) of a rows x cols matrix of that dtype and device."""
+    try:  # the usual case first: each attribute of a tensor costs about 0.1 us
+        if t.dtype is dtype and t.get_device() == dev and t.shape == (rows, cols):
+            stride, step = t.stride()
+            if step == 1 or cols <= 1:
+                return t.data_ptr(), stride if rows > 1 else cols
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -720,16 +728,18 @@ def _matrix_like(t, name, dtype, dev, rows, cols):
         raise ValueError(f"{name} is on {t.device}, expected {_device(dev)}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    stride, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), stride if rows > 1 else cols
+    raise ValueError(f"{name} must have unit column stride")
 
 
 def _vector(t, dtype, count, name, dev):
     """Device pointer of a contiguous tensor of `count` elements, or None."""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() == count and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -738,9 +748,7 @@ def _vector(t, dtype, count, name, dev):
         raise ValueError(f"{name} is on {t.device}, expected {_device(dev)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() != count:
-        raise ValueError(f"{name} has {t.numel()} elements, expected {count}")
-    return t.data_ptr()
+    raise ValueError(f"{name} has {t.numel()} elements, expected {count}")
 
 
 def _param_type(weight):
@@ -953,6 +961,13 @@ _NO_MATRIX = (None, 0)
 _NO_CODES = (None, 0, None, I8, GROUP)
 
 
+def _first(t, name):
+    """(device pointer, row stride, rows, columns, device index, dtype, its code) of a call's first matrix."""
+    p, stride, rows, cols = _matrix(t, name)
+    dtype = t.dtype
+    return p, stride, rows, cols, t.get_device(), dtype, _DTYPE_CODES[dtype]
+
+
 def _optional_matrix(t, name, dtype, dev, rows, cols):
     return _NO_MATRIX if t is None else _matrix_like(t, name, dtype, dev, rows, cols)
 
@@ -962,11 +977,13 @@ def _codes(codes, scales, name, dev, rows, cols, whole_row=False):
     group) of codes of a rows x cols matrix, or of none."""
     if codes is None and scales is None:
         return _NO_CODES
-    ct = _CODE_TYPES.get(codes.dtype) if isinstance(codes, torch.Tensor) else None
+    dtype = getattr(codes, "dtype", None)
+    ct = _CODE_TYPES.get(dtype)
     if ct is None:
         raise TypeError(f"{name} must be a torch.int8 or torch.float8_e4m3fn tensor")
-    p, stride = _matrix_like(codes, name, codes.dtype, dev, rows, cols)
-    groups = scales.shape[1] if isinstance(scales, torch.Tensor) and scales.dim() == 2 else 0
+    p, stride = _matrix_like(codes, name, dtype, dev, rows, cols)
+    shape = getattr(scales, "shape", ())
+    groups = shape[1] if len(shape) == 2 else 0
     if groups == 1 and whole_row:
         group = 0
     elif groups and groups == (cols + GROUP - 1) // GROUP:
@@ -993,15 +1010,13 @@ def rmsnorm_forward(x, weight, out=None, residual=None, total=None, rstd=None, c
     total * rstd * weight per row; codes and scales keep out (CODES_OF_OUT) or
     total * rstd (CODES_OF_NORMALISED) in 8 bits.  Every output but the ones
     wanted may be None; total may be x or residual."""
-    xp, xs, rows, cols = _matrix(x, "x")
-    dev, dt = x.get_device(), x.dtype
+    xp, xs, rows, cols, dev, dt, code = _first(x, "x")
     pt = _param_type(weight)
     cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
     _launch("rmsnorm_forward", dev, xp, xs, *_optional_matrix(residual, "residual", dt, dev, rows, cols),
             _vector(weight, pt, cols, "weight", dev), *_optional_matrix(total, "total", dt, dev, rows, cols),
             *_optional_matrix(out, "out", dt, dev, rows, cols), _vector(rstd, torch.float32, rows, "rstd", dev),
-            cp, cs, sp, ct, codes_of, group, rows, cols if cols < _U32 else _U32, eps, _DTYPE_CODES[dt],
-            _DTYPE_CODES[pt])
+            cp, cs, sp, ct, codes_of, group, rows, cols if cols < _U32 else _U32, eps, code, _DTYPE_CODES[pt])
 
 
 @functools.lru_cache(maxsize=4096)
@@ -1024,8 +1039,7 @@ def rmsnorm_backward(dout, x, weight, rstd, dx, dweight, codes=None, scales=None
     x (the forward pass's total), or from its codes (CODES_OF_NORMALISED; x
     None).  out, unless None, gets the forward pass's out again.  accumulate_*:
     add to what they hold.  workspace: new_rmsnorm_workspace(rows, cols, device)."""
-    gp, gs, rows, cols = _matrix(dout, "dout")
-    dev, dt = dout.get_device(), dout.dtype
+    gp, gs, rows, cols, dev, dt, code = _first(dout, "dout")
     if (x is None) == (codes is None):
         raise ValueError("either x or codes must be given")
     pt = _param_type(weight)
@@ -1035,7 +1049,7 @@ def rmsnorm_backward(dout, x, weight, rstd, dx, dweight, codes=None, scales=None
             _vector(weight, pt, cols, "weight", dev), _vector(rstd, torch.float32, rows, "rstd", dev),
             *_matrix_like(dx, "dx", dt, dev, rows, cols), _vector(dweight, pt, cols, "dweight", dev),
             *_optional_matrix(out, "out", dt, dev, rows, cols), rows, cols if cols < _U32 else _U32,
-            _DTYPE_CODES[dt], _DTYPE_CODES[pt],
+            code, _DTYPE_CODES[pt],
             (ACCUMULATE_DX if accumulate_dx else 0) | (ACCUMULATE_PARAMS if accumulate_params else 0), ws)
 
 
@@ -1050,13 +1064,12 @@ def activation_forward(gate, up, out, kind=SILU, gate_codes=None, gate_scales=No
     """out = act(gate) * up (act(gate) if up is None), act SILU or GELU; the codes
     and scales keep both inputs in 8 bits for the backward pass.  out may be
     gate or up."""
-    gp, gs, rows, cols = _matrix(gate, "gate")
-    dev, dt = gate.get_device(), gate.dtype
+    gp, gs, rows, cols, dev, dt, code = _first(gate, "gate")
     gc = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
     uc = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
     _launch("activation_forward", dev, gp, gs, *_optional_matrix(up, "up", dt, dev, rows, cols),
             *_matrix_like(out, "out", dt, dev, rows, cols), *gc[:3], *uc[:3], _code_type(gc, uc), rows,
-            cols if cols < _U32 else _U32, kind, _DTYPE_CODES[dt])
+            cols if cols < _U32 else _U32, kind, code)
 
 
 def activation_backward(dout, gate, up, dgate, dup, kind=SILU, gate_codes=None, gate_scales=None, up_codes=None,
@@ -1064,32 +1077,29 @@ def activation_backward(dout, gate, up, dgate, dup, kind=SILU, gate_codes=None, 
     """Gradients of activation_forward into dgate and dup (None without up), from
     gate and up or, where those are None, from their codes; out, unless None,
     gets act(gate) * up again.  Outputs may be dout, gate or up."""
-    op, os_, rows, cols = _matrix(dout, "dout")
-    dev, dt = dout.get_device(), dout.dtype
+    op, os_, rows, cols, dev, dt, code = _first(dout, "dout")
     gc = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
     uc = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
     _launch("activation_backward", dev, op, os_, *_optional_matrix(gate, "gate", dt, dev, rows, cols),
             *_optional_matrix(up, "up", dt, dev, rows, cols), *gc[:3], *uc[:3], _code_type(gc, uc),
             *_matrix_like(dgate, "dgate", dt, dev, rows, cols), *_optional_matrix(dup, "dup", dt, dev, rows, cols),
             *_optional_matrix(out, "out", dt, dev, rows, cols), rows, cols if cols < _U32 else _U32, kind,
-            _DTYPE_CODES[dt])
+            code)
 
 
 def activation_pack(x, codes, scales):
     """x in 8 bits: codes, and a scale for every GROUP columns."""
-    xp, xs, rows, cols = _matrix(x, "x")
-    dev = x.get_device()
+    xp, xs, rows, cols, dev, _, code = _first(x, "x")
     _launch("activation_pack", dev, xp, xs, *_codes(codes, scales, "codes", dev, rows, cols)[:4], rows,
-            cols if cols < _U32 else _U32, _DTYPE_CODES[x.dtype])
+            cols if cols < _U32 else _U32, code)
 
 
 def activation_unpack(codes, scales, out):
     """The values that codes stand for, rounded to out's type."""
-    op, os_, rows, cols = _matrix(out, "out")
-    dev = out.get_device()
+    op, os_, rows, cols, dev, _, code = _first(out, "out")
     cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
     _launch("activation_unpack", dev, cp, cs, sp, ct, group, op, os_, rows, cols if cols < _U32 else _U32,
-            _DTYPE_CODES[out.dtype])
+            code)
 
 
 def rotary_frequencies(rotated, base=10000.0, scaling=ROTARY_UNSCALED, factor=1.0, length=0.0, low=0.0, high=0.0,
