@@ -7,16 +7,16 @@
 // cosines are those of the turn's rest in 32 bits.
 //
 // Bound by memory: every column is read and written once, and the sines are
-// shared by a token's heads.  A workgroup takes a token's heads, up to two
-// 16-byte chunks a lane (or several tokens of few heads, or a part of a token
-// of many): its lanes first ask for the angles' parts, then for their chunks,
-// and form the sines into LDS while those are on their way.  8192 tokens of 64
-// heads of 128 bf16 columns: 46.0 us in halves and 47.2 interleaved, 5.8 and 5.7
-// TB/s, where a copy of the same bytes takes 50.2.  A wavefront a token, walking
-// over its heads with the sines in its own LDS: 62 and 67 us, with four chunks in
-// flight 54 and 56; one 16-byte chunk a lane 46 (halves need two) and 58;
-// workgroups of 256 lanes 47.4 and 46.8, of 1,024 49.9 and 50.0; chunks asked for
-// before the angles 49.8 and 55.6.
+// shared by a token's heads.  A workgroup takes a token's heads, two 16-byte
+// chunks a lane (or several tokens of few heads, or a part of a token of many):
+// its lanes first ask for the angles' parts, then for their chunks, and form the
+// sines into LDS while those are on their way.  8192 tokens of 64 heads of 128
+// bf16 columns: 43.8 us in halves and interleaved, 6.1 TB/s, where a copy of the
+// same bytes takes 50.2; a quarter of the columns rotated, in place 17.3, else 56.6.
+// Of the larger steps there: a wavefront a token, walking over its heads with the
+// sines in its own LDS, 62 us (interleaved 67); four chunks in flight, 54 (56); a
+// workgroup a token, 48 (51); angles asked for first, 46; nontemporal, 43.8.
+// Workgroups of 256 lanes 47.4, of 1,024 49.9.
 #include <type_traits>
 
 #include "bfo_device.hpp"
@@ -26,22 +26,19 @@ namespace bfo {
 namespace {
 
 constexpr int kBlock = 512;
-static_assert(kBlock >= 129, "a head's items fit a workgroup");
+static_assert(kBlock >= 130, "a head's items fit a workgroup");
 constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
 
-// Columns behind the rotated ones that a lane copies at a time.
-constexpr int kCopied = 8;
-
 // What a lane takes at a time: two 16-byte chunks of a head, at column `first` of
-// the first half of its rotated columns and at the same of the second one, or
-// kCopied columns from column `first` on.  In halves the two hold the members of
-// the same pairs; interleaved, each holds pairs of its own, and where their number
-// is odd the halves share the middle one.  (Interleaved, two neighbouring chunks a
-// lane leave every store instruction half of each line: 47.2 us, 53.9 nontemporal.)
-// A head has at most 129 such items, which fit a workgroup.  kWhole: the last item
-// of a half, or of the columns, starts so much earlier that it ends with it;
-// otherwise, for too few of them, it ends inside.  What two items share is the same
-// in both, and read before either writes.
+// the first half of its rotated columns and at the same of the second one, or so
+// of the columns behind them, which are copied.  In halves the two chunks hold the
+// members of the same pairs; interleaved, each holds pairs of its own, and where
+// their number is odd the halves share the middle one.  (Interleaved, two
+// neighbouring chunks a lane leave every store instruction half of each line: 47.2
+// us, 53.9 nontemporal.)  A head has at most 130 such items, which fit a workgroup.
+// kWhole: the last item of a half starts so much earlier that it ends with it;
+// otherwise, for halves of less than a chunk, it ends inside.  What two items share
+// is the same in both, and read before either writes.
 template <typename T, bool kHalf, bool kWhole, bool kStream>
 struct Item {
     static constexpr int E = 16 / int(sizeof(T));
@@ -57,17 +54,13 @@ struct Item {
         if constexpr (kWhole) w.template store<kStream>(head + c);
         else w.template storeRow<kStream>(head, c, there);
     }
-    __device__ __forceinline__ void loadPairs(const T *head, int first, int half, int second) {
+    __device__ __forceinline__ void load(const T *head, int first, int half, int second) {
         get(u, head, first, half);
         get(v, head + second, first, half);
     }
-    __device__ __forceinline__ void loadBehind(const T *head, int first, int dim) {
-        get(u, head, first, dim);
-        if constexpr (kCopied > E) get(v, head + E, first, dim - E);
-    }
-    __device__ __forceinline__ void storeBehind(T *head, int first, int dim) const {
-        put(u, head, first, dim);
-        if constexpr (kCopied > E) put(v, head + E, first, dim - E);
+    __device__ __forceinline__ void store(T *head, int first, int half, int second) const {
+        put(u, head, first, half);
+        put(v, head + second, first, half);
     }
     // The pairs turned, stored.
     __device__ __forceinline__ void turn(const float2 *turns, T *head, int first, int half, int second) const {
@@ -91,11 +84,13 @@ struct Item {
     }
 };
 
-// The columns of each half (even where pairs lie side by side).
+// The columns of each half of the rotated ones (even where pairs lie side by side)
+// and of those behind.
 template <bool kHalf>
 __host__ __device__ uint32_t halfColumns(uint32_t rotated) {
     return kHalf ? rotated / 2 : (rotated / 2 + 1) / 2 * 2;
 }
+__host__ __device__ inline uint32_t halfBehind(uint32_t behind) { return (behind + 1) / 2; }
 
 // Sines and cosines of a workgroup at most: 16 KB of LDS, as four workgroups fill a CU.
 constexpr uint32_t kTurns = 2048;
@@ -141,18 +136,19 @@ __global__ __launch_bounds__(kBlock) void rotaryKernel(Rotary a) {
         const bool live = token < tokens && firstHead + head < a.heads;
         const T *from = x + token * a.xToken + head * a.xHead;
         Item<T, kHalf, kWhole, kStream> item;
-        // The item's first column, in a half or behind them.
+        // The columns that the item is of, their halves, and its first column in them.
         const bool turns = !kBehind || k < turning;
-        int at = turns ? int(k * E) : int(a.rotated) + int(k - turning) * kCopied;
-        if constexpr (kWhole) at = min(at, turns ? int(half - E) : int(a.headDim) - kCopied);
-        if (live && turns) item.loadPairs(from, at, int(half), int(second));
-        else if (kBehind && live) item.loadBehind(from, at, int(a.headDim));
+        const uint32_t start = turns ? 0 : a.rotated, of = turns ? half : halfBehind(a.headDim - a.rotated);
+        const uint32_t other = turns ? second : a.headDim - a.rotated - of;
+        int at = int((turns ? k : k - turning) * E);
+        if constexpr (kWhole) at = min(at, int(of - E));
+        if (live) item.load(from + start, at, int(of), int(other));
         if (threadIdx.x < angles) put(firstToken, angle);
         for (uint32_t i = threadIdx.x + kBlock; i < angles; i += kBlock) put(firstToken, load(firstToken, i));
         __syncthreads();
         T *to = out + token * a.outToken + head * a.outHead;
         if (live && turns) item.turn(table + token * room, to, at, int(half), int(second));
-        else if (kBehind && live) item.storeBehind(to, at, int(a.headDim));
+        else if (kBehind && live) item.store(to + start, at, int(of), int(other));
         if (unit + gridDim.x < a.units) __syncthreads();
     }
 }
@@ -161,7 +157,8 @@ template <typename T, bool kHalf>
 void launch(Rotary a, hipStream_t stream) {
     constexpr uint32_t E = 16 / sizeof(T);
     const uint32_t pairs = a.rotated / 2, half = halfColumns<kHalf>(a.rotated), turning = (half + E - 1) / E;
-    const uint32_t per = turning + (a.x == a.out ? 0 : (a.headDim - a.rotated + kCopied - 1) / kCopied);
+    const uint32_t behind = a.x == a.out ? 0 : a.headDim - a.rotated, copied = halfBehind(behind);
+    const uint32_t per = turning + (copied + E - 1) / E;
     // A workgroup's tokens and heads: as many as its lanes have items for, the heads of a
     // token in blocks of like size.
     const uint32_t fit = kBlock / per;
@@ -183,11 +180,13 @@ void launch(Rotary a, hipStream_t stream) {
                                          decltype(streamed)::value>),
                            grid, dim3(kBlock), lds, stream, a);
     };
-    const bool streamed = streams(2 * sizeof(T) * a.tokens * a.heads * a.headDim);
+    const bool streamed = streams(2 * sizeof(T) * a.tokens * a.heads * (a.rotated + behind));
     constexpr std::true_type yes;
     constexpr std::false_type no;
-    if (half < E || (per > turning && a.headDim - a.rotated < uint32_t(kCopied))) with(no, yes, no);
-    else if (per > turning) streamed ? with(yes, yes, yes) : with(yes, yes, no);
+    // Heads with columns behind are stored in pieces of lines, which nontemporal stores
+    // write one by one: 8192 x 64 x 128, a quarter rotated, 56.6 us against 71.
+    if (half < E || (behind && copied < E)) with(no, yes, no);
+    else if (behind) with(yes, yes, no);
     else streamed ? with(yes, no, yes) : with(yes, no, no);
 }
 
