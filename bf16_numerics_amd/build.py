@@ -1,12 +1,15 @@
-"""Build libbf16opt.so (the C-ABI library) for gfx950 with hipcc, in-tree.
+"""Build libbf16opt.so (the C-ABI library) for gfx950 with hipcc, in-tree: the
+sources side by side into a temporary folder, then linked.
 
 Floating-point flags: -ffp-contract=off (no implicit multiply-add fusion: the
 update's op sequence is fixed), correctly rounded fp32 divide/sqrt and fp32
 denormals kept (HIP's defaults, stated explicitly), and packed-fp32
 instructions disabled.
 """
+from concurrent.futures import ThreadPoolExecutor
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -24,7 +27,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-pthread",
     "-ffp-contract=off",
     "-fhip-fp32-correctly-rounded-divide-sqrt",
@@ -38,12 +40,20 @@ def hipcc():
     return os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
 
 
-def build(verbose: bool = False, extra=()) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra, "-o", tmp, *SOURCES]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+
+
+def build(verbose: bool = False, extra=()) -> str:
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as folder:
+        objects = [os.path.join(folder, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda so: _run([hipcc(), *HIPCC_FLAGS, *extra, "-c", "-o", so[1], so[0]], verbose),
+                          zip(SOURCES, objects)))
+        _run([hipcc(), *HIPCC_FLAGS, *extra, "-shared", "-o", tmp, *objects], verbose)
     os.replace(tmp, LIB)
     return LIB
 
