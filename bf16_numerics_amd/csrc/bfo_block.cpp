@@ -16,7 +16,8 @@ bool knownCodes(int type) { return type == BFO_I8 || type == BFO_E4M3; }
 uint64_t groupsOf(uint64_t cols, uint32_t group) { return group ? (cols + group - 1) / group : 1; }
 
 // Codes of rows x cols values: both arrays or neither.
-int codeMatrix(const void *codes, uint64_t stride, const float *scales, int type, uint64_t rows, uint64_t cols, Rows &out) {
+int codeMatrix(const void *codes, uint64_t stride, const float *scales, int type, uint64_t rows, uint64_t cols,
+               Rows &out) {
     const int rc = optionalMatrix(codes, stride, rows, cols, 1, out);
     if (rc != BFO_OK) return rc;
     if (!codes) return scales ? BFO_EINVAL : BFO_OK;

@@ -59,13 +59,12 @@ hipError_t launchLayerNormBackward(const LayerNormBackward &a, hipStream_t strea
 
 // True for calls whose matrices of `bytes` in all are loaded and stored
 // nontemporally, as they pass through the caches anyway: from half of the last-level
-// cache's 256 MB on.  In turn on inputs that no cache holds, without and with:
-// RMS norm with codes 8192 x 4096 bf16 (303 MB) 57.9 and 49.8 us, 4096 rows 31.5 and
-// 26.9, 1024 rows the same; gated activation with codes 8192 x 11008 (727 MB) 124
-// and 121, 2048 rows (181 MB) 33.9 and 30.2, its gradient 155 and 147, 42.1 and 36.1,
-// 512 rows (57 MB) 11.0 and 11.8; rotary 2048 x 64 x 128 (67 MB) 12.0 and 13.1.
-// With a matrix product that reads the norm's output behind it, 8192 rows 261 and 259
-// us, 2048 76.9 and 77.1.
+// cache's 256 MB on.  On three sets of inputs in turn, without and with: RMS norm with
+// codes 8192 x 4096 bf16 (303 MB) 57.9 and 49.8 us, 4096 rows 31.5 and 26.9, 1024 rows
+// the same; gated activation with codes 8192 x 11008 (727 MB) 124 and 115, 2048 rows
+// (181 MB) 33.9 and 30.2, its gradient 155 and 145, 42.1 and 36.1, 512 rows (57 MB) 11.0
+// and 11.8; rotary 2048 x 64 x 128 (67 MB) 12.0 and 13.1.  With a matrix product that
+// reads the norm's output behind it, 8192 rows 261 and 259 us, 2048 76.9 and 77.1.
 inline bool streams(uint64_t bytes) { return bytes >= (uint64_t(128) << 20); }
 
 // Codes of a matrix, `stride` bytes from row to row, and their scales.

@@ -194,8 +194,9 @@ void launch(Rotary a, hipStream_t stream) {
 
 hipError_t launchRotary(const Rotary &a, int dtype, int layout, hipStream_t stream) {
     if (!a.tokens || !a.heads) return hipSuccess;
-    if (dtype == BFO_BF16) layout == BFO_ROTARY_HALF ? launch<bf16_t, true>(a, stream) : launch<bf16_t, false>(a, stream);
-    else layout == BFO_ROTARY_HALF ? launch<float, true>(a, stream) : launch<float, false>(a, stream);
+    const bool half = layout == BFO_ROTARY_HALF;
+    if (dtype == BFO_BF16) half ? launch<bf16_t, true>(a, stream) : launch<bf16_t, false>(a, stream);
+    else half ? launch<float, true>(a, stream) : launch<float, false>(a, stream);
     return hipGetLastError();
 }
 

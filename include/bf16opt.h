@@ -712,9 +712,9 @@ int rmsnorm_backward(const void *dout, uint64_t dout_stride, const void *x, uint
  * gate_codes with gate_scales, and up_codes with up_scales where up is given,
  * keep both inputs in codes for the backward pass (all of them or none), in
  * groups of BFO_GROUP columns.  out may be gate or up (same pointer and stride).
- * Any infinity or NaN in gate gives what the formula gives, except that -inf
- * gives NaN.  1 <= cols <= BFO_ACTIVATION_MAX_COLS; rows * ceil(cols /
- * BFO_GROUP) <= 2^31 (above -> BFO_ERANGE). */
+ * NaN and infinities in gate give what the formula does (-inf: NaN).
+ * 1 <= cols <= BFO_ACTIVATION_MAX_COLS; rows * ceil(cols / BFO_GROUP) <= 2^31
+ * (above -> BFO_ERANGE). */
 enum { BFO_SILU = 0, BFO_GELU = 1 };
 #define BFO_ACTIVATION_MAX_COLS (1u << 28)
 int activation_forward(const void *gate, uint64_t gate_stride, const void *up, uint64_t up_stride, void *out,
@@ -761,10 +761,16 @@ int activation_unpack(const void *codes, uint64_t codes_stride, const float *sca
  * anything else.  Host only. */
 #define BFO_ROTARY_MAX_DIM 1024u
 #define BFO_ROTARY_MAX_HEADS 65535u
-enum { BFO_ROTARY_UNSCALED = 0, BFO_ROTARY_LINEAR = 1, BFO_ROTARY_BASE = 2, BFO_ROTARY_BY_TURNS = 3, BFO_ROTARY_BY_PAIR = 4 };
+enum {
+    BFO_ROTARY_UNSCALED = 0,
+    BFO_ROTARY_LINEAR = 1,
+    BFO_ROTARY_BASE = 2,
+    BFO_ROTARY_BY_TURNS = 3,
+    BFO_ROTARY_BY_PAIR = 4
+};
 typedef struct {
     int32_t kind;
-    uint32_t reserved;
+    uint32_t reserved;  /* not read */
     double base;
     double factor;
     double length;
