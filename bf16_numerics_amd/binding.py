@@ -1146,6 +1146,8 @@ def rotary_apply(x, frequencies, out, positions=None, period=0, layout=ROTARY_HA
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
     if not isinstance(frequencies, torch.Tensor):
         raise TypeError("frequencies must be a torch.Tensor")
+    if period < 0:
+        raise ValueError(f"period is {period}")
     tokens, heads, dim = x.shape
     pairs = frequencies.numel()
     _launch("rotary_apply", dev, xp, xt, xh, op, ot, oh, tokens, _sized(heads, _U32), _sized(dim, _U32),
