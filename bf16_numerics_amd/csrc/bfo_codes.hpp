@@ -1,9 +1,8 @@
 // bfo_codes.hpp -- what the operators between a block's matrix products share:
 // ways to load and store a row's chunks, and 8-bit codes with scales.
 //
-// Codes: values of a row in groups of
-// kGroup columns (or the whole row), each code an 8-bit integer or an e4m3
-// float, each value code * scale.
+// Codes: values of a row in groups of kGroup columns (or the whole row), each
+// code an 8-bit integer or an e4m3 float, each value code * scale.
 //
 // scale = max(amax / top, 2^-126), amax the group's largest absolute value and
 // top what the code type holds at most (127, 448), so that the largest value
@@ -49,11 +48,12 @@ __device__ __forceinline__ void moveDown(uint32_t (&w)[kWords], int bytes) {
 
 // How a row's chunks are loaded: kEven, widths of whole chunks; kEvenStream, those
 // nontemporally; kRagged, any other width from a chunk on; kNarrow, less than a
-// chunk, value by value.  But for the last, no load waits for a branch: of a row that
-// ends inside the chunk, or before it, its last whole one is asked for, and settle
-// puts it in place where the values are used.  (Behind a branch the compiler waits for every load before
-// it: backward of 16384 x 1600 bf16 from codes 41.5 us against 34.2; of 8192 x 5003,
-// whose ends were read value by value, 152 against 80.)
+// chunk, value by value.  But for the last, no load waits for a branch: of a row
+// that ends inside the chunk, or before it, its last whole one is asked for, and
+// settle puts it in place where the values are used.  (Behind a branch the compiler
+// waits for every load before it: backward of 16384 x 1600 bf16 from codes 41.5 us
+// against 34.2; of 8192 x 5003, whose ends were read value by value, 152 against 80.
+// Nontemporal stores would gain ragged rows 1 to 3%.)
 enum Loads { kNarrow, kRagged, kEven, kEvenStream };
 constexpr bool inParts(Loads loads) { return loads == kNarrow || loads == kRagged; }
 template <Loads kLoads, typename T, int E>
