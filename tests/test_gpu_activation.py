@@ -275,3 +275,18 @@ def test_large_calls(bfo, dt, gated):
         check_activation_backward(0, d, G, H, dgate, dup, again, 1)
         bfo.activation_backward(d, gate, up, dgate, dup, out=again)
         check_activation_backward(0, d, gate.double(), up.double() if gated else None, dgate, dup, again)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+def test_codes_of_a_matrix_as_it_is_are_the_definition_bit_for_bit(bfo, dt, kind):
+    """Every step of the definition is one binary32 operation, so there is nothing to tolerate."""
+    for rows, cols in ((300, 1000), (64, 4096), (7, 129), (5, 3)):
+        x = matrix(generator(cols), rows, cols, TYPES[dt])
+        codes, scales = codes_for(bfo, rows, cols, kind)
+        bfo.activation_pack(x, codes, scales)
+        wide = torch.nn.functional.pad(x.float(), (0, -cols % 128)).view(rows, -1, 128)
+        want = (wide.abs().amax(2) * torch.tensor(1 / TOP[CODES[kind]], device=DEV)).clamp(min=SMALLEST)
+        v = (wide * (1 / want)[:, :, None]).view(rows, -1)[:, :cols]
+        assert torch.equal(scales, want)
+        assert torch.equal(codes.float(), (v.round() if kind == "i8" else v.to(CODES[kind]).float()))
