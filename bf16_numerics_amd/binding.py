@@ -779,7 +779,7 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 
 def _launch(name, dev, *args):
     """Call entry point `name` with device `dev` current, on its current stream."""
-    fn = getattr(_L, name)
+    fn = getattr(_L, name)  # ctypes keeps it
     if _current_device() == dev:
         rc = fn(*args, _current_raw_stream(dev))
     else:
@@ -963,9 +963,27 @@ _NO_CODES = (None, 0, None, I8, GROUP)
 
 def _first(t, name):
     """(device pointer, row stride, rows, columns, device index, dtype, its code) of a call's first matrix."""
-    p, stride, rows, cols = _matrix(t, name)
-    dtype = t.dtype
-    return p, stride, rows, cols, t.get_device(), dtype, _DTYPE_CODES[dtype]
+    try:
+        dtype, dev = t.dtype, t.get_device()
+        code = _DTYPE_CODES.get(dtype)
+        if code is not None and dev >= 0:
+            rows, cols = t.shape
+            stride, step = t.stride()
+            if step == 1 or cols <= 1:
+                return t.data_ptr(), stride if rows > 1 else cols, rows, cols, dev, dtype, code
+    except (AttributeError, ValueError):
+        pass
+    _matrix(t, name)  # says what is wrong with it
+    raise ValueError(f"{name} must be a matrix on a GPU")
+
+
+def _weight(t, cols, dev):
+    """(device pointer, dtype's code) of a weight."""
+    dtype = getattr(t, "dtype", None)
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError("weight must be a torch.bfloat16 or torch.float32 tensor")
+    return _vector(t, dtype, cols, "weight", dev), code
 
 
 def _optional_matrix(t, name, dtype, dev, rows, cols):
@@ -1011,12 +1029,12 @@ def rmsnorm_forward(x, weight, out=None, residual=None, total=None, rstd=None, c
     total * rstd (CODES_OF_NORMALISED) in 8 bits.  Every output but the ones
     wanted may be None; total may be x or residual."""
     xp, xs, rows, cols, dev, dt, code = _first(x, "x")
-    pt = _param_type(weight)
+    wp, wcode = _weight(weight, cols, dev)
     cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
     _launch("rmsnorm_forward", dev, xp, xs, *_optional_matrix(residual, "residual", dt, dev, rows, cols),
-            _vector(weight, pt, cols, "weight", dev), *_optional_matrix(total, "total", dt, dev, rows, cols),
+            wp, *_optional_matrix(total, "total", dt, dev, rows, cols),
             *_optional_matrix(out, "out", dt, dev, rows, cols), _vector(rstd, torch.float32, rows, "rstd", dev),
-            cp, cs, sp, ct, codes_of, group, rows, cols if cols < _U32 else _U32, eps, code, _DTYPE_CODES[pt])
+            cp, cs, sp, ct, codes_of, group, rows, cols if cols < _U32 else _U32, eps, code, wcode)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -1042,14 +1060,14 @@ def rmsnorm_backward(dout, x, weight, rstd, dx, dweight, codes=None, scales=None
     gp, gs, rows, cols, dev, dt, code = _first(dout, "dout")
     if (x is None) == (codes is None):
         raise ValueError("either x or codes must be given")
-    pt = _param_type(weight)
+    wp, wcode = _weight(weight, cols, dev)
     cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
     ws = _workspace_ptr(workspace, rmsnorm_workspace_bytes(rows, cols), dev, "new_rmsnorm_workspace")
     _launch("rmsnorm_backward", dev, gp, gs, *_optional_matrix(x, "x", dt, dev, rows, cols), cp, cs, sp, ct, group,
-            _vector(weight, pt, cols, "weight", dev), _vector(rstd, torch.float32, rows, "rstd", dev),
-            *_matrix_like(dx, "dx", dt, dev, rows, cols), _vector(dweight, pt, cols, "dweight", dev),
+            wp, _vector(rstd, torch.float32, rows, "rstd", dev), *_matrix_like(dx, "dx", dt, dev, rows, cols),
+            _vector(dweight, weight.dtype, cols, "dweight", dev),
             *_optional_matrix(out, "out", dt, dev, rows, cols), rows, cols if cols < _U32 else _U32,
-            code, _DTYPE_CODES[pt],
+            code, wcode,
             (ACCUMULATE_DX if accumulate_dx else 0) | (ACCUMULATE_PARAMS if accumulate_params else 0), ws)
 
 
