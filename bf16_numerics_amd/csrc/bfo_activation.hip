@@ -12,7 +12,7 @@
 // but for the group's largest value.
 //
 // Bound by memory: 8192 x 11008 bf16, gated, both inputs kept (727 MB) 115 us,
-// 6.3 TB/s, the vector ALUs 61% busy; backward from codes with out again (907 MB)
+// 6.3 TB/s, the vector ALUs 53% busy; backward from codes with out again (907 MB)
 // 145 us, 6.3 TB/s.  One group a lane's turn: two or four asked for at once 123 and
 // 130 us, workgroups of 128, 512 and 1,024 lanes 115, 116 and 122.
 #include "bfo_codes.hpp"
@@ -30,9 +30,9 @@ struct Activation {
     __device__ __forceinline__ explicit Activation(float g) {
         // Above 100, where sigma is 0 or 1, g * g might overflow, and 0 times that be NaN.
         const float q = fminf(g * g, 1e4f);
-        const float z = kKind == BFO_SILU ? g : kSlope * g * fmaf(kCubic, q, 1.0f);
-        // Below about -88 the exponential is infinite and sigma 0.
-        sigma = __builtin_amdgcn_rcpf(1.0f + exp2Fast(-kLog2e * z));
+        // -z log2(e): below about -88 its power of 2 is infinite and sigma 0.
+        const float power = kKind == BFO_SILU ? -kLog2e * g : g * fmaf(-kLog2e * kSlope * kCubic, q, -kLog2e * kSlope);
+        sigma = __builtin_amdgcn_rcpf(1.0f + exp2Fast(power));
         act = g * sigma;
         const float dz = kKind == BFO_SILU ? 1.0f : kSlope * fmaf(3.0f * kCubic, q, 1.0f);
         slope = fmaf(act * (1.0f - sigma), dz, sigma);

@@ -104,6 +104,12 @@ typedef uint32_t Bytes8 __attribute__((ext_vector_type(2), aligned(1)));
 
 __device__ __forceinline__ uint32_t absBits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// The value that the lane kBy on in a row of 16 has (in the shape that the compiler
+// makes one instruction of with the maximum that it goes into).
+template <int kBy>
+__device__ __forceinline__ uint32_t rotated(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), kRowRotate + kBy, 0xF, 0xF, true));
+}
 // The largest of the values of the kLanes lanes (16 or 32 from a multiple of it
 // on, or the wavefront), in all of them.
 template <int kLanes>
@@ -112,10 +118,10 @@ __device__ __forceinline__ uint32_t laneMax(uint32_t v) {
     if constexpr (kLanes == 64) {
         return waveExtreme<true>(v);
     } else {
-        v = max(v, uint32_t(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 8, 0xF, 0xF, false)));
-        v = max(v, uint32_t(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 4, 0xF, 0xF, false)));
-        v = max(v, uint32_t(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 2, 0xF, 0xF, false)));
-        v = max(v, uint32_t(__builtin_amdgcn_update_dpp(v, v, kRowRotate + 1, 0xF, 0xF, false)));
+        v = max(v, rotated<8>(v));
+        v = max(v, rotated<4>(v));
+        v = max(v, rotated<2>(v));
+        v = max(v, rotated<1>(v));
         if constexpr (kLanes == 32) {
             const auto both = __builtin_amdgcn_permlane16_swap(v, v, false, false);
             v = max(uint32_t(both[0]), uint32_t(both[1]));
@@ -133,7 +139,11 @@ __device__ __forceinline__ CodeScale codeScale(uint32_t amax) {
     constexpr float kTopInverse = kType == BFO_I8 ? 1.0f / 127.0f : 1.0f / 448.0f, kSmallest = 0x1p-126f;
     float s = __uint_as_float(amax) * kTopInverse;
     s = s < kSmallest ? kSmallest : s;  // a NaN stays
-    return {s, 1.0f / s};
+    // The hardware's reciprocal is a step off at most, from where one of Newton's steps
+    // rounds it as a division would.  (Of an infinity it makes a NaN, which the codes of
+    // such a group may be.)
+    const float r = __builtin_amdgcn_rcpf(s);
+    return {s, fmaf(fmaf(-s, r, 1.0f), r, r)};
 }
 
 // The codes of N values, four to a word.
