@@ -977,6 +977,18 @@ def _first(t, name):
     raise ValueError(f"{name} must be a matrix on a GPU")
 
 
+def _elsewhere(fn, dev, *args):
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _entry(name, dev):
+    """Entry point `name`, called with device `dev` current.  (Of calls with many arguments, packing them
+    twice costs half a microsecond.)"""
+    fn = getattr(_L, name)
+    return fn if _current_device() == dev else functools.partial(_elsewhere, fn, dev)
+
+
 def _weight(t, cols, dev):
     """(device pointer, dtype's code) of a weight."""
     dtype = getattr(t, "dtype", None)
@@ -1031,10 +1043,12 @@ def rmsnorm_forward(x, weight, out=None, residual=None, total=None, rstd=None, c
     xp, xs, rows, cols, dev, dt, code = _first(x, "x")
     wp, wcode = _weight(weight, cols, dev)
     cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
-    _launch("rmsnorm_forward", dev, xp, xs, *_optional_matrix(residual, "residual", dt, dev, rows, cols),
-            wp, *_optional_matrix(total, "total", dt, dev, rows, cols),
-            *_optional_matrix(out, "out", dt, dev, rows, cols), _vector(rstd, torch.float32, rows, "rstd", dev),
-            cp, cs, sp, ct, codes_of, group, rows, cols if cols < _U32 else _U32, eps, code, wcode)
+    rp, rs = _optional_matrix(residual, "residual", dt, dev, rows, cols)
+    tp, ts = _optional_matrix(total, "total", dt, dev, rows, cols)
+    op, os_ = _optional_matrix(out, "out", dt, dev, rows, cols)
+    _check("rmsnorm_forward", _entry("rmsnorm_forward", dev)(
+        xp, xs, rp, rs, wp, tp, ts, op, os_, _vector(rstd, torch.float32, rows, "rstd", dev), cp, cs, sp, ct, codes_of,
+        group, rows, cols if cols < _U32 else _U32, eps, code, wcode, _current_raw_stream(dev)))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -1063,19 +1077,14 @@ def rmsnorm_backward(dout, x, weight, rstd, dx, dweight, codes=None, scales=None
     wp, wcode = _weight(weight, cols, dev)
     cp, cs, sp, ct, group = _codes(codes, scales, "codes", dev, rows, cols, whole_row=True)
     ws = _workspace_ptr(workspace, rmsnorm_workspace_bytes(rows, cols), dev, "new_rmsnorm_workspace")
-    _launch("rmsnorm_backward", dev, gp, gs, *_optional_matrix(x, "x", dt, dev, rows, cols), cp, cs, sp, ct, group,
-            wp, _vector(rstd, torch.float32, rows, "rstd", dev), *_matrix_like(dx, "dx", dt, dev, rows, cols),
-            _vector(dweight, weight.dtype, cols, "dweight", dev),
-            *_optional_matrix(out, "out", dt, dev, rows, cols), rows, cols if cols < _U32 else _U32,
-            code, wcode,
-            (ACCUMULATE_DX if accumulate_dx else 0) | (ACCUMULATE_PARAMS if accumulate_params else 0), ws)
-
-
-def _code_type(first, second):
-    """The one code type of two matrices, of which the second may be none."""
-    if second[0] is not None and first[3] != second[3]:
-        raise TypeError("gate_codes and up_codes must have the same type")
-    return first[3]
+    xp, xs = _optional_matrix(x, "x", dt, dev, rows, cols)
+    dp, ds = _matrix_like(dx, "dx", dt, dev, rows, cols)
+    op, os_ = _optional_matrix(out, "out", dt, dev, rows, cols)
+    _check("rmsnorm_backward", _entry("rmsnorm_backward", dev)(
+        gp, gs, xp, xs, cp, cs, sp, ct, group, wp, _vector(rstd, torch.float32, rows, "rstd", dev), dp, ds,
+        _vector(dweight, weight.dtype, cols, "dweight", dev), op, os_, rows, cols if cols < _U32 else _U32, code, wcode,
+        (ACCUMULATE_DX if accumulate_dx else 0) | (ACCUMULATE_PARAMS if accumulate_params else 0), ws,
+        _current_raw_stream(dev)))
 
 
 def activation_forward(gate, up, out, kind=SILU, gate_codes=None, gate_scales=None, up_codes=None, up_scales=None):
@@ -1083,11 +1092,15 @@ def activation_forward(gate, up, out, kind=SILU, gate_codes=None, gate_scales=No
     and scales keep both inputs in 8 bits for the backward pass.  out may be
     gate or up."""
     gp, gs, rows, cols, dev, dt, code = _first(gate, "gate")
-    gc = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
-    uc = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
-    _launch("activation_forward", dev, gp, gs, *_optional_matrix(up, "up", dt, dev, rows, cols),
-            *_matrix_like(out, "out", dt, dev, rows, cols), *gc[:3], *uc[:3], _code_type(gc, uc), rows,
-            cols if cols < _U32 else _U32, kind, code)
+    up_, us = _optional_matrix(up, "up", dt, dev, rows, cols)
+    op, os_ = _matrix_like(out, "out", dt, dev, rows, cols)
+    gcp, gcs, gsp, ct, _ = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
+    ucp, ucs, usp, uct, _ = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
+    if ucp is not None and uct != ct:
+        raise TypeError("gate_codes and up_codes must have the same type")
+    _check("activation_forward", _entry("activation_forward", dev)(
+        gp, gs, up_, us, op, os_, gcp, gcs, gsp, ucp, ucs, usp, ct, rows, cols if cols < _U32 else _U32, kind, code,
+        _current_raw_stream(dev)))
 
 
 def activation_backward(dout, gate, up, dgate, dup, kind=SILU, gate_codes=None, gate_scales=None, up_codes=None,
@@ -1096,13 +1109,18 @@ def activation_backward(dout, gate, up, dgate, dup, kind=SILU, gate_codes=None, 
     gate and up or, where those are None, from their codes; out, unless None,
     gets act(gate) * up again.  Outputs may be dout, gate or up."""
     op, os_, rows, cols, dev, dt, code = _first(dout, "dout")
-    gc = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
-    uc = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
-    _launch("activation_backward", dev, op, os_, *_optional_matrix(gate, "gate", dt, dev, rows, cols),
-            *_optional_matrix(up, "up", dt, dev, rows, cols), *gc[:3], *uc[:3], _code_type(gc, uc),
-            *_matrix_like(dgate, "dgate", dt, dev, rows, cols), *_optional_matrix(dup, "dup", dt, dev, rows, cols),
-            *_optional_matrix(out, "out", dt, dev, rows, cols), rows, cols if cols < _U32 else _U32, kind,
-            code)
+    gp, gs = _optional_matrix(gate, "gate", dt, dev, rows, cols)
+    up_, us = _optional_matrix(up, "up", dt, dev, rows, cols)
+    gcp, gcs, gsp, ct, _ = _codes(gate_codes, gate_scales, "gate_codes", dev, rows, cols)
+    ucp, ucs, usp, uct, _ = _codes(up_codes, up_scales, "up_codes", dev, rows, cols)
+    if ucp is not None and uct != ct:
+        raise TypeError("gate_codes and up_codes must have the same type")
+    dgp, dgs = _matrix_like(dgate, "dgate", dt, dev, rows, cols)
+    dup_, dus = _optional_matrix(dup, "dup", dt, dev, rows, cols)
+    ap, as_ = _optional_matrix(out, "out", dt, dev, rows, cols)
+    _check("activation_backward", _entry("activation_backward", dev)(
+        op, os_, gp, gs, up_, us, gcp, gcs, gsp, ucp, ucs, usp, ct, dgp, dgs, dup_, dus, ap, as_, rows,
+        cols if cols < _U32 else _U32, kind, code, _current_raw_stream(dev)))
 
 
 def activation_pack(x, codes, scales):
@@ -1131,20 +1149,29 @@ def rotary_frequencies(rotated, base=10000.0, scaling=ROTARY_UNSCALED, factor=1.
     return torch.tensor(out[:], dtype=torch.float64, device=device)
 
 
-def _heads(t, name):
-    """(device pointer, token stride, head stride) of a tokens x heads x columns tensor."""
+def _heads(t, name, like=None):
+    """(device pointer, token stride, head stride, shape, dtype, device index) of a tokens x heads x columns
+    tensor, of the shape, dtype and device in `like` if that is given."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _DTYPE_CODES:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be 3-D (tokens, heads, columns), got {t.dim()} dimensions")
+    dtype, shape, dev = t.dtype, t.shape, t.get_device()
+    if like is None:
+        if dtype not in _DTYPE_CODES:
+            raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+        if len(shape) != 3:
+            raise ValueError(f"{name} must be 3-D (tokens, heads, columns), got {len(shape)} dimensions")
+    elif (shape, dtype, dev) != like:
+        if dtype != like[1]:
+            raise TypeError(f"{name} must be {like[1]}, got {dtype}")
+        if dev != like[2]:
+            raise ValueError(f"{name} is on {t.device}, expected {_device(like[2])}")
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {tuple(like[0])}")
     tokens, heads, step = t.stride()
-    if step != 1 and t.shape[2] > 1:
+    if step != 1 and shape[2] > 1:
         raise ValueError(f"{name} must have unit column stride")
-    if not t.is_cuda:
+    if dev < 0:
         raise ValueError(f"{name} is on {t.device}, expected a GPU")
-    return t.data_ptr(), tokens, heads
+    return t.data_ptr(), tokens, heads, shape, dtype, dev
 
 
 def rotary_apply(x, frequencies, out, positions=None, period=0, layout=ROTARY_HALF, amplitude=1.0, backward=False):
@@ -1153,22 +1180,16 @@ def rotary_apply(x, frequencies, out, positions=None, period=0, layout=ROTARY_HA
     back, which takes the gradient of out to that of x.  frequencies: float64, on
     the GPU.  positions: int32 per token, or None for the token's index (modulo
     period if that is not 0).  out may be x."""
-    xp, xt, xh = _heads(x, "x")
-    op, ot, oh = _heads(out, "out")
-    dev = x.get_device()
-    if out.dtype != x.dtype:
-        raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
-    if out.get_device() != dev:
-        raise ValueError(f"out is on {out.device}, expected {_device(dev)}")
-    if out.shape != x.shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
+    xp, xt, xh, shape, dtype, dev = _heads(x, "x")
+    op, ot, oh, _, _, _ = _heads(out, "out", (shape, dtype, dev))
     if not isinstance(frequencies, torch.Tensor):
         raise TypeError("frequencies must be a torch.Tensor")
     if period < 0:
         raise ValueError(f"period is {period}")
-    tokens, heads, dim = x.shape
+    tokens, heads, dim = shape
     pairs = frequencies.numel()
-    _launch("rotary_apply", dev, xp, xt, xh, op, ot, oh, tokens, _sized(heads, _U32), _sized(dim, _U32),
-            _sized(2 * pairs, _U32), layout, _vector(frequencies, torch.float64, pairs, "frequencies", dev),
-            _vector(positions, torch.int32, tokens, "positions", dev), period, amplitude, int(backward),
-            _DTYPE_CODES[x.dtype])
+    _check("rotary_apply", _entry("rotary_apply", dev)(
+        xp, xt, xh, op, ot, oh, tokens, _sized(heads, _U32), _sized(dim, _U32), _sized(2 * pairs, _U32), layout,
+        _vector(frequencies, torch.float64, pairs, "frequencies", dev),
+        _vector(positions, torch.int32, tokens, "positions", dev), period, amplitude, int(backward),
+        _DTYPE_CODES[dtype], _current_raw_stream(dev)))
