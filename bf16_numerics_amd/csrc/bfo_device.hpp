@@ -89,10 +89,9 @@ struct Chunk {
         }
     }
     // Stores the columns [c, c + N) of those from `base` on that lie in [0, cols).
-    template <bool kNontemporal = false>
     __device__ __forceinline__ void storeRow(T *base, int c, int cols) const {
         if (c + N <= cols) {
-            store<kNontemporal>(base + c);
+            store(base + c);
         } else if (c < cols) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -103,10 +102,9 @@ struct Chunk {
     // 0 for the others, and for all if not `live`.  The zeros come first, so that
     // no load waits for another one's lanes.  Here and below a `base` that is the
     // same in all lanes keeps the addresses at one scalar and one lane offset.
-    template <bool kNontemporal = false>
     __device__ __forceinline__ void loadRow(const T *base, int c, int cols, bool live = true) {
         zero();
-        if (live && c + N <= cols) load<kNontemporal>(base + c);
+        if (live && c + N <= cols) load(base + c);
         else if (live && c < cols) loadPart(base, c, 0, cols);
     }
     // The same with [lo, hi) there and -inf elsewhere.
@@ -133,13 +131,10 @@ struct Chunk {
 
 // Stores N values, rounded to T, at those of the columns [c, c + N) from
 // `base` on that lie in [lo, hi).
-template <bool kNontemporal = false, typename T, int N>
+template <typename T, int N>
 __device__ __forceinline__ void storeRow(T *base, int c, int lo, int hi, const float (&v)[N]) {
     if (c >= lo && c + N <= hi) {
-        Chunk<T, N> q(v);
-        // The compiler stores values that it has just rounded to bf16 without the hint.
-        if constexpr (kNontemporal) q.forget();
-        q.template store<kNontemporal>(base + c);
+        Chunk<T, N>(v).store(base + c);
     } else if (c + N > lo && c < hi) {
 #pragma unroll
         for (int i = 0; i < N; ++i)

@@ -47,12 +47,12 @@ struct Item {
     // A chunk at column c of a head, of which `there` columns are there.
     __device__ __forceinline__ static void get(Chunk<T, E> &w, const T *head, int c, int there) {
         if constexpr (kWhole) w.template load<kStream>(head + c);
-        else w.template loadRow<kStream>(head, c, there);
+        else w.loadRow(head, c, there);
     }
     __device__ __forceinline__ static void put(Chunk<T, E> w, T *head, int c, int there) {
         if constexpr (kStream) w.forget();
         if constexpr (kWhole) w.template store<kStream>(head + c);
-        else w.template storeRow<kStream>(head, c, there);
+        else w.storeRow(head, c, there);
     }
     __device__ __forceinline__ void load(const T *head, int first, int half, int second) {
         get(u, head, first, half);
