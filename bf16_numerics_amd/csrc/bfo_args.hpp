@@ -68,8 +68,10 @@ bool conflict(const Rows &m, bool written, const Use (&use)[N]) {
     return false;
 }
 
-// True when a written matrix shares a byte with another one of the call; a
-// written one that is `inPlace` may be the same matrix as one that is read.
+// True when a written matrix shares a byte with another one of the call; but
+// where both are marked `inPlace`, a written one may be the same matrix as one
+// that is read.  (Only matrices of one type may be marked: the kernels read a
+// value before they write it, not the bytes of other columns around it.)
 struct MatrixUse {
     Rows at;
     bool written, inPlace;
@@ -81,7 +83,7 @@ bool conflict(const MatrixUse (&use)[N]) {
             const MatrixUse &a = use[i], &b = use[j];
             if (!(a.written || b.written) || !overlap(a.at, b.at)) continue;
             const bool same = a.at.p == b.at.p && (a.at.stride == b.at.stride || a.at.rows < 2);
-            if (!(same && (a.written != b.written) && (a.inPlace || b.inPlace))) return true;
+            if (!(same && a.written != b.written && a.inPlace && b.inPlace)) return true;
         }
     return false;
 }

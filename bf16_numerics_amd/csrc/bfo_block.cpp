@@ -65,7 +65,7 @@ int activationForward(ActivationForward a, uint64_t rows, uint32_t cols, void *s
     if (rc != BFO_OK) return rc;
     if (rows && ((pack && !coded) || (a.upCodes.p != nullptr) != (gated && coded))) return BFO_EINVAL;
     if (!coded) a.codeType = kNoCodes;
-    const MatrixUse matrices[] = {{gate, false, false}, {up, false, false}, {out, true, true},
+    const MatrixUse matrices[] = {{gate, false, true}, {up, false, true}, {out, true, true},
                                   {gateCodes, true, false}, {upCodes, true, false}};
     const Use use[] = {writes(a.gateCodes.scales, scales), writes(a.upCodes.scales, scales)};
     if (conflict(matrices) || conflict(matrices, use)) return BFO_EINVAL;
@@ -109,7 +109,7 @@ int rmsnorm_forward(const void *x, uint64_t x_stride, const void *residual, uint
                   codeMatrix(codes, codes_stride, scales, code_type, rows, cols, coded)});
     if (rc != BFO_OK) return rc;
     if (!alignedTo(weight, sizeOf(param_dtype)) || !alignedTo(rstd, 4)) return BFO_EMISALIGNED;
-    const MatrixUse matrices[] = {{in, false, false}, {more, false, false}, {sum, true, true}, {res, true, false},
+    const MatrixUse matrices[] = {{in, false, true}, {more, false, true}, {sum, true, true}, {res, true, false},
                                   {coded, true, false}};
     const Use use[] = {reads(weight, cols * sizeOf(param_dtype)), writes(rstd, 4 * rows),
                        writes(scales, 4 * rows * groupsOf(cols, group))};
@@ -205,7 +205,7 @@ int activation_backward(const void *dout, uint64_t dout_stride, const void *gate
     if (rows && ((gate != nullptr) == coded || (up != nullptr) != (gated && !coded) ||
                  (up_codes != nullptr) != (gated && coded)))
         return BFO_EINVAL;
-    const MatrixUse matrices[] = {{g, false, false}, {in, false, false}, {more, false, false},
+    const MatrixUse matrices[] = {{g, false, true}, {in, false, true}, {more, false, true},
                                   {inCodes, false, false}, {moreCodes, false, false}, {gradIn, true, true},
                                   {gradMore, true, true}, {again, true, true}};
     const Use use[] = {reads(gate_scales, scales), reads(up_scales, scales)};
@@ -281,7 +281,7 @@ int rotary_apply(const void *x, uint64_t x_token_stride, uint64_t x_head_stride,
     if (!alignedTo(frequencies, 8) || !alignedTo(positions, 4)) return BFO_EMISALIGNED;
     const bool same = x == out && (tokens < 2 || x_token_stride == out_token_stride) &&
                       (heads < 2 || x_head_stride == out_head_stride);
-    const MatrixUse matrices[] = {{in, false, false}, {res, true, same}};
+    const MatrixUse matrices[] = {{in, false, same}, {res, true, same}};
     const Use use[] = {reads(frequencies, 4 * uint64_t(rotated)), reads(positions, 4 * tokens)};
     if (conflict(matrices) || conflict(matrices, use)) return BFO_EINVAL;
     const Rotary a{x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, tokens, heads, head_dim,

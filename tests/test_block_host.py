@@ -297,3 +297,22 @@ def test_binding_names_what_is_wrong(bfo):
         with pytest.raises(bfo.BfoError) as e:
             bfo.rmsnorm_workspace_bytes(4, cols)
         assert e.value.status == bfo.ERANGE
+
+
+def test_activation_gradients_do_not_go_over_the_codes(bfo):
+    """Outputs may be dout, gate and up, the matrices of their own type; over codes, a byte a column, they would be
+    written where other columns have still to be read: refused also where pointer and bytes from row to row agree."""
+    coded = dict(g=None, u=None, gq=ptr(6), gsc=ptr(7), uq=ptr(8), usc=ptr(9))
+    for dt, size in ((0, 2), (1, 4)):
+        for codes in ("gq", "uq"):
+            for out, stride in (("dg", "dgs"), ("du", "dus"), ("out", "os")):
+                over = {**coded, "dt": dt, out: coded[codes]}
+                what = (dt, codes, out)
+                assert act_backward(bfo, **over, rows=1) == bfo.EINVAL, what
+                assert act_backward(bfo, **over, rows=1, cols=1) == bfo.EINVAL, what
+                over[codes + "s"], over[stride] = 256 * size, 256
+                for rows in (1, 2, 4):
+                    assert act_backward(bfo, **over, rows=rows) == bfo.EINVAL, (what, rows)
+            # without a gate too
+            one = dict(g=None, u=None, du=None, gq=ptr(6), gqs=256 * size, gsc=ptr(7), dt=dt, dg=ptr(6))
+            assert act_backward(bfo, **one) == bfo.EINVAL and act_backward(bfo, **{**one, "dg": ptr(3)}, out=ptr(6)) == bfo.EINVAL
