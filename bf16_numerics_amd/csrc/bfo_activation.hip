@@ -21,18 +21,44 @@ namespace bfo {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr float kSlope = 1.5957691216057308f, kCubic = 0.044715f;
+constexpr float kSlope = 1.5957691216057308f, kCubic = 0.044715f;  // 2 sqrt(2 / pi)
+
+// exp(-z) as the hardware's power of 2.  A rounding of the exponent -z log2(e) is one
+// of the power times |z|, which 16 bits of a result do not show but 32 do: 63 * 2^-24
+// of an activation at g = -80.  For fp32 results the power is corrected by what the
+// exponent's rounding left, unless it is past the range anyway (infinite, or 0): from
+// the product's own rest and log2(e)'s for SiLU, from 64 bits for GELU's cubic.
+// Without and with that, gated, codes kept, fp32: 8192 x 11008 199.0 and 198.9 us (GELU
+// 198.6 and 199.0), 1003 x 6400 16.6 and 16.8 (GELU 16.6 and 17.3).
+template <int kKind, bool kFine>
+__device__ __forceinline__ float expNegative(float g, float q) {
+    if constexpr (!kFine)
+        return exp2Fast(kKind == BFO_SILU ? -kLog2e * g
+                                          : g * fmaf(-kLog2e * kSlope * kCubic, q, -kLog2e * kSlope));
+    constexpr double kLog2eFull = 1.44269504088896340736, kLinear = -kLog2eFull * 1.5957691216057308;
+    float power, left;
+    if constexpr (kKind == BFO_SILU) {
+        constexpr float kRest = float(kLog2eFull - double(kLog2e));
+        power = -kLog2e * g;
+        left = fmaf(-kRest, g, fmaf(-kLog2e, g, -power));
+    } else {
+        const double d = g, whole = d * fma(kLinear * 0.044715, d * d, kLinear);
+        power = float(whole);
+        left = float(whole - double(power));
+    }
+    const float e = exp2Fast(power);
+    return fabsf(power) < 128.0f ? fmaf(e, left * kLn2, e) : e;
+}
 
 // sigma(z), act and its derivative.
-template <int kKind>
+template <int kKind, bool kFine>
 struct Activation {
     float sigma, act, slope;
     __device__ __forceinline__ explicit Activation(float g) {
         // Above 100, where sigma is 0 or 1, g * g might overflow, and 0 times that be NaN.
         const float q = fminf(g * g, 1e4f);
-        // -z log2(e): below about -88 its power of 2 is infinite and sigma 0.
-        const float power = kKind == BFO_SILU ? -kLog2e * g : g * fmaf(-kLog2e * kSlope * kCubic, q, -kLog2e * kSlope);
-        sigma = __builtin_amdgcn_rcpf(1.0f + exp2Fast(power));
+        // For z below about -88 the exponential is infinite and sigma 0.
+        sigma = __builtin_amdgcn_rcpf(1.0f + expNegative<kKind, kFine>(g, q));
         act = g * sigma;
         const float dz = kKind == BFO_SILU ? 1.0f : kSlope * fmaf(3.0f * kCubic, q, 1.0f);
         slope = fmaf(act * (1.0f - sigma), dz, sigma);
@@ -96,7 +122,7 @@ __global__ __launch_bounds__(kBlock) void actForwardKernel(ActivationForward a) 
             float y[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const Activation<kKind> f(g[e]);
+                const Activation<kKind, sizeof(T) == 4> f(g[e]);
                 y[e] = kGated ? f.act * u[e] : f.act;
             }
             storeChunk<kLoads>(static_cast<T *>(a.out.p) + p.row * a.out.stride, p.c, C, y);
@@ -156,7 +182,7 @@ __global__ __launch_bounds__(kBlock) void actBackwardKernel(ActivationBackward a
             float act[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const Activation<kKind> f(g[e]);
+                const Activation<kKind, sizeof(T) == 4> f(g[e]);
                 act[e] = f.act;
                 y[e] = (kGated ? d[e] * u[e] : d[e]) * f.slope;
             }

@@ -3,8 +3,8 @@ codes by themselves, against their definitions in 64 bits."""
 import pytest
 import torch
 
-from block_reference import CODES, DEV, SMALLEST, TOP, TYPES, U, activation, check_activation_backward, \
-    check_activation_forward, check_codes, check_rounded, empty, matrix, normal, untouched, values
+from block_reference import CODES, DEV, SMALLEST, TOP, TYPES, U, activation, check, \
+    check_activation_backward, check_activation_forward, check_codes, check_rounded, empty, matrix, normal, untouched, values
 
 pytestmark = pytest.mark.gpu
 SHAPES = [(1, 1), (3, 1), (1, 11008), (7, 2), (5, 15), (33, 16), (17, 31), (40, 127), (16, 128), (19, 129), (9, 511),
@@ -290,3 +290,30 @@ def test_codes_of_a_matrix_as_it_is_are_the_definition_bit_for_bit(bfo, dt, kind
         v = (wide * (1 / want)[:, :, None]).view(rows, -1)[:, :cols]
         assert torch.equal(scales, want)
         assert torch.equal(codes.float(), (v.round() if kind == "i8" else v.to(CODES[kind]).float()))
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_negative_gates_keep_their_digits(bfo, kind):
+    """fp32 results relative to themselves, however small: z's exponential is off by two roundings and the one
+    that takes in what its exponent's rounding left, their sum by one, the reciprocal by two and the product with
+    the gate by one; none of them grows with |z|.  (Down to z = -85 nothing is below 2^-126.)"""
+    g, low = generator(77), (80.0, 9.8)[kind]
+    gate = -low * torch.rand(64, 1000, generator=g, device=DEV)
+    gate[0] = -torch.linspace(0, low, 1000, device=DEV)
+    up, d = (normal(g, 64, 1000) for _ in range(2))
+    out, dg, du, plain = (torch.empty_like(gate) for _ in range(4))
+    G, H, D = gate.double(), up.double(), d.double()
+    act, slope, s, t, z, dz = activation(kind, G)
+    rel = (3 * t + 4) * U
+    # the derivative: sigma, act * (1 - sigma) * dz with five roundings of dz and two products, and their sum
+    off = s * rel + (act * t * dz).abs() * (rel + 9 * U) + (act * dz).abs() * (s * rel + U) + U * slope.abs()
+    bfo.activation_forward(gate, None, plain, kind=kind)
+    check(plain, act, act.abs() * (rel + U), "out")
+    bfo.activation_forward(gate, up, out, kind=kind)
+    check(out, act * H, (act * H).abs() * (rel + 2 * U), "gated out")
+    bfo.activation_backward(d, gate, up, dg, du, kind=kind, out=out)
+    check(dg, D * H * slope, (D * H).abs() * (off + 2 * U * slope.abs()), "dgate")
+    check(du, D * act, (D * act).abs() * (rel + 2 * U), "dup")
+    check(out, act * H, (act * H).abs() * (rel + 2 * U), "out again")
+    bfo.activation_backward(d, gate, None, dg, None, kind=kind)
+    check(dg, D * slope, D.abs() * (off + U * slope.abs()), "dgate without up")
