@@ -4,7 +4,8 @@
 //   (a, b) -> amplitude * (a cos - b sin, a sin + b cos),
 // backward by the negative angle, which is the transpose.  Angles are formed
 // and reduced to a turn in 64 bits, so that far positions keep them; sines and
-// cosines are those of the turn's rest in 32 bits.
+// cosines are those of the turn's rest in 32 bits, moved by what its rounding left
+// (which is up to 2^-26 of a turn, all of a sine near half a turn).
 //
 // Bound by memory: every column is read and written once, and the sines are
 // shared by a token's heads.  A workgroup takes a token's heads, two 16-byte
@@ -27,7 +28,7 @@ namespace {
 
 constexpr int kBlock = 512;
 static_assert(kBlock >= 130, "a head's items fit a workgroup");
-constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
+constexpr double kRadians = 6.283185307179586476925, kTurn = 1.0 / kRadians;  // of a turn
 
 // What a lane takes at a time: two 16-byte chunks of a head, at column `first` of
 // the first half of its rotated columns and at the same of the second one, or so
@@ -117,9 +118,11 @@ __global__ __launch_bounds__(kBlock) void rotaryKernel(Rotary a) {
         const double position = a.positions ? double(angle.position) : double(a.period ? n % a.period : n);
         double turn = position * angle.frequency * kTurn;
         turn -= rint(turn);
+        const float rest = float(turn), left = float((turn - double(rest)) * kRadians);
         float s, c;
-        sincospif(2.0f * float(turn), &s, &c);
-        table[angle.token * room + angle.pair] = {c * a.amplitude, (a.backward ? -s : s) * a.amplitude};
+        sincospif(2.0f * rest, &s, &c);
+        const float sine = fmaf(c, left, s), cosine = fmaf(-s, left, c);
+        table[angle.token * room + angle.pair] = {cosine * a.amplitude, (a.backward ? -sine : sine) * a.amplitude};
     };
     for (uint32_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
         const uint32_t block = a.headBlocks.divide(unit);

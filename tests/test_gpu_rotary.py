@@ -1,4 +1,6 @@
 """Rotary positions on the GPU against their definition in 64 bits."""
+import math
+
 import pytest
 import torch
 
@@ -149,3 +151,22 @@ def test_more_work_than_workgroups(bfo):
     assert not x[:-50].any()                      # zeros of either sign
     del x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_small_sines_and_cosines_keep_their_digits(bfo, backward):
+    """Near whole quarters of a turn, relative to themselves: sine or cosine is off by two steps (four roundings), the
+    sum with what the turn's rounding left by one, and that part, below 2^-23, by a few roundings of its own; the
+    angle's two roundings in 64 bits are below 2^-50."""
+    g = torch.Generator(device=DEV).manual_seed(14)
+    off = 10.0 ** (-7.5 + 5.5 * torch.rand(512, generator=g, device=DEV, dtype=torch.float64))
+    quarter = 0.25 * (1 + torch.arange(512, device=DEV) % 3)
+    f = 2 * math.pi * (quarter + off * (1 - 2 * (torch.arange(512, device=DEV) // 3 % 2)))
+    x = torch.zeros(2, 1, 1024, device=DEV)
+    x[:, :, :512] = 1.0                                    # pairs (1, 0) become (cos, sin)
+    out = torch.empty_like(x)
+    positions = torch.tensor([1, -1], dtype=torch.int32, device=DEV)
+    bfo.rotary_apply(x, f, out, positions=positions, backward=backward)
+    angle = positions.double()[:, None] * f * (-1 if backward else 1)
+    ref = torch.cat([torch.cos(angle), torch.sin(angle)], 1)[:, None]
+    assert ((out.double() - ref).abs() <= 6 * 2.0 ** -24 * ref.abs() + 1e-13).all()
