@@ -1191,5 +1191,5 @@ def rotary_apply(x, frequencies, out, positions=None, period=0, layout=ROTARY_HA
     _check("rotary_apply", _entry("rotary_apply", dev)(
         xp, xt, xh, op, ot, oh, tokens, _sized(heads, _U32), _sized(dim, _U32), _sized(2 * pairs, _U32), layout,
         _vector(frequencies, torch.float64, pairs, "frequencies", dev),
-        _vector(positions, torch.int32, tokens, "positions", dev), period, amplitude, int(backward),
+        _vector(positions, torch.int32, tokens, "positions", dev), _sized(period, _U64), amplitude, int(backward),
         _DTYPE_CODES[dtype], _current_raw_stream(dev)))

@@ -170,3 +170,13 @@ def test_small_sines_and_cosines_keep_their_digits(bfo, backward):
     angle = positions.double()[:, None] * f * (-1 if backward else 1)
     ref = torch.cat([torch.cos(angle), torch.sin(angle)], 1)[:, None]
     assert ((out.double() - ref).abs() <= 6 * 2.0 ** -24 * ref.abs() + 1e-13).all()
+
+
+def test_periods_past_64_bits_are_not_their_low_words(bfo):
+    x, _ = inputs(15, 100, 2, 16, torch.float32)
+    f = bfo.rotary_frequencies(16, device=DEV)
+    want, out = torch.empty_like(x), torch.empty_like(x)
+    bfo.rotary_apply(x, f, want)
+    for period in (101, (1 << 64) - 1, 1 << 64, (1 << 64) + 5):
+        bfo.rotary_apply(x, f, out, period=period)
+        assert torch.equal(out, want), period
