@@ -317,3 +317,66 @@ def test_negative_gates_keep_their_digits(bfo, kind):
     check(out, act * H, (act * H).abs() * (rel + 2 * U), "out again")
     bfo.activation_backward(d, gate, None, dg, None, kind=kind)
     check(dg, D * slope, D.abs() * (off + U * slope.abs()), "dgate without up")
+
+
+@pytest.mark.parametrize("cols", [8, 9])
+def test_more_groups_than_workgroups_of_whole_and_ragged_rows(bfo, cols):
+    """Above 2^26 groups the workgroups take several turns: rows of one group, of whole chunks and not, forward,
+    backward from the codes and from the inputs, and the codes' values."""
+    rows, t, g = (1 << 26) + 40, torch.bfloat16, generator(4)
+    x = torch.zeros(rows, cols, dtype=t, device=DEV)
+    x[-64:] = matrix(g, 64, cols, t)
+    d = torch.zeros(rows, cols, dtype=t, device=DEV)
+    d[-64:] = matrix(g, 64, cols, t, size=0.01)
+    codes, scales = bfo.new_codes(rows, cols, DEV)
+    out = torch.full_like(x, 3.0)
+    bfo.activation_forward(x, None, out, gate_codes=codes, gate_scales=scales)
+    check_activation_forward(0, x[-64:], None, out[-64:])
+    check_codes(codes[-64:], scales[-64:], x[-64:].double(), 0, "gate")
+    assert not out[:-64].any() and not codes[:-64].any() and (scales[:-64] == SMALLEST).all()
+    kept = values(codes[-64:], scales[-64:])
+    for coded in (True, False):
+        out.fill_(3.0)
+        bfo.activation_backward(d, None if coded else x, None, out, None, gate_codes=codes if coded else None,
+                                gate_scales=scales if coded else None)
+        check_activation_backward(0, d[-64:], kept if coded else x[-64:].double(), None, out[-64:], None, off=int(coded))
+        assert not out[:-64].any()
+    out.fill_(3.0)
+    bfo.activation_unpack(codes, scales, out)
+    check_rounded(out[-64:], kept, U * kept.abs(), "unpack")
+    assert not out[:-64].any()
+    del x, d, codes, scales, out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("keep", ["i8", "e4m3"])
+def test_large_calls_of_every_kind(bfo, dt, kind, gated, keep):
+    """128 MB and more forward and backward, whole chunks (nontemporal) and not; packed and unpacked too."""
+    for cols in (4096, 4099):
+        rows = 8200 if dt == "bf16" else 4200
+        g, t = generator(cols), TYPES[dt]
+        gate, d = matrix(g, rows, cols, t, size=2.0), matrix(g, rows, cols, t, size=0.01)
+        up = matrix(g, rows, cols, t) if gated else None
+        out, kept = torch.empty_like(gate), {}
+        kept["gate_codes"], kept["gate_scales"] = codes_for(bfo, rows, cols, keep)
+        if gated:
+            kept["up_codes"], kept["up_scales"] = codes_for(bfo, rows, cols, keep)
+        bfo.activation_forward(gate, up, out, kind=kind, **kept)
+        check_activation_forward(kind, gate, up, out)
+        check_codes(kept["gate_codes"], kept["gate_scales"], gate.double(), 0, "gate")
+        G, H = values(kept["gate_codes"], kept["gate_scales"]), None
+        if gated:
+            check_codes(kept["up_codes"], kept["up_scales"], up.double(), 0, "up")
+            H = values(kept["up_codes"], kept["up_scales"])
+        dgate, dup, again = torch.empty_like(gate), torch.empty_like(gate) if gated else None, torch.empty_like(gate)
+        bfo.activation_backward(d, None, None, dgate, dup, kind=kind, out=again, **kept)
+        check_activation_backward(kind, d, G, H, dgate, dup, again, 1)
+        codes, scales = codes_for(bfo, rows, cols, keep)
+        bfo.activation_pack(gate, codes, scales)
+        assert torch.equal(codes.view(torch.int8), kept["gate_codes"].view(torch.int8))
+        assert torch.equal(scales, kept["gate_scales"])
+        bfo.activation_unpack(codes, scales, again)
+        check_rounded(again, G, U * G.abs(), "unpack")

@@ -276,3 +276,23 @@ def test_large_calls(bfo, dt):
         check_rms_backward(d, values(codes, scales), w, rstd, *run_backward(bfo, d, None, w, rstd, codes=codes,
                                                                             scales=scales))
         check_rms_backward(d, total.double() * rstd.double()[:, None], w, rstd, *run_backward(bfo, d, total, w, rstd))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("per_row", [False, True])
+@pytest.mark.parametrize("of_out", [False, True])
+def test_large_calls_of_every_code(bfo, dt, kind, per_row, of_out):
+    """128 MB and more: codes of either type and group, of the output or of the normalised row, and its gradient."""
+    rows, cols, t = (6000 if dt == "bf16" else 3000), 4096, TYPES[dt]
+    g = generator(71)
+    x, r, d = (matrix(g, rows, cols, t) for _ in range(3))
+    w = weights(g, cols, t)
+    out, total, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device=DEV)
+    codes, scales = codes_for(bfo, rows, cols, kind, per_row)
+    bfo.rmsnorm_forward(x, w, out, residual=r, total=total, rstd=rstd, codes=codes, scales=scales,
+                        codes_of=bfo.CODES_OF_OUT if of_out else bfo.CODES_OF_NORMALISED)
+    check_rms_forward(x, r, w, 1e-5, total, out, rstd, codes, scales, of_out=of_out)
+    if not of_out:
+        check_rms_backward(d, values(codes, scales), w, rstd, *run_backward(bfo, d, None, w, rstd, codes=codes,
+                                                                            scales=scales))
