@@ -249,16 +249,18 @@ int bfo_rotary_frequencies(const bfo_rotary_scaling *scaling, uint32_t rotated, 
         return BFO_EINVAL;
     if (s.kind == BFO_ROTARY_BASE && rotated < 4) return BFO_EINVAL;
     const double kTwoPi = 6.283185307179586476925, r = rotated;
-    const double base = s.kind == BFO_ROTARY_BASE ? s.base * std::pow(s.factor, r / (r - 2.0)) : s.base;
     // The (real) pair that makes `turns` turns over the original length.
-    auto pairOf = [&](double turns) { return r * std::log(s.length / (turns * kTwoPi)) / (2.0 * std::log(s.base)); };
+    auto pairOf = [&](double turns) {
+        return r * (std::log(s.length) - std::log(turns) - std::log(kTwoPi)) / (2.0 * std::log(s.base));
+    };
     for (uint32_t i = 0; i < rotated / 2; ++i) {
-        const double f = std::pow(base, -2.0 * i / r);
+        double f = std::pow(s.base, -2.0 * i / r);
+        if (s.kind == BFO_ROTARY_BASE) f *= std::pow(s.factor, -2.0 * i / (r - 2.0));
         double keep = 1.0;  // how much of the frequency stays; the rest is divided by the factor
         if (s.kind == BFO_ROTARY_LINEAR) keep = 0.0;
         if (s.kind == BFO_ROTARY_BY_TURNS) keep = (s.length * f / kTwoPi - s.low) / (s.high - s.low);
         if (s.kind == BFO_ROTARY_BY_PAIR) keep = (pairOf(s.low) - i) / (pairOf(s.low) - pairOf(s.high));
-        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        keep = !(keep > 0.0) ? 0.0 : keep > 1.0 ? 1.0 : keep;  // no number: a pair at bounds that are one
         frequencies[i] = f * keep + (keep < 1.0 ? f / s.factor * (1.0 - keep) : 0.0);
     }
     return BFO_OK;

@@ -316,3 +316,24 @@ def test_activation_gradients_do_not_go_over_the_codes(bfo):
             # without a gate too
             one = dict(g=None, u=None, du=None, gq=ptr(6), gqs=256 * size, gsc=ptr(7), dt=dt, dg=ptr(6))
             assert act_backward(bfo, **one) == bfo.EINVAL and act_backward(bfo, **{**one, "dg": ptr(3)}, out=ptr(6)) == bfo.EINVAL
+
+
+def test_rotary_frequencies_of_far_parameters(bfo):
+    """Whatever the documentation allows has finite frequencies: turns and factors whose quotients or powers pass
+    binary64, and bounds whose logarithms are the same number."""
+    f, pair = bfo.rotary_frequencies, torch.arange(32, dtype=torch.float64)
+    plain = 10000.0 ** (-2 * pair / 64)
+    # from low = 1e-310 on the pairs' bounds are real numbers as always
+    bound = lambda turns: 64 * (math.log(2048.0) - math.log(turns) - math.log(2 * math.pi)) / (2 * math.log(10000.0))  # noqa: E731
+    got = f(64, scaling=bfo.ROTARY_BY_PAIR, factor=8.0, length=2048.0, low=1e-310, high=32.0)
+    keep = ((bound(1e-310) - pair) / (bound(1e-310) - bound(32.0))).clamp(0, 1)
+    assert torch.allclose(got, plain * keep + plain / 8 * (1 - keep), rtol=1e-12, atol=0)
+    # a factor whose power is past binary64: the first pair as it is, the last divided by it
+    got = f(4, scaling=bfo.ROTARY_BASE, factor=1e300)
+    assert got[0] == 1 and math.isclose(got[1], 0.01 / 1e300, rel_tol=1e-12)
+    # bounds next to one another, at the turns of a pair itself: that pair is between them, the others are not
+    for low, at in ((32.0, -1), (2048.0 / (2 * math.pi), 0), (2048.0 / (2 * math.pi) * 10000.0 ** -0.5, 16)):
+        got = f(64, scaling=bfo.ROTARY_BY_PAIR, factor=8.0, length=2048.0, low=low, high=math.nextafter(low, math.inf))
+        above, below = (got - plain).abs() <= 1e-12 * plain, (got - plain / 8).abs() <= 1e-12 * plain
+        assert (above | below | (pair == at)).all()
+        assert (got <= plain * (1 + 1e-12)).all() and (got >= plain / 8 * (1 - 1e-12)).all()
