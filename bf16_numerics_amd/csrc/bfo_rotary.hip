@@ -93,7 +93,9 @@ __host__ __device__ uint32_t halfColumns(uint32_t rotated) {
 }
 __host__ __device__ inline uint32_t halfBehind(uint32_t behind) { return (behind + 1) / 2; }
 
-// Sines and cosines of a workgroup at most: 16 KB of LDS, as four workgroups fill a CU.
+// Pairs of a workgroup's tokens at most.  A token's sines take room for a multiple of
+// eight pairs: 16 KB of LDS in all where there are as many, and up to 32 KB (512 tokens
+// of one to four pairs), of which a CU holds five and its lanes four.
 constexpr uint32_t kTurns = 2048;
 
 // kBehind: columns behind the rotated ones are copied.

@@ -727,7 +727,8 @@ int activation_forward(const void *gate, uint64_t gate_stride, const void *up, u
  *   dgate = dout * up * act'(gate);  dup = dout * act(gate)
  * (without up: dgate = dout * act'(gate), and dup is NULL).  out, unless NULL,
  * gets act(gate) * up again, for the next product's weight gradient.  Each
- * output may be one of dout, gate and up (same pointer and stride). */
+ * output may be one of dout, gate and up (same pointer and stride), none the
+ * codes. */
 int activation_backward(const void *dout, uint64_t dout_stride, const void *gate, uint64_t gate_stride,
                         const void *up, uint64_t up_stride, const void *gate_codes, uint64_t gate_codes_stride,
                         const float *gate_scales, const void *up_codes, uint64_t up_codes_stride,
@@ -754,7 +755,9 @@ int activation_unpack(const void *codes, uint64_t codes_stride, const float *sca
  *   BFO_ROTARY_BY_TURNS  divided by factor below `low` turns in length positions,
  *                        as it is above `high`, and between them mixed in proportion
  *                        to the number of turns
- *   BFO_ROTARY_BY_PAIR   the same, mixed in proportion to the pair's index
+ *   BFO_ROTARY_BY_PAIR   the same, mixed in proportion to the pair's index, between
+ *                        the (real) indexes that make these turns; a model whose
+ *                        bounds were rounded to whole pairs brings its own frequencies
  * (0 < low < high; length and these two are used by the last two kinds only).
  * frequencies: rotated / 2 doubles of host memory, which a caller copies to the
  * device once.  rotated: even, 2 ... BFO_ROTARY_MAX_DIM.  BFO_EINVAL for
